@@ -66,7 +66,8 @@ const char* mmf_version(void);
 const char* mmf_last_error(void);
 
 /* Synchronise `stream`, then return MMF_ERR_CUDA for a pending CUDA error,
- * MMF_ERR_INVALID_ARG if mmf_embed met a token id outside [0, V), or
+ * MMF_ERR_INVALID_ARG if mmf_embed met a token id, or mmf_head_loss a label,
+ * outside [0, V), or
  * MMF_ERR_TIMEOUT if a kernel recorded a bounded-wait timeout since the last
  * check (the status word is cleared), else MMF_OK. */
 mmf_status mmf_check(void* stream);
@@ -288,6 +289,152 @@ size_t mmf_glu_ws_size(int32_t M, int32_t d, int32_t I);
 mmf_status mmf_glu(const mmf_tlinear* gate, const mmf_tlinear* up, const mmf_tlinear* down,
                    const void* x, const void* residual, void* y, int32_t M, mmf_dtype dtype,
                    float eps, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Training: BitLinear and GLU with activations kept in 8 bits                */
+/* ------------------------------------------------------------------------- */
+
+/* What a layer's forward keeps of its input x [M, K] for the backward: the
+ * int8 codes that the forward contraction reads anyway, 1 byte per element and
+ * 16 per row (a bf16 copy of x would be 2 bytes per element, of x^ 2 more).
+ * All device memory owned by the caller, 16-byte aligned.
+ *   q     int8 [M, K]: the activation codes
+ *   scale float [M]: s, so that x^ is kept as xt = q / s
+ *   qsum  int32 [M]: sum of the row's codes
+ *   rinv  float [M]: 1 / sqrt(mean(x^2) + eps) */
+typedef struct mmf_act8 {
+  int8_t* q;
+  float* scale;
+  int32_t* qsum;
+  float* rinv;
+} mmf_act8;
+
+/* Outputs of a backward, each in the activation dtype, each may be NULL (not
+ * computed). dw[i] / dbias[i] belong to layer i. 16-byte aligned, overwritten. */
+typedef struct mmf_linear_grads {
+  void* dx;        /* [M, K] */
+  void* dw[3];     /* [N, K]: gradient of the latent weights */
+  void* dgain;     /* [K] */
+  void* dbias[3];  /* [N] */
+} mmf_linear_grads;
+
+/* Scratch bytes of mmf_bitlinear_train for nlin layers N x K. */
+size_t mmf_bitlinear_train_ws_size(int32_t nlin, int32_t N, int32_t K);
+
+/* Training forward: nlin (1..3) BitLinear layers of one shape and one gain on
+ * the same input, as mmf_bitlinear computes them, keeping the input's codes.
+ *   lins (host) array of nlin layers; x (device) [M, K] in dtype
+ *   y    (device) [M, nlin, N] in dtype (for f, c, g: the scan's `pre`)
+ *   kept (host struct) receives the codes, scales, sums and 1 / rms of x
+ * M = 0 does nothing. Errors: INVALID_ARG, UNSUPPORTED_SHAPE (shapes or gains
+ * differ), MISALIGNED, WORKSPACE, CUDA. */
+mmf_status mmf_bitlinear_train(const mmf_tlinear* lins, int32_t nlin, const void* x, mmf_dtype dtype, int32_t M,
+                               void* y, float eps, const mmf_act8* kept, void* ws, size_t ws_bytes, void* stream);
+
+/* Scratch bytes of mmf_bitlinear_backward. */
+size_t mmf_bitlinear_backward_ws_size(int32_t nlin, int32_t N, int32_t K, int32_t M, mmf_dtype dtype);
+
+/* Gradients of mmf_bitlinear_train for dy = dL/dy [M, nlin, N] in dtype. The
+ * pages say that the models are trained with fused kernels ([DC] "Memory
+ * efficiency") and print no formula: this is the derivative of the forward
+ * with both roundings (activation codes, ternary weights) passed straight
+ * through, the weight scale gamma held constant, and xt = q / s read from the
+ * codes. With n the norm's output before the gain:
+ *   dx^   = sum_i gamma_i dy_i W_i          (W ternary)
+ *   dW_i  = dy_i^T xt                       dbias_i = sum_t dy_i[t]
+ *   n     = x rinv when x is given, else xt / gain (0 where gain is 0)
+ *   dx    = rinv (gain dx^ - n mean_k(dx^ n gain)) + dres,  dgain = sum_t dx^ n
+ * Without x a column's n is known to half a code step over its gain, and a
+ * column whose gain is exactly 0 left nothing in its codes: give x for layers
+ * whose gains come near 0. Sums run in fp32, in an order that depends on the
+ * sizes alone; fp32 gradients are multiplied as three bf16 parts (24 bits);
+ * for bf16 dW reads xt rounded to bf16.
+ *   x    (device) [M, K] in dtype, or NULL; dres (device) [M, K] in dtype, or
+ *        NULL: added to dx (a residual's gradient); it may be grads->dx itself.
+ * M = 0 writes zeros to dw, dgain and dbias. Errors: as mmf_bitlinear_train. */
+mmf_status mmf_bitlinear_backward(const mmf_tlinear* lins, int32_t nlin, const mmf_act8* kept, const void* x,
+                                  const void* dy, const void* dres, mmf_dtype dtype, int32_t M,
+                                  const mmf_linear_grads* grads, void* ws, size_t ws_bytes, void* stream);
+
+/* Scratch bytes of mmf_glu_train. */
+size_t mmf_glu_train_ws_size(int32_t M, int32_t d, int32_t I, mmf_dtype dtype);
+
+/* Training forward of the channel mixer: mmf_glu, keeping the codes of x [M, d]
+ * (kept_x) and of p [M, I] (kept_p); u = gate(x), v = up(x) and p are not kept.
+ * Errors: as mmf_glu. */
+mmf_status mmf_glu_train(const mmf_tlinear* gate, const mmf_tlinear* up, const mmf_tlinear* down, const void* x,
+                         const void* residual, void* y, int32_t M, mmf_dtype dtype, float eps, const mmf_act8* kept_x,
+                         const mmf_act8* kept_p, void* ws, size_t ws_bytes, void* stream);
+
+/* Outputs of mmf_glu_backward, as mmf_linear_grads. */
+typedef struct mmf_glu_grads {
+  void* dx;                                 /* [M, d] */
+  void *dw_gate, *dw_up, *dw_down;          /* [I, d], [I, d], [d, I] */
+  void *dgain, *dgain_down;                 /* [d], [I] */
+  void *dbias_gate, *dbias_up, *dbias_down; /* [I], [I], [d] */
+} mmf_glu_grads;
+
+/* Scratch bytes of mmf_glu_backward. */
+size_t mmf_glu_backward_ws_size(int32_t M, int32_t d, int32_t I, mmf_dtype dtype);
+
+/* Gradients of mmf_glu_train for dy = dL/dy [M, d]: the down projection's
+ * backward through kept_p, then with u and v computed again from kept_x (exact
+ * integer products), sg = sigmoid(u), dp = dL/dp:
+ *   du = dp v sg (1 + u (1 - sg)),  dv = dp u sg
+ * and the backward of gate and up. For bf16 runs du / s and dv / s are rounded
+ * to bf16 once, for both of their products. p's norm is read through its codes
+ * (see mmf_bitlinear_backward on gains near 0); x, dres as there. The residual's
+ * own gradient is dy. M = 0 writes zeros to all but dx. Errors: as mmf_glu. */
+mmf_status mmf_glu_backward(const mmf_tlinear* gate, const mmf_tlinear* up, const mmf_tlinear* down,
+                            const mmf_act8* kept_x, const mmf_act8* kept_p, const void* x, const void* dy,
+                            const void* dres, mmf_dtype dtype, int32_t M, const mmf_glu_grads* grads, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Training: softmax cross entropy through the LM head                        */
+/* ------------------------------------------------------------------------- */
+
+typedef enum mmf_reduction { MMF_REDUCE_NONE = 0, MMF_REDUCE_SUM = 1, MMF_REDUCE_MEAN = 2 } mmf_reduction;
+
+/* Scratch bytes of mmf_head_loss for M tokens and a head of N = V rows. */
+size_t mmf_head_loss_ws_size(int32_t M, int32_t V, int32_t K);
+
+/* Cross entropy of the logits z = BitLinear_head(x) [M, V] against labels,
+ * without storing them: each tile of 128 tokens x 128 vocabulary entries is
+ * reduced to its maximum and sum of exponentials where it is computed (the
+ * logits stay in fp32, they are not rounded to dtype).
+ *   loss_t = log sum_v exp(z[t, v]) - z[t, labels[t]]
+ * Tokens with labels[t] == ignore_index contribute 0 and are not counted. Any
+ * other label outside [0, V) does the same and is reported by mmf_check.
+ *   labels (device) int32 [M]
+ *   loss   (device) float [M] for MMF_REDUCE_NONE, else one value: the sum, or
+ *          the mean over the counted tokens (0 when there are none)
+ *   kept   (host struct) the codes of x; lse (device) float [M]; count (device)
+ *          one float: the counted tokens, at least 1 (not written for
+ *          MMF_REDUCE_NONE) - all for mmf_head_loss_backward
+ * M = 0 writes a zero loss for SUM and MEAN. Errors: as mmf_bitlinear_train. */
+mmf_status mmf_head_loss(const mmf_tlinear* head, const void* x, mmf_dtype dtype, int32_t M, const int32_t* labels,
+                         int32_t ignore_index, mmf_reduction reduction, float eps, float* loss, const mmf_act8* kept,
+                         float* lse, float* count, void* ws, size_t ws_bytes, void* stream);
+
+/* Scratch bytes of mmf_head_loss_backward: the gradient of the logits exists
+ * for one piece of the vocabulary at a time (at most 256 MiB of it). */
+size_t mmf_head_loss_backward_ws_size(int32_t M, int32_t V, int32_t K, mmf_dtype dtype);
+
+/* Gradients of mmf_head_loss. The logits are computed again from the codes,
+ * piece by piece of the vocabulary, and become
+ *   dz[t, v] = w_t (exp(z[t, v] - lse_t) - [v == labels[t]])
+ * with w_t = dloss (NONE: dloss[t]; MEAN: dloss / count; ignored tokens: 0),
+ * then the head's BitLinear backward (straight through, as
+ * mmf_bitlinear_backward; for bf16 runs dz / s is rounded to bf16 once).
+ *   dloss (device) float, one value or [M] for NONE; NULL: 1
+ *   grads->dw[0], dbias[0] are the head's. labels, ignore_index, reduction and
+ *   count as in the forward; x as in mmf_bitlinear_backward.
+ * M = 0 writes zeros to all but dx. Errors: as mmf_bitlinear_train. */
+mmf_status mmf_head_loss_backward(const mmf_tlinear* head, const mmf_act8* kept, const void* x,
+                                  const int32_t* labels, const float* lse, const float* count, const float* dloss,
+                                  int32_t ignore_index, mmf_reduction reduction, mmf_dtype dtype, int32_t M,
+                                  const mmf_linear_grads* grads, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------- */
 /* Blocks and recurrent state                                                 */

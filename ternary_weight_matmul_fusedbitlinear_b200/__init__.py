@@ -10,4 +10,8 @@ from .api import (  # noqa: F401
     mlgru_scan_gnorm, mlgru_scan_states, mlgru_scan_backward, quantize_weights, unpack_codes, embed, argmax, Model,
     stack_forward, stack_ws_size, version, prof_enable, prof_reset, prof_collect,
 )
+from .train import (  # noqa: F401
+    Act8, GluGrads, HeadKept, LinearGrads, bitlinear_backward, bitlinear_train, glu_backward, glu_train, head_loss,
+    head_loss_backward,
+)
 from ._lib import LIB_PATH, MMFError, load  # noqa: F401

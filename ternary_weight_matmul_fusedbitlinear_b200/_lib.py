@@ -38,6 +38,19 @@ class BlockWeights(ctypes.Structure):
     _fields_ = [(n, TLinear) for n in ("f", "c", "g", "o", "gate", "up", "down")] + [("gnorm", ctypes.c_void_p)]
 
 
+class Act8(ctypes.Structure):
+    _fields_ = [("q", c_vp), ("scale", c_vp), ("qsum", c_vp), ("rinv", c_vp)]
+
+
+class LinearGrads(ctypes.Structure):
+    _fields_ = [("dx", c_vp), ("dw", c_vp * 3), ("dgain", c_vp), ("dbias", c_vp * 3)]
+
+
+class GluGrads(ctypes.Structure):
+    _fields_ = [(n, c_vp) for n in ("dx", "dw_gate", "dw_up", "dw_down", "dgain", "dgain_down", "dbias_gate",
+                                    "dbias_up", "dbias_down")]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "mmf_version": (ctypes.c_char_p, []),
@@ -63,6 +76,21 @@ SIGNATURES = {
     "mmf_glu_ws_size": (c_sz, [c_i32, c_i32, c_i32]),
     "mmf_glu": (ctypes.c_int, [ctypes.POINTER(TLinear)] * 3 + [c_vp, c_vp, c_vp, c_i32, ctypes.c_int, c_f, c_vp,
                                                              c_sz, c_vp]),
+    "mmf_bitlinear_train_ws_size": (c_sz, [c_i32, c_i32, c_i32]),
+    "mmf_bitlinear_train": (ctypes.c_int, [c_vp, c_i32, c_vp, ctypes.c_int, c_i32, c_vp, c_f, c_vp, c_vp, c_sz, c_vp]),
+    "mmf_bitlinear_backward_ws_size": (c_sz, [c_i32, c_i32, c_i32, c_i32, ctypes.c_int]),
+    "mmf_bitlinear_backward": (ctypes.c_int, [c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, ctypes.c_int, c_i32, c_vp, c_vp,
+                                              c_sz, c_vp]),
+    "mmf_glu_train_ws_size": (c_sz, [c_i32, c_i32, c_i32, ctypes.c_int]),
+    "mmf_glu_train": (ctypes.c_int, [c_vp] * 6 + [c_i32, ctypes.c_int, c_f, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "mmf_glu_backward_ws_size": (c_sz, [c_i32, c_i32, c_i32, ctypes.c_int]),
+    "mmf_glu_backward": (ctypes.c_int, [c_vp] * 8 + [ctypes.c_int, c_i32, c_vp, c_vp, c_sz, c_vp]),
+    "mmf_head_loss_ws_size": (c_sz, [c_i32, c_i32, c_i32]),
+    "mmf_head_loss": (ctypes.c_int, [c_vp, c_vp, ctypes.c_int, c_i32, c_vp, c_i32, ctypes.c_int, c_f, c_vp, c_vp, c_vp,
+                                     c_vp, c_vp, c_sz, c_vp]),
+    "mmf_head_loss_backward_ws_size": (c_sz, [c_i32, c_i32, c_i32, ctypes.c_int]),
+    "mmf_head_loss_backward": (ctypes.c_int, [c_vp] * 7 + [c_i32, ctypes.c_int, ctypes.c_int, c_i32, c_vp, c_vp, c_sz,
+                                              c_vp]),
     "mmf_block_create": (ctypes.c_int, [ctypes.POINTER(BlockWeights), c_i32, c_i32, ctypes.POINTER(c_vp)]),
     "mmf_block_destroy": (None, [c_vp]),
     "mmf_block_release_codes": (ctypes.c_int, [c_vp]),

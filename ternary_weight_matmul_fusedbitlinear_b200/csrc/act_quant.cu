@@ -27,7 +27,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) rmsnorm_quant_kernel(const T* __restrict__ x, int K,
                                                                  const float* __restrict__ gain, float eps,
                                                                  int8_t* __restrict__ q, float* __restrict__ scale,
-                                                                 int32_t* __restrict__ qsum) {
+                                                                 int32_t* __restrict__ qsum, float* __restrict__ rinv_out) {
   extern __shared__ float xs[];  // K floats
   __shared__ double red_d[kWarps];
   __shared__ float red_f[kWarps];
@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_quant_kernel(const T* __rest
     for (int w = 0; w < kWarps; ++w) t += red_i[w];
     scale[row] = s;
     qsum[row] = t;
+    if (rinv_out != nullptr) rinv_out[row] = rinv;
   }
 }
 
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(256) rmsnorm_quant_staged_kernel(const T* __re
                                                                    int8_t* __restrict__ q, float* __restrict__ scale,
                                                                    int32_t* __restrict__ qsum, int slots,
                                                                    int stride, int* status, uint4* fill,
-                                                                   size_t fill16) {
+                                                                   size_t fill16, float* __restrict__ rinv_out) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   const int warps = blockDim.x >> 5;
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(256) rmsnorm_quant_staged_kernel(const T* __re
     if (lane == 0) {
       scale[row] = rc.scale;
       qsum[row] = rc.qsum;
+      if (rinv_out != nullptr) rinv_out[row] = rc.rinv;
     }
 
     // refill this buffer with the row `slots` rows ahead
@@ -220,7 +222,8 @@ bool staged_geometry(int K, int esize, StagedGeom& g) {
 
 template <typename T, bool GAIN>
 cudaError_t launch_staged(const StagedGeom& g, const void* x, int M, int K, const float* gain, float eps, int8_t* q,
-                          float* scale, int32_t* qsum, int* status, void* fill, size_t fill_bytes, cudaStream_t stream) {
+                          float* scale, int32_t* qsum, int* status, void* fill, size_t fill_bytes, float* rinv,
+                          cudaStream_t stream) {
   auto kern = rmsnorm_quant_staged_kernel<T, GAIN>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)g.smem);
   if (e != cudaSuccess) return e;
@@ -228,22 +231,22 @@ cudaError_t launch_staged(const StagedGeom& g, const void* x, int M, int K, cons
   cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, g.warps * 32, g.smem);
   const int grid = std::max(1, std::min(ceil_div(M, g.warps), num_sms() * std::max(per_sm, 1)));
   return launch_pdl(kern, dim3(grid), dim3(g.warps * 32), g.smem, stream, static_cast<const T*>(x), M, K, gain, eps,
-                    q, scale, qsum, g.slots, g.stride, status, static_cast<uint4*>(fill), fill_bytes / 16);
+                    q, scale, qsum, g.slots, g.stride, status, static_cast<uint4*>(fill), fill_bytes / 16, rinv);
 }
 
 }  // namespace
 
 cudaError_t launch_rmsnorm_quant(const void* x, mmf_dtype dt, int M, int K, const float* gain, float eps,
                                  int8_t* q, float* scale, int32_t* qsum, int* status, cudaStream_t stream, void* fill,
-                                 size_t fill_bytes) {
+                                 size_t fill_bytes, float* rinv) {
   if (M == 0) return fill_bytes ? cudaMemsetAsync(fill, 0xff, fill_bytes, stream) : cudaSuccess;
   StagedGeom g;
   if (staged_geometry(K, dt == MMF_BF16 ? 2 : 4, g) && fill_bytes % 16 == 0) {
     if (dt == MMF_BF16)
-      return gain ? launch_staged<bf16, true>(g, x, M, K, gain, eps, q, scale, qsum, status, fill, fill_bytes, stream)
-                  : launch_staged<bf16, false>(g, x, M, K, gain, eps, q, scale, qsum, status, fill, fill_bytes, stream);
-    return gain ? launch_staged<float, true>(g, x, M, K, gain, eps, q, scale, qsum, status, fill, fill_bytes, stream)
-                : launch_staged<float, false>(g, x, M, K, gain, eps, q, scale, qsum, status, fill, fill_bytes, stream);
+      return gain ? launch_staged<bf16, true>(g, x, M, K, gain, eps, q, scale, qsum, status, fill, fill_bytes, rinv, stream)
+                  : launch_staged<bf16, false>(g, x, M, K, gain, eps, q, scale, qsum, status, fill, fill_bytes, rinv, stream);
+    return gain ? launch_staged<float, true>(g, x, M, K, gain, eps, q, scale, qsum, status, fill, fill_bytes, rinv, stream)
+                : launch_staged<float, false>(g, x, M, K, gain, eps, q, scale, qsum, status, fill, fill_bytes, rinv, stream);
   }
   if (fill_bytes) {
     const cudaError_t e = cudaMemsetAsync(fill, 0xff, fill_bytes, stream);
@@ -255,12 +258,12 @@ cudaError_t launch_rmsnorm_quant(const void* x, mmf_dtype dt, int M, int K, cons
     auto kern = rmsnorm_quant_kernel<bf16>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<M, kThreads, smem, stream>>>(static_cast<const bf16*>(x), K, gain, eps, q, scale, qsum);
+    kern<<<M, kThreads, smem, stream>>>(static_cast<const bf16*>(x), K, gain, eps, q, scale, qsum, rinv);
   } else {
     auto kern = rmsnorm_quant_kernel<float>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<M, kThreads, smem, stream>>>(static_cast<const float*>(x), K, gain, eps, q, scale, qsum);
+    kern<<<M, kThreads, smem, stream>>>(static_cast<const float*>(x), K, gain, eps, q, scale, qsum, rinv);
   }
   return cudaGetLastError();
 }

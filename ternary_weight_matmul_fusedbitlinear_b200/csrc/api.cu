@@ -8,7 +8,7 @@
 #include <string>
 #include <vector>
 
-#include "kernels.cuh"
+#include "api_common.cuh"
 
 using namespace mmf;
 
@@ -18,7 +18,9 @@ namespace {
 
 thread_local std::string g_last_error;
 
-mmf_status fail(mmf_status st, const char* fmt, ...) {
+}  // namespace
+
+mmf_status mmf::fail(mmf_status st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -28,40 +30,20 @@ mmf_status fail(mmf_status st, const char* fmt, ...) {
   return st;
 }
 
-mmf_status cuda_fail(cudaError_t e, const char* where) {
+mmf_status mmf::cuda_fail(cudaError_t e, const char* where) {
   return fail(MMF_ERR_CUDA, "%s: CUDA error %d (%s)", where, (int)e, cudaGetErrorString(e));
 }
 
-#define MMF_CUDA(call, where)                      \
-  do {                                             \
-    cudaError_t e_ = (call);                       \
-    if (e_ != cudaSuccess) return cuda_fail(e_, where); \
-  } while (0)
-
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-inline size_t elem_bytes(mmf_dtype dt) { return dt == MMF_BF16 ? 2 : 4; }
-inline bool dtype_ok(mmf_dtype dt) { return dt == MMF_F32 || dt == MMF_BF16; }
-inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
-
-// Bump allocator over the caller's workspace (256-byte granules).
-struct Carver {
-  char* base;
-  size_t off = 0;
-  explicit Carver(void* b) : base(static_cast<char*>(b)) {}
-  template <typename T> T* take(size_t count) {
-    T* p = reinterpret_cast<T*>(base ? base + off : nullptr);
-    off += round_up(sizeof(T) * count, 256);
-    return p;
-  }
-};
+namespace {
 
 // Per-device status word written by kernels that give up a bounded wait.
 constexpr int kMaxDevices = 64;
 int* g_dev_status[kMaxDevices] = {};
 std::mutex g_dev_status_mu;
 
-mmf_status device_status_ptr(int** out) {
+}  // namespace
+
+mmf_status mmf::device_status_ptr(int** out) {
   int dev = 0;
   MMF_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
   if (dev < 0 || dev >= kMaxDevices) return fail(MMF_ERR_INVALID_ARG, "device %d out of range", dev);
@@ -76,9 +58,9 @@ mmf_status device_status_ptr(int** out) {
   return MMF_OK;
 }
 
+namespace {
+
 // ------------------------------------------------------------------ launch timing
-// Every launch goes through timed(): when the profiler is on, two CUDA events
-// bracket it on its stream; mmf_prof_collect folds finished pairs into totals.
 struct ProfPair {
   int kind;
   cudaEvent_t a, b;
@@ -112,17 +94,23 @@ int prof_kind(const char* name) {
   return (int)g_prof_kinds.size() - 1;
 }
 
-template <class F>
-cudaError_t timed(const char* name, cudaStream_t s, F&& launch) {
-  if (!g_prof_on) return launch();
-  std::lock_guard<std::mutex> lk(g_prof_mu);
-  cudaEvent_t a = prof_event(), b = prof_event();
+}  // namespace
+
+bool mmf::prof_is_on() { return g_prof_on; }
+
+mmf::ProfSpan::ProfSpan(const char* n, cudaStream_t st) : name(n), s(st) {
+  g_prof_mu.lock();
+  a = prof_event();
+  b = prof_event();
   if (a) cudaEventRecord(a, s);
-  cudaError_t e = launch();
+}
+mmf::ProfSpan::~ProfSpan() {
   if (b) cudaEventRecord(b, s);
   if (a && b) g_prof_pending.push_back(ProfPair{prof_kind(name), a, b});
-  return e;
+  g_prof_mu.unlock();
 }
+
+namespace {
 
 // Contraction dispatch: the tcgen05 kernel from 128 tokens, the mma.sync
 // kernel for decode-sized token counts and for shapes the tcgen05 kernel does
@@ -174,8 +162,10 @@ bool decode_fused_quant_wanted(int M, int N) {
   return M <= 4 && ceil_div(N, 16) <= num_sms();
 }
 
+}  // namespace
+
 // `what` names the projection for the launch-timing totals ("fcg", "o", ...).
-cudaError_t run_gemm(const TGemmArgs& a, Epi epi, mmf_dtype dt, cudaStream_t s, const char* what = "") {
+cudaError_t mmf::run_gemm(const TGemmArgs& a, Epi epi, mmf_dtype dt, cudaStream_t s, const char* what) {
   const bool use_tc = gemm_uses_tc(a, epi);
   char name[48];
   snprintf(name, sizeof(name), "%s%s%s", use_tc ? "tgemm_tc" : "tgemm_mma", what[0] ? ":" : "", what);
@@ -187,18 +177,12 @@ cudaError_t run_gemm(const TGemmArgs& a, Epi epi, mmf_dtype dt, cudaStream_t s, 
   return timed(name, s, [&] { return launch_tgemm_mma(a, epi, dt, s); });
 }
 
-// Device status word for kernels with bounded waits, or null when it cannot be had.
-int* status_word() {
+int* mmf::status_word() {
   int* st = nullptr;
   return device_status_ptr(&st) == MMF_OK ? st : nullptr;
 }
 
-// Quantised activations of M tokens of length K.
-struct QAct {
-  int8_t* q;
-  float* s;
-  int32_t* qsum;
-};
+namespace {
 
 // RMSNorm + int8 quantisation of x (a.M tokens of length a.K, RMSNorm gain
 // `gain`), then the contraction `a` (whose q/s/qsum point at qa). Single-token
@@ -238,7 +222,9 @@ bool prefill_unpacked_enabled() {
   return e == nullptr || strcmp(e, "0") != 0;
 }
 
-mmf_status check_tlinear(const mmf_tlinear* l, const char* name) {
+}  // namespace
+
+mmf_status mmf::check_tlinear(const mmf_tlinear* l, const char* name) {
   if (l == nullptr) return fail(MMF_ERR_INVALID_ARG, "%s: null layer", name);
   if (l->packed == nullptr || l->gamma == nullptr) return fail(MMF_ERR_INVALID_ARG, "%s: null packed/gamma", name);
   if (l->N < 1 || l->K < 1) return fail(MMF_ERR_INVALID_ARG, "%s: N=%d K=%d must be >= 1", name, l->N, l->K);
@@ -249,7 +235,7 @@ mmf_status check_tlinear(const mmf_tlinear* l, const char* name) {
   return MMF_OK;
 }
 
-TGemmArgs gemm_args(const mmf_tlinear* const* segs, int nseg, const int8_t* q, const float* s,
+TGemmArgs mmf::gemm_args(const mmf_tlinear* const* segs, int nseg, const int8_t* q, const float* s,
                     const int32_t* qsum, int M, void* out, int ldo, const void* residual, float* h) {
   TGemmArgs a{};
   for (int i = 0; i < 3; ++i) {
@@ -273,16 +259,13 @@ TGemmArgs gemm_args(const mmf_tlinear* const* segs, int nseg, const int8_t* q, c
   return a;
 }
 
-
-QAct carve_qact(Carver& c, int M, int K) {
+QAct mmf::carve_qact(Carver& c, int M, int K) {
   QAct a;
   a.q = c.take<int8_t>((size_t)M * K);
   a.s = c.take<float>(M);
   a.qsum = c.take<int32_t>(M);
   return a;
 }
-
-}  // namespace
 
 void mmf::set_last_error(const char* msg) { g_last_error = msg; }
 
@@ -336,6 +319,8 @@ extern "C" mmf_status mmf_check(void* stream) {
     MMF_CUDA(cudaMemset(st, 0, sizeof(int)), "mmf_check: clear status");
     if (v == 8)
       return fail(MMF_ERR_INVALID_ARG, "a token id was outside [0, V); its embedding row was written as zeros");
+    if (v == 9)
+      return fail(MMF_ERR_INVALID_ARG, "a label was outside [0, V) and not ignore_index; its token was left out");
     return fail(MMF_ERR_TIMEOUT, "a device-side bounded wait gave up (code %d)", v);
   }
   return MMF_OK;
@@ -566,7 +551,9 @@ size_t glu_ws(int M, int d, int I, mmf_dtype dt) {
   return c.off + 256;
 }
 
-mmf_status check_glu(const mmf_tlinear* gate, const mmf_tlinear* up, const mmf_tlinear* down, int d) {
+}  // namespace
+
+mmf_status mmf::check_glu(const mmf_tlinear* gate, const mmf_tlinear* up, const mmf_tlinear* down, int d) {
   mmf_status st;
   if ((st = check_tlinear(gate, "gate")) != MMF_OK) return st;
   if ((st = check_tlinear(up, "up")) != MMF_OK) return st;
@@ -577,6 +564,8 @@ mmf_status check_glu(const mmf_tlinear* gate, const mmf_tlinear* up, const mmf_t
   if (gate->gain != up->gain) return fail(MMF_ERR_UNSUPPORTED_SHAPE, "glu: gate and up must share one gain");
   return MMF_OK;
 }
+
+namespace {
 
 // p = SiLU(gate(x)) * up(x); y = down(p) + residual. x is quantised with the
 // gate's RMSNorm gain (gate and up share it), p with the down projection's.

@@ -12,10 +12,11 @@ namespace mmf {
 
 constexpr int kQuantPartials = 592;   // CTAs of the absmean partial-sum pass (4 x 148 SMs)
 
-// TMA tensor maps (host): a 2-D row-major [rows, cols] array of esize-byte elements.
+// TMA tensor maps (host): a 2-D row-major [rows, cols] array of esize-byte elements,
+// its rows pitch_bytes apart (0: dense).
 bool tma_available();
 bool make_tma_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int esize, uint64_t cols,
-                 uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz);
+                 uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz, uint64_t pitch_bytes = 0);
 int num_sms();
 // Bound of the kernels' device-side waits, in SM cycles: about 1 s at 2 GHz, or
 // MMF_WAIT_LIMIT_US microseconds when set (tests make waits run out quickly).
@@ -51,12 +52,12 @@ cudaError_t launch_unpack_codes(const uint32_t* packed, int N, int K, uint8_t* o
 cudaError_t launch_quantize_weights(const float* W, int N, int K, uint32_t* packed, float* gamma, void* ws,
                                     cudaStream_t stream);
 
-// `status` (nullable) is the device status word for bounded-wait timeouts.
-// Optionally, as side work for a later kernel, it sets `fill_bytes` bytes at
+// `status` (nullable) is the device status word for bounded-wait timeouts;
+// `rinv` (nullable) gets each row's 1 / sqrt(mean x^2 + eps). Optionally, as side work for a later kernel, it sets `fill_bytes` bytes at
 // `fill` (16-byte aligned) to 0xff, stream-ordered like a memset.
 cudaError_t launch_rmsnorm_quant(const void* x, mmf_dtype dt, int M, int K, const float* gain, float eps,
                                  int8_t* q, float* scale, int32_t* qsum, int* status, cudaStream_t stream,
-                                 void* fill = nullptr, size_t fill_bytes = 0);
+                                 void* fill = nullptr, size_t fill_bytes = 0, float* rinv = nullptr);
 
 // Epilogues of the ternary contraction.
 enum class Epi : int {
@@ -64,7 +65,36 @@ enum class Epi : int {
   kAcc = 1,       // int32 acc[m, n]
   kScanStep = 2,  // 3 segments f,c,g: one MLGRU step, h[m, n] in place, o'[m, n]
   kGlu = 3,       // 2 segments gate,up: p[m, n] = SiLU(u) * v
+  // training (tcgen05 kernel only, one-byte codes; any N, K a multiple of 16)
+  kLse = 4,       // per token and 128 columns: max and sum of exp of the logits; the label's logit
+  kDz = 5,        // gradient of the loss by the logits, over the token's scale, as bf16 planes
+  kGluBwd = 6,    // 2 segments gate,up: gradients of u and v, over the token's scale, as bf16 planes
 };
+
+// What the training epilogues read and write besides TGemmArgs. "Planes": one
+// bf16 plane for bf16 runs, three (g0 + g1 + g2, 24 bits) for fp32 runs, each
+// plane_rows rows tall.
+struct TrainEpi {
+  const int32_t* labels;    // kLse, kDz: [M]
+  int col0, vocab;          // kLse, kDz: vocabulary index of column 0; vocabulary size
+  float2* part;             // kLse: [ceil(N / 128)][M] (max, sum) in log2 units
+  float* zlabel;            // kLse: [M] the label's logit in log2 units (written where the label lies in these columns)
+  const float* lse;         // kDz: [M]
+  const float* dloss;       // kDz: upstream gradient, [M] or one value
+  const float* count;       // kDz: counted tokens to divide by, or null
+  int per_token;            // kDz: dloss is [M]
+  int ignore_index;
+  const float* dxh;         // kGluBwd: [M, N] gradient of the down projection's normalised input
+  const int8_t* qp;         // kGluBwd: codes [M, N] of the down projection's input, their scales, 1 / rms,
+  const float *sp, *rp;     //   the row means of dxh x^, and the down projection's gain or null
+  const float *cp, *gain_p;
+  int plane_rows, plane_cols;   // columns written per segment (N padded, zeros past N)
+};
+
+// Weight scale as it is folded into a stored gradient and divided out again: 1
+// where it is so small that every code of the matrix is 0 (a code needs
+// |W| >= 5e-6, so gamma >= 5e-6 / (N K)).
+__host__ __device__ __forceinline__ float fold_gamma(float g) { return g > 1e-20f ? g : 1.0f; }
 
 struct TGemmArgs {
   const uint32_t* w[3];     // packed ternary weights per segment, [N, K/16]
@@ -109,6 +139,109 @@ bool tgemm_mma_fused_quant_supported(int M, int K, int esize);
 // and N % 128 == 0; `status` is the device status word for bounded-wait timeouts.
 bool tgemm_tc_supported(const TGemmArgs& a, Epi epi);
 cudaError_t launch_tgemm_tc(const TGemmArgs& a, Epi epi, mmf_dtype dt, int* status, cudaStream_t stream);
+// The training epilogues kLse, kDz, kGluBwd (a.wu set; out: bf16 planes, ldo columns).
+cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, mmf_dtype dt, int* status,
+                               cudaStream_t stream);
+
+// bf16 training products (bgemm_tc.cu), D fp32 accumulated:
+//   dw = false: D[i, j] = gamma row_scale[i] sum_r A[i, r] B[r, j], A [I, R] K-major
+//   dw = true:  D[i, j] = sum_r A[r, i] B[r, j] (/ fold_gamma(inv_gamma)), A [R, I]
+// B is [R, J]; J a multiple of 16; lda, ldb multiples of 8 elements.
+struct BGemmArgs {
+  bool dw;
+  const void* a;            // bf16; plane p starts p * a_plane rows further
+  int lda, a_plane, planes;
+  const void* b;            // bf16
+  int ldb;
+  int I, J, R;
+  int splits;               // > 1: fp32 slices [splits][slice_rows][J] at out[0], to be added up by the reader
+  int slice_rows;           // dw = false, or splits > 1: bgemm_slice_rows(I)
+  void* out[3];
+  bool out_f32;             // dw, splits 1: fp32 or bf16 result (else always fp32)
+  bool accumulate;          // fp32 output: add to what is there
+  int seg_pitch, seg_rows;  // dw, splits 1: row i goes to out[i / seg_pitch] row i % seg_pitch if < seg_rows
+  const float* gamma;       // dw = false: device scalar or null
+  const float* row_scale;   // dw = false: [I] or null
+  const float* inv_gamma[3];  // dw, splits 1: device scalars or null
+};
+int bgemm_splits(int I, int J, int R, int planes, int most);
+int bgemm_slice_rows(int I);
+cudaError_t launch_bgemm_tc(const BGemmArgs& g, int* status, cudaStream_t stream);
+
+// Operand preparation for those products, one launch (train.cu).
+struct PrepArgs {
+  const uint32_t* w[3];     // packed codes per segment -> wb [nseg * w_pitch, K] bf16 (rows past N zero); null wb: none
+  int nseg, N, w_pitch, K;
+  void* wb;
+  uint8_t* wu[3];           // also one byte per weight [N, K] per segment, or null
+  const int8_t* q;          // codes [M, qK] -> qb [M, qK] bf16, times 1 / scale[m] when q_scaled; null qb: none
+  const float* scale;
+  int M, qK;
+  bool q_scaled;
+  void* qb;
+  const void* dy;           // [M, g_seg, g_N] -> planes gb [planes][g_rows][g_seg * g_pitch], pad zero; null gb: none
+  mmf_dtype dy_dt;
+  int g_seg, g_N, g_pitch, g_planes, g_rows;
+  bool g_scaled;            // times 1 / scale[m]
+  void* gb;
+};
+cudaError_t launch_train_prep(const PrepArgs& a, cudaStream_t stream);
+
+// Backward of RMSNorm + quantisation (straight through) per row of length K:
+//   v = sum of the slices of dx^;  n = x rinv or q / (s gain);  c = mean(v x^)
+//   dx = rinv (gain v - n c) + dres
+// stat: only c (into cmean) and, with several slices, v (back into slice 0).
+struct NormBackArgs {
+  float* dxh;               // [slices][slice_rows][K]
+  int slices, slice_rows, M, K;
+  const int8_t* q;
+  const float *scale, *rinv, *gain;
+  const void* x;            // or null
+  const void* dres;         // or null
+  void* dx;
+  float* cmean;
+};
+cudaError_t launch_norm_back(const NormBackArgs& a, bool stat, mmf_dtype dt, cudaStream_t stream);
+
+// Column sums over tokens, in a fixed order (two launches when the rows are split).
+//   kGrad:   out[s][n] = sum_t src[t, s, n]                       (a caller's gradient in dt)
+//   kPlanes: out[s][n] = sum_t scale[t] sum_p plane_p[t, s, n] / fold_gamma(inv_gamma[s])
+//   kGain:   out[0][k] = sum_t v[t, k] n[t, k]                    (v, n as in NormBackArgs; slice 0 holds v when summed)
+enum class ColSum : int { kGrad = 0, kPlanes = 1, kGain = 2 };
+struct ColSumArgs {
+  const void* src;
+  int M, segs, N, pitch;    // columns s * pitch + n of a row of segs * pitch (kGrad: pitch = N)
+  int planes, plane_rows;
+  const float* scale;
+  const float* inv_gamma[3];
+  NormBackArgs nb;          // kGain
+  void* out[3];             // in dt; null: that segment is skipped
+  float* part;              // scratch, colsum_ws_floats(M, columns)
+};
+size_t colsum_ws_floats(int M, int cols);
+cudaError_t launch_colsum(const ColSumArgs& a, ColSum kind, mmf_dtype dt, cudaStream_t stream);
+
+// out[seg][n][k] = sum of the slices of dW (in order) / fold_gamma(inv_gamma[seg]), in dt.
+struct DwJoinArgs {
+  const float* part;        // [slices][slice_rows][K], row seg * seg_pitch + n
+  int slices, slice_rows, segs, seg_pitch, N, K;
+  const float* inv_gamma[3];
+  void* out[3];
+};
+cudaError_t launch_dw_join(const DwJoinArgs& a, mmf_dtype dt, cudaStream_t stream);
+
+// Loss from kLse's partials: lse[t], the tokens' losses, then (reduce) their sum or mean and the count.
+struct LossArgs {
+  const float2* part;
+  int slots, M, vocab;
+  const float* zlabel;
+  const int32_t* labels;
+  int ignore_index;
+  float *lse, *token;       // [M]
+  int reduction;            // mmf_reduction
+  float *loss, *count;      // loss: one value (sum, mean); count: counted tokens (at least 1)
+};
+cudaError_t launch_loss_join(const LossArgs& a, int* status, cudaStream_t stream);
 
 // One decode step (T = 1) of L consecutive blocks in one cooperative launch
 // (decode_step.cu). Per-block device descriptor, built at block creation:

@@ -83,6 +83,7 @@ struct Vec<float> {
 struct RowCode {
   float scale;
   int qsum;
+  float rinv;
 };
 
 // Warp-collective: all 32 lanes call it with the same row. `v` points at the
@@ -154,7 +155,7 @@ __device__ __forceinline__ RowCode quant_row(const uint4* v, int nvec, int K, co
     V::store_codes(qr + (size_t)vi * E, c, isum);
     if constexpr (INPLACE) asm volatile("" ::: "memory");
   }
-  return RowCode{sc, __reduce_add_sync(0xffffffffu, isum)};
+  return RowCode{sc, __reduce_add_sync(0xffffffffu, isum), rinv};
 }
 
 }  // namespace mmf

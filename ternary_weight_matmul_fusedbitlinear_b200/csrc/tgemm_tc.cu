@@ -91,11 +91,54 @@ struct TcArgs {
   int* status;
   long long wait_cycles;   // bound of every wait
   uint32_t skip_it;        // test hook: CTA 0 never loads this k-step (~0u: none)
+  TrainEpi t;              // training epilogues only
 };
+
+__host__ __device__ constexpr bool is_train(Epi e) { return e == Epi::kLse || e == Epi::kDz || e == Epi::kGluBwd; }
+__host__ __device__ constexpr bool is_glu(Epi e) { return e == Epi::kGlu || e == Epi::kGluBwd; }
+// Bytes of one staged output element: the training epilogues stage bf16 planes.
+template <Epi EPI, typename T>
+constexpr int out_bytes() {
+  return EPI == Epi::kAcc ? 4 : is_train(EPI) ? 2 : (int)sizeof(T);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_fast(float z) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(z));
+  return r;
+}
+
+// 32 logits of one token in log2 units, columns n0.. of the segment (past N: -inf).
+__device__ __forceinline__ void logits32(const uint32_t (&r)[32], int qs, float sc2, const float* bias, int n0, int N,
+                                         float (&z)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) z[j] = (float)((int)r[j] - qs) * sc2;
+  if (bias != nullptr) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (n0 + j < N) z[j] = fmaf(__ldg(bias + n0 + j), kLog2e, z[j]);
+  }
+  if (n0 + 32 > N) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (n0 + j >= N) z[j] = -INFINITY;
+  }
+}
+
+// Plane `pl` of g = g0 + g1 + g2 with bf16 planes: the next 8 bits of what the planes before left.
+__device__ __forceinline__ void take_plane(float (&g)[32], float (&out)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    out[j] = round_to<bf16>(g[j]);
+    g[j] -= out[j];
+  }
+}
 
 // Rows of weight segment `seg` starting at `row0` feed half `h` of tile `nt`.
 __device__ __forceinline__ void half_source(const TcArgs& p, Epi epi, int nt, int h, int& seg, int& row0) {
-  if (epi == Epi::kGlu) {
+  if (is_glu(epi)) {
     seg = h;
     row0 = nt * HALF;
   } else {
@@ -117,10 +160,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap map_b1, const __grid_constant__ CUtensorMap map_b2,
                     const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_res,
                     const TcArgs p) {
-  constexpr int OB = EPI == Epi::kAcc ? 4 : (int)sizeof(T);
+  constexpr int OB = out_bytes<EPI, T>();
   static_assert(!RB || (EPI == Epi::kStore && OB == 2), "residual prefetch: kStore with 2-byte outputs");
   using Smem = SmemLayout<OB, UNP, RB>;
   constexpr int NS = Smem::NS;
+  constexpr int kPlanes = sizeof(T) == 2 ? 1 : 3;   // training epilogues
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -347,6 +391,145 @@ __global__ void __launch_bounds__(kThreads, 1)
           stage_row(buf, lane, out, (T*)nullptr);
           release(n0, y0, buf);
         }
+      } else if constexpr (EPI == Epi::kLse) {
+        // Online softmax statistics of this token's 128 logits, in log2 units
+        // (exp2 of a difference, so nothing overflows); never stored.
+        const int c0 = nt * BN + group * HALF;
+        if (c0 < p.g.N) {
+          const float sc2 = *p.g.gamma[0] * inv_s * kLog2e;
+          const int lab = row_ok ? p.t.labels[m] - p.t.col0 : -1;
+          float mx = -INFINITY, sum = 0.0f;
+          for (int c = 0; c < HALF / 32; ++c) {
+            const int n0 = c0 + 32 * c;
+            if (n0 >= p.g.N) break;
+            uint32_t r[32];
+            tmem_ld32(tbase + group * HALF + 32 * c, r);
+            float z[32];
+            logits32(r, qs, sc2, p.g.bias[0], n0, p.g.N, z);
+            float cm = z[0];
+#pragma unroll
+            for (int j = 1; j < 32; ++j) cm = fmaxf(cm, z[j]);
+            if (lab >= n0 && lab < n0 + 32) {
+              float zl = z[0];
+#pragma unroll
+              for (int j = 1; j < 32; ++j) zl = (lab == n0 + j) ? z[j] : zl;
+              p.t.zlabel[m] = zl;
+            }
+            const float nm = fmaxf(mx, cm);
+            const float ref = nm == -INFINITY ? 0.0f : nm;   // nothing but -inf so far: exp2(-inf) = 0
+            sum *= exp2_fast(mx - ref);
+            mx = nm;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum += exp2_fast(z[j] - ref);
+          }
+          if (row_ok) p.t.part[(size_t)(nt * 2 + group) * p.g.M + m] = make_float2(mx, sum);
+        }
+      } else if constexpr (EPI == Epi::kDz) {
+        // dz = weight (softmax - onehot) over the token's scale s, so that one
+        // rounding to bf16 serves both products (s is put back per row of dx^,
+        // and dW multiplies by the codes themselves).
+        const int c0 = nt * BN + group * HALF;
+        if (c0 < p.t.plane_cols) {
+          const float sc2 = *p.g.gamma[0] * inv_s * kLog2e;
+          int lab = -1;
+          float wt = 0.0f, lse2 = 0.0f;
+          if (row_ok) {
+            const int l = p.t.labels[m];
+            if (l != p.t.ignore_index && l >= 0 && l < p.t.vocab) {
+              lab = l - p.t.col0;
+              wt = p.t.dloss != nullptr ? p.t.dloss[p.t.per_token ? m : 0] : 1.0f;
+              if (p.t.count != nullptr) wt /= *p.t.count;
+              wt *= inv_s;
+              lse2 = p.t.lse[m] * kLog2e;
+            }
+          }
+          for (int c = 0; c < HALF / 32; ++c) {
+            const int n0 = c0 + 32 * c;
+            if (n0 >= p.t.plane_cols) break;
+            uint32_t r[32];
+            tmem_ld32(tbase + group * HALF + 32 * c, r);
+            float z[32];
+            logits32(r, qs, sc2, p.g.bias[0], n0, p.g.N, z);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float g = exp2_fast(z[j] - lse2) - (lab == n0 + j ? 1.0f : 0.0f);
+              z[j] = wt == 0.0f || n0 + j >= p.g.N ? 0.0f : g * wt;
+            }
+#pragma unroll
+            for (int pl = 0; pl < kPlanes; ++pl) {
+              float out[32];
+              take_plane(z, out);
+              uint8_t* buf;
+              claim(buf);
+              stage_row(buf, lane, out, (bf16*)nullptr);
+              release(n0, pl * p.t.plane_rows + y0, buf);
+            }
+          }
+        }
+      } else if constexpr (EPI == Epi::kGluBwd) {
+        // u and v again from the codes; dp from the down projection's dx^ and
+        // its norm (read through the codes of p); du, dv over the token's scale.
+        const float sc_u = *p.g.gamma[0] * inv_s, sc_v = *p.g.gamma[1] * inv_s;
+        const float fu = fold_gamma(*p.g.gamma[0]) * inv_s, fv = fold_gamma(*p.g.gamma[1]) * inv_s;
+        const float r_p = row_ok ? p.t.rp[m] : 0.0f, c_p = row_ok ? p.t.cp[m] : 0.0f;
+        const float inv_sp = row_ok ? 1.0f / p.t.sp[m] : 0.0f;
+        for (int cc = 0; cc < 2; ++cc) {
+          const int c = group * 2 + cc;
+          const int n0 = nt * HALF + 32 * c;
+          if (n0 >= p.t.plane_cols) break;
+          float dp[32];
+#pragma unroll
+          for (int j = 0; j < 32; j += 16) {   // N is a multiple of 16
+            if (row_ok && n0 + j < p.g.N) {
+              const size_t at = (size_t)m * p.g.N + n0 + j;
+              const int4 q16 = *reinterpret_cast<const int4*>(p.t.qp + at);
+              const int* qw = &q16.x;
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                const float4 d4 = *reinterpret_cast<const float4*>(p.t.dxh + at + e);
+                const float* d = &d4.x;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                  const float xh = (float)((qw[e / 4] << (24 - 8 * b)) >> 24) * inv_sp;
+                  const float gn = p.t.gain_p != nullptr ? __ldg(p.t.gain_p + n0 + j + e + b) : 1.0f;
+                  const float n = p.t.gain_p == nullptr ? xh : (gn != 0.0f ? xh / gn : 0.0f);
+                  dp[j + e + b] = r_p * (gn * d[b] - n * c_p);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) dp[j + e] = 0.0f;
+            }
+          }
+          uint32_t ru[32], rv[32];
+          tmem_ld32(tbase + 32 * c, ru);
+          tmem_ld32(tbase + HALF + 32 * c, rv);
+          float du[32], dv[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float u = (float)((int)ru[j] - qs) * sc_u, v = (float)((int)rv[j] - qs) * sc_v;
+            const bool in = n0 + j < p.g.N;
+            if (p.g.bias[0] != nullptr && in) u += __ldg(p.g.bias[0] + n0 + j);
+            if (p.g.bias[1] != nullptr && in) v += __ldg(p.g.bias[1] + n0 + j);
+            const float sg = __fdividef(1.0f, 1.0f + exp2_fast(-u * kLog2e));
+            const float us = u * sg;
+            du[j] = in && row_ok ? dp[j] * v * fmaf(us, 1.0f - sg, sg) * fu : 0.0f;
+            dv[j] = in && row_ok ? dp[j] * us * fv : 0.0f;
+          }
+#pragma unroll
+          for (int pl = 0; pl < kPlanes; ++pl) {
+            float out[32];
+            uint8_t* buf;
+            take_plane(du, out);
+            claim(buf);
+            stage_row(buf, lane, out, (bf16*)nullptr);
+            release(n0, pl * p.t.plane_rows + y0, buf);
+            take_plane(dv, out);
+            claim(buf);
+            stage_row(buf, lane, out, (bf16*)nullptr);
+            release(p.t.plane_cols + n0, pl * p.t.plane_rows + y0, buf);
+          }
+        }
       } else {
         const int h = group;                      // 128-column half of the tile
         int seg, row0;
@@ -437,6 +620,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- host side
 template <Epi EPI, typename T, bool UNP, bool RB = false>
+cudaError_t launch_mapped(const CUtensorMap& ma, const CUtensorMap (&mb)[3], const CUtensorMap& mo,
+                          const CUtensorMap& mr, const TcArgs& p, cudaStream_t stream) {
+  const size_t smem = sizeof(SmemLayout<out_bytes<EPI, T>(), UNP, RB>) + 1024;
+  auto kern = tgemm_tc_kernel<EPI, T, UNP, RB>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int tiles = p.m_tiles * p.n_tiles;
+  const int grid = std::min(tiles, num_sms());
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, stream, ma, mb[0], mb[1], mb[2], mo, mr, p);
+}
+
+template <Epi EPI, typename T, bool UNP, bool RB = false>
 cudaError_t launch_typed(const CUtensorMap& ma, const CUtensorMap (&mb)[3], const TcArgs& p, cudaStream_t stream) {
   CUtensorMap mo;
   const bool acc_out = EPI == Epi::kAcc;
@@ -451,13 +646,7 @@ cudaError_t launch_typed(const CUtensorMap& ma, const CUtensorMap (&mb)[3], cons
   if (EPI == Epi::kStore && p.g.residual != nullptr &&
       !make_tma_2d(&mr, p.g.residual, odt, esize, (uint64_t)p.g.N, (uint64_t)p.g.M, kEpiChunk, 32, oswz))
     return cudaErrorInvalidValue;
-  const size_t smem = sizeof(SmemLayout<(EPI == Epi::kAcc ? 4 : (int)sizeof(T)), UNP, RB>) + 1024;
-  auto kern = tgemm_tc_kernel<EPI, T, UNP, RB>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  const int tiles = p.m_tiles * p.n_tiles;
-  const int grid = std::min(tiles, num_sms());
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, stream, ma, mb[0], mb[1], mb[2], mo, mr, p);
+  return launch_mapped<EPI, T, UNP, RB>(ma, mb, mo, mr, p, stream);
 }
 
 }  // namespace
@@ -487,7 +676,7 @@ cudaError_t launch_tgemm_tc(const TGemmArgs& a, Epi epi, mmf_dtype dt, int* stat
                                       (uint64_t)a.N, BK / 16, HALF, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (!ok) return cudaErrorInvalidValue;
   }
-  TcArgs p;
+  TcArgs p = {};
   p.g = a;
   p.status = status;
   p.wait_cycles = wait_limit_cycles();
@@ -513,6 +702,44 @@ cudaError_t launch_tgemm_tc(const TGemmArgs& a, Epi epi, mmf_dtype dt, int* stat
     default: return cudaErrorNotSupported;
   }
 #undef MMF_TC_LAUNCH
+}
+
+cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, mmf_dtype dt, int* status,
+                               cudaStream_t stream) {
+  if (a.M == 0) return cudaSuccess;
+  CUtensorMap ma, mb[3], mo;
+  if (!make_tma_2d(&ma, a.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.M, BK, BM,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  for (int r = 0; r < 3; ++r)
+    if (!make_tma_2d(&mb[r], a.wu[r < a.nseg ? r : 0], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.N,
+                     BK, HALF, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  const int planes = dt == MMF_BF16 ? 1 : 3;
+  mo = ma;   // kLse stores no tile
+  if (epi != Epi::kLse &&
+      !make_tma_2d(&mo, a.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)a.ldo, (uint64_t)planes * t.plane_rows,
+                   kEpiChunk, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
+  TcArgs p;
+  p.g = a;
+  p.t = t;
+  p.status = status;
+  p.wait_cycles = wait_limit_cycles();
+  p.skip_it = (uint32_t)test_hook("MMF_TC_SKIP_KSTEP");
+  p.m_tiles = ceil_div(a.M, BM);
+  p.n_tiles = is_glu(epi) ? ceil_div(a.N, HALF) : ceil_div(a.N, BN);
+  const bool b = dt == MMF_BF16;
+  switch (epi) {
+    case Epi::kLse: return launch_mapped<Epi::kLse, bf16, true>(ma, mb, mo, mo, p, stream);
+    case Epi::kDz:
+      return b ? launch_mapped<Epi::kDz, bf16, true>(ma, mb, mo, mo, p, stream)
+               : launch_mapped<Epi::kDz, float, true>(ma, mb, mo, mo, p, stream);
+    case Epi::kGluBwd:
+      return b ? launch_mapped<Epi::kGluBwd, bf16, true>(ma, mb, mo, mo, p, stream)
+               : launch_mapped<Epi::kGluBwd, float, true>(ma, mb, mo, mo, p, stream);
+    default: return cudaErrorNotSupported;
+  }
 }
 
 }  // namespace mmf

@@ -1,0 +1,459 @@
+// Training: the row, column and operand kernels around the tensor-core
+// products of the backward pass (sm_100a). All of them are bound by the bytes
+// they move; sums over rows or columns are held in fp32 and taken in a fixed
+// order, so a result never depends on how blocks are scheduled.
+#include "kernels.cuh"
+
+namespace mmf {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---------------------------------------------------------------- operands
+// A bf16 pair of ternary codes: stored field 0, 1, 2 -> -1, 0, 1.
+__device__ __forceinline__ uint32_t code_bf16(uint32_t c) { return c == 0u ? 0xBF80u : (c == 1u ? 0u : 0x3F80u); }
+
+struct PrepUnits {
+  PrepArgs a;
+  size_t w_units, q_units, g_units;   // 16 weights; 16 codes; 8 gradient columns
+  int g_row_units;
+};
+
+// One launch for the operands of a backward: packed codes -> bf16 (and bytes),
+// int8 codes -> bf16, the gradient -> padded bf16 planes. Each unit is one
+// 16- or 32-byte store.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) train_prep_kernel(const PrepUnits u) {
+  pdl_trigger();
+  pdl_wait();
+  const PrepArgs& a = u.a;
+  const size_t total = u.w_units + u.q_units + u.g_units;
+  for (size_t id = (size_t)blockIdx.x * kThreads + threadIdx.x; id < total; id += (size_t)gridDim.x * kThreads) {
+    if (id < u.w_units) {
+      const int wpr = a.K / 16;
+      const int row = (int)(id / wpr), j = (int)(id % wpr);
+      const int seg = row / a.w_pitch, n = row - seg * a.w_pitch;
+      const uint32_t word = n < a.N ? __ldg(a.w[seg] + (size_t)n * wpr + j) : 0x55555555u;   // all zero weights
+      if (a.wb != nullptr) {
+        uint32_t o[8];
+#pragma unroll
+        for (int c = 0; c < 16; c += 2) {   // column 4i + b at bits 8b + 2i
+          const int s0 = 8 * (c & 3) + 2 * (c >> 2), s1 = 8 * ((c + 1) & 3) + 2 * ((c + 1) >> 2);
+          o[c / 2] = code_bf16((word >> s0) & 3u) | (code_bf16((word >> s1) & 3u) << 16);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.wb) + id * 32);
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      if (a.wu[seg] != nullptr && n < a.N)
+        *reinterpret_cast<uint4*>(a.wu[seg] + ((size_t)n * wpr + j) * 16) =
+            make_uint4(word & 0x03030303u, (word >> 2) & 0x03030303u, (word >> 4) & 0x03030303u,
+                       (word >> 6) & 0x03030303u);
+    } else if (id < u.w_units + u.q_units) {
+      const size_t k = id - u.w_units;
+      const int4 v = *reinterpret_cast<const int4*>(a.q + k * 16);
+      const float sc = a.q_scaled ? 1.0f / __ldg(a.scale + k / (a.qK / 16)) : 1.0f;
+      const int* w = &v.x;
+      float f[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) f[c] = (float)((w[c >> 2] << (24 - 8 * (c & 3))) >> 24) * sc;
+      bf16* dst = static_cast<bf16*>(a.qb) + k * 16;
+      store8(dst, *reinterpret_cast<float(*)[8]>(&f[0]));
+      store8(dst + 8, *reinterpret_cast<float(*)[8]>(&f[8]));
+    } else {
+      const size_t k = id - u.w_units - u.q_units;
+      const int row = (int)(k / u.g_row_units), c0 = (int)(k % u.g_row_units) * 8;
+      const int seg = c0 / a.g_pitch, n0 = c0 - seg * a.g_pitch;
+      const T* src = static_cast<const T*>(a.dy) + ((size_t)row * a.g_seg + seg) * a.g_N;
+      const float sc = a.g_scaled && row < a.M ? 1.0f / __ldg(a.scale + row) : 1.0f;
+      float v[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] = row < a.M && n0 + c < a.g_N ? to_f32(src[n0 + c]) * sc : 0.0f;
+      const size_t ld = (size_t)a.g_seg * a.g_pitch;
+      for (int p = 0; p < a.g_planes; ++p) {
+        float o[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          o[c] = round_to<bf16>(v[c]);
+          v[c] -= o[c];
+        }
+        store8(static_cast<bf16*>(a.gb) + ((size_t)p * a.g_rows + row) * ld + c0, o);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- RMSNorm backward
+__device__ __forceinline__ void ld4(const float* p, float (&v)[4]) {
+  const float4 f = *reinterpret_cast<const float4*>(p);
+  v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+}
+__device__ __forceinline__ void ld4(const bf16* p, float (&v)[4]) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+  v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+__device__ __forceinline__ void st4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void st4(bf16* p, const float (&v)[4]) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  uint2 u;
+  u.x = *reinterpret_cast<uint32_t*>(&a);
+  u.y = *reinterpret_cast<uint32_t*>(&b);
+  *reinterpret_cast<uint2*>(p) = u;
+}
+
+// dx^ of 4 columns, summed over the slices in order.
+__device__ __forceinline__ void slices4(const NormBackArgs& a, size_t at, float (&v)[4]) {
+  ld4(a.dxh + at, v);
+  const size_t step = (size_t)a.slice_rows * a.K;
+  for (int s = 1; s < a.slices; ++s) {
+    float w[4];
+    ld4(a.dxh + s * step + at, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += w[i];
+  }
+}
+
+// x^ and the norm's output before the gain, of 4 columns: from the codes, or
+// from x when the caller kept it. A column whose gain is 0 left nothing in the
+// codes: its n counts as 0.
+template <typename T>
+__device__ __forceinline__ void norm4(const NormBackArgs& a, size_t at, int k, float inv_s, float rinv, float (&xh)[4],
+                                      float (&n)[4], float (&g)[4]) {
+  if (a.gain != nullptr) ld4(a.gain + k, g);
+  else g[0] = g[1] = g[2] = g[3] = 1.0f;
+  if (a.x != nullptr) {
+    ld4(static_cast<const T*>(a.x) + at, n);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      n[i] *= rinv;
+      xh[i] = n[i] * g[i];
+    }
+  } else {
+    const int w = *reinterpret_cast<const int*>(a.q + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      xh[i] = (float)((w << (24 - 8 * i)) >> 24) * inv_s;
+      n[i] = a.gain == nullptr ? xh[i] : (g[i] != 0.0f ? xh[i] / g[i] : 0.0f);
+    }
+  }
+}
+
+// WPR warps per row (1 for many rows, 8 for few or long ones). The second pass
+// reads the row again from L1/L2, where the first one has just brought it.
+template <typename T, int WPR, bool STAT>
+__global__ void __launch_bounds__(kThreads) norm_back_kernel(const NormBackArgs a) {
+  __shared__ float red[kThreads / 32];
+  pdl_trigger();
+  pdl_wait();
+  constexpr int kRows = kThreads / 32 / WPR, kLanes = 32 * WPR;
+  const int lane = threadIdx.x % kLanes, warp = threadIdx.x >> 5;
+  for (int row0 = blockIdx.x * kRows; row0 < a.M; row0 += gridDim.x * kRows) {
+    const int row = row0 + (int)threadIdx.x / kLanes;
+    const bool in = row < a.M;
+    const size_t base = (size_t)row * a.K;
+    const float inv_s = in ? 1.0f / a.scale[row] : 0.0f, rinv = in ? a.rinv[row] : 0.0f;
+    float dot = 0.0f;
+    if (in) {
+#pragma unroll 4
+      for (int k = lane * 4; k < a.K; k += kLanes * 4) {
+        float v[4], xh[4], n[4], g[4];
+        slices4(a, base + k, v);
+        if constexpr (STAT) {   // only the codes are read for the mean
+          const int w = *reinterpret_cast<const int*>(a.q + base + k);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) xh[i] = (float)((w << (24 - 8 * i)) >> 24) * inv_s;
+          if (a.slices > 1) st4(a.dxh + base + k, v);
+        } else {
+          norm4<T>(a, base + k, k, inv_s, rinv, xh, n, g);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dot = fmaf(v[i], xh[i], dot);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if constexpr (WPR > 1) {
+      if ((threadIdx.x & 31) == 0) red[warp] = dot;
+      __syncthreads();
+      dot = 0.0f;
+      for (int w = 0; w < WPR; ++w) dot += red[warp / WPR * WPR + w];
+      __syncthreads();
+    }
+    const float c = dot / (float)a.K;
+    if constexpr (STAT) {
+      if (in && lane == 0) a.cmean[row] = c;
+    } else if (in) {
+#pragma unroll 4
+      for (int k = lane * 4; k < a.K; k += kLanes * 4) {
+        float v[4], xh[4], n[4], g[4], o[4];
+        slices4(a, base + k, v);
+        norm4<T>(a, base + k, k, inv_s, rinv, xh, n, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = rinv * fmaf(g[i], v[i], -n[i] * c);
+        if (a.dres != nullptr) {
+          float d[4];
+          ld4(static_cast<const T*>(a.dres) + base + k, d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] += d[i];
+        }
+        st4(static_cast<T*>(a.dx) + base + k, o);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- column sums
+constexpr int kColsPerBlock = 64, kRowLanes = kThreads / kColsPerBlock;
+
+template <ColSum KIND, typename T>
+__device__ __forceinline__ float col_term(const ColSumArgs& a, int t, int c) {
+  if constexpr (KIND == ColSum::kGrad) {
+    return to_f32(static_cast<const T*>(a.src)[(size_t)t * a.segs * a.pitch + c]);
+  } else if constexpr (KIND == ColSum::kPlanes) {
+    float v = 0.0f;
+    for (int p = 0; p < a.planes; ++p)
+      v += to_f32(static_cast<const bf16*>(a.src)[((size_t)p * a.plane_rows + t) * a.segs * a.pitch + c]);
+    return v * a.scale[t];
+  } else {
+    const NormBackArgs& b = a.nb;
+    const size_t at = (size_t)t * b.K + c;
+    float v = b.dxh[at];
+    for (int s = 1; s < b.slices; ++s) v += b.dxh[(size_t)s * b.slice_rows * b.K + at];
+    if (b.x != nullptr) return v * to_f32(static_cast<const T*>(b.x)[at]) * b.rinv[t];
+    const float g = b.gain != nullptr ? b.gain[c] : 1.0f;
+    return g != 0.0f ? v * ((float)b.q[at] / b.scale[t] / g) : 0.0f;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void col_store(const ColSumArgs& a, int c, float v) {
+  const int seg = c / a.pitch, n = c - seg * a.pitch;
+  if (seg >= a.segs || n >= a.N || a.out[seg] == nullptr) return;
+  if (a.inv_gamma[seg] != nullptr) v /= fold_gamma(*a.inv_gamma[seg]);
+  static_cast<T*>(a.out[seg])[n] = from_f32<T>(v);
+}
+
+// Block (x: 64 columns, y: a range of rows); a thread sums every 4th row of its
+// column, the four are added in order. One range writes the result, several
+// write partial sums.
+template <ColSum KIND, typename T>
+__global__ void __launch_bounds__(kThreads) colsum_kernel(const ColSumArgs a, int cols, int rows_per) {
+  __shared__ float red[kRowLanes][kColsPerBlock];
+  pdl_trigger();
+  pdl_wait();
+  const int c = blockIdx.x * kColsPerBlock + threadIdx.x % kColsPerBlock, rl = threadIdx.x / kColsPerBlock;
+  const int t0 = blockIdx.y * rows_per, t1 = min(a.M, t0 + rows_per);
+  float sum = 0.0f;
+  if (c < cols) {
+#pragma unroll 4
+    for (int t = t0 + rl; t < t1; t += kRowLanes) sum += col_term<KIND, T>(a, t, c);
+  }
+  red[rl][threadIdx.x % kColsPerBlock] = sum;
+  __syncthreads();
+  if (rl == 0 && c < cols) {
+    float v = red[0][threadIdx.x];
+    for (int i = 1; i < kRowLanes; ++i) v += red[i][threadIdx.x];
+    if (gridDim.y == 1) col_store<T>(a, c, v);
+    else a.part[(size_t)blockIdx.y * cols + c] = v;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) colsum_join_kernel(const ColSumArgs a, int cols, int parts) {
+  pdl_trigger();
+  pdl_wait();
+  const int c = blockIdx.x * kThreads + threadIdx.x;
+  if (c >= cols) return;
+  float v = 0.0f;
+  for (int i = 0; i < parts; ++i) v += a.part[(size_t)i * cols + c];
+  col_store<T>(a, c, v);
+}
+
+// Row ranges: at least 64 rows each, about two blocks per SM in all.
+int colsum_parts(int M, int cols) {
+  const int want = std::max(1, 2 * 148 / ceil_div(cols, kColsPerBlock));
+  return std::max(1, std::min(want, ceil_div(M, 64)));
+}
+
+// ---------------------------------------------------------------- joining slices of dW
+template <typename T>
+__global__ void __launch_bounds__(kThreads) dw_join_kernel(const DwJoinArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const int kq = a.K / 4;
+  const size_t total = (size_t)a.segs * a.N * kq;
+  const size_t step = (size_t)a.slice_rows * a.K;
+  for (size_t id = (size_t)blockIdx.x * kThreads + threadIdx.x; id < total; id += (size_t)gridDim.x * kThreads) {
+    const int k = (int)(id % kq) * 4;
+    const int r = (int)(id / kq), seg = r / a.N, n = r - seg * a.N;
+    if (a.out[seg] == nullptr) continue;
+    const float* src = a.part + ((size_t)seg * a.seg_pitch + n) * a.K + k;
+    float v[4];
+    ld4(src, v);
+    for (int s = 1; s < a.slices; ++s) {
+      float w[4];
+      ld4(src + s * step, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += w[i];
+    }
+    if (a.inv_gamma[seg] != nullptr) {
+      const float f = 1.0f / fold_gamma(*a.inv_gamma[seg]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] *= f;
+    }
+    st4(static_cast<T*>(a.out[seg]) + (size_t)n * a.K + k, v);
+  }
+}
+
+// ---------------------------------------------------------------- the loss
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kJoinRows = 32, kJoinGroups = kThreads / kJoinRows;
+
+// 32 rows per block, 8 threads per row: thread (row, g) folds the row's slots
+// g, g + 8, ... (slot-major, so a warp reads 32 neighbouring rows), the eight
+// are folded in order. loss_t = (lse - z_label), both in log2 units until here.
+__global__ void __launch_bounds__(kThreads) loss_rows_kernel(const LossArgs a, int* status) {
+  __shared__ float2 red[kJoinGroups][kJoinRows];
+  pdl_trigger();
+  pdl_wait();
+  const int r = threadIdx.x % kJoinRows, g = threadIdx.x / kJoinRows;
+  const int m = blockIdx.x * kJoinRows + r;
+  float mx = -INFINITY, sum = 0.0f;
+  auto fold = [&](float2 o) {
+    const float nm = fmaxf(mx, o.x);
+    if (nm != -INFINITY) sum = sum * exp2f(mx - nm) + o.y * exp2f(o.x - nm);
+    else sum += o.y;   // keeps a NaN
+    mx = nm;
+  };
+  if (m < a.M) {
+#pragma unroll 4
+    for (int s = g; s < a.slots; s += kJoinGroups) fold(a.part[(size_t)s * a.M + m]);
+  }
+  red[g][r] = make_float2(mx, sum);
+  __syncthreads();
+  if (g == 0 && m < a.M) {
+    for (int i = 1; i < kJoinGroups; ++i) fold(red[i][r]);
+    const float lse2 = mx + log2f(sum);
+    const int l = a.labels[m];
+    float loss = 0.0f;
+    if (l != a.ignore_index) {
+      if (l >= 0 && l < a.vocab) loss = (lse2 - a.zlabel[m]) * kLn2;
+      else if (status != nullptr) atomicExch(status, 9);   // reported by mmf_check; counts as ignored
+    }
+    a.lse[m] = lse2 * kLn2;
+    a.token[m] = loss;
+  }
+}
+
+// One block: the tokens' sum in fp64 and the number counted, in a fixed order.
+__global__ void __launch_bounds__(1024) loss_reduce_kernel(const LossArgs a) {
+  __shared__ double sums[32];
+  __shared__ int counts[32];
+  pdl_trigger();
+  pdl_wait();
+  double s = 0.0;
+  int n = 0;
+  for (int m = threadIdx.x; m < a.M; m += 1024) {
+    s += (double)a.token[m];
+    const int l = a.labels[m];
+    n += l != a.ignore_index && l >= 0 && l < a.vocab;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    sums[threadIdx.x >> 5] = s;
+    counts[threadIdx.x >> 5] = n;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 32; ++w) {
+      s += sums[w];
+      n += counts[w];
+    }
+    const float count = (float)max(1, n);
+    *a.count = count;
+    *a.loss = (float)(a.reduction == MMF_REDUCE_MEAN ? s / (double)count : s);
+  }
+}
+
+int blocks_for(size_t units, int per_sm) {
+  return (int)std::max<size_t>(1, std::min<size_t>((units + kThreads - 1) / kThreads, (size_t)num_sms() * per_sm));
+}
+
+}  // namespace
+
+cudaError_t launch_train_prep(const PrepArgs& a, cudaStream_t stream) {
+  PrepUnits u;
+  u.a = a;
+  u.w_units = a.nseg > 0 ? (size_t)a.nseg * a.w_pitch * (a.K / 16) : 0;
+  u.q_units = a.qb != nullptr ? (size_t)a.M * (a.qK / 16) : 0;
+  u.g_row_units = a.gb != nullptr ? a.g_seg * a.g_pitch / 8 : 0;
+  u.g_units = (size_t)u.g_row_units * a.g_rows;
+  const size_t total = u.w_units + u.q_units + u.g_units;
+  if (total == 0) return cudaSuccess;
+  const dim3 grid(blocks_for(total, 8));
+  return a.dy_dt == MMF_BF16 ? launch_pdl(train_prep_kernel<bf16>, grid, dim3(kThreads), 0, stream, u)
+                             : launch_pdl(train_prep_kernel<float>, grid, dim3(kThreads), 0, stream, u);
+}
+
+template <typename T>
+static cudaError_t norm_back_typed(const NormBackArgs& a, bool stat, cudaStream_t stream) {
+  // one warp per row once there are enough rows for every SM's warps
+  const bool warp_rows = a.M >= num_sms() * 16 && a.K <= 4096;
+  const dim3 grid(warp_rows ? std::min(ceil_div(a.M, 8), num_sms() * 8) : std::min(a.M, num_sms() * 8));
+  const dim3 block(kThreads);
+  if (stat)
+    return warp_rows ? launch_pdl(norm_back_kernel<T, 1, true>, grid, block, 0, stream, a)
+                     : launch_pdl(norm_back_kernel<T, 8, true>, grid, block, 0, stream, a);
+  return warp_rows ? launch_pdl(norm_back_kernel<T, 1, false>, grid, block, 0, stream, a)
+                   : launch_pdl(norm_back_kernel<T, 8, false>, grid, block, 0, stream, a);
+}
+
+cudaError_t launch_norm_back(const NormBackArgs& a, bool stat, mmf_dtype dt, cudaStream_t stream) {
+  if (a.M == 0) return cudaSuccess;
+  return dt == MMF_BF16 ? norm_back_typed<bf16>(a, stat, stream) : norm_back_typed<float>(a, stat, stream);
+}
+
+size_t colsum_ws_floats(int M, int cols) {
+  const int parts = colsum_parts(M, cols);
+  return parts > 1 ? (size_t)parts * cols : 0;
+}
+
+template <typename T>
+static cudaError_t colsum_typed(const ColSumArgs& a, ColSum kind, cudaStream_t stream) {
+  const int cols = a.segs * a.pitch, parts = colsum_parts(a.M, cols), rows_per = ceil_div(a.M, parts);
+  const dim3 grid(ceil_div(cols, kColsPerBlock), parts), block(kThreads);
+  cudaError_t e = cudaSuccess;
+  switch (kind) {
+    case ColSum::kGrad: e = launch_pdl(colsum_kernel<ColSum::kGrad, T>, grid, block, 0, stream, a, cols, rows_per); break;
+    case ColSum::kPlanes: e = launch_pdl(colsum_kernel<ColSum::kPlanes, T>, grid, block, 0, stream, a, cols, rows_per); break;
+    case ColSum::kGain: e = launch_pdl(colsum_kernel<ColSum::kGain, T>, grid, block, 0, stream, a, cols, rows_per); break;
+  }
+  if (e != cudaSuccess || parts == 1) return e;
+  return launch_pdl(colsum_join_kernel<T>, dim3(ceil_div(cols, kThreads)), block, 0, stream, a, cols, parts);
+}
+
+cudaError_t launch_colsum(const ColSumArgs& a, ColSum kind, mmf_dtype dt, cudaStream_t stream) {
+  return dt == MMF_BF16 ? colsum_typed<bf16>(a, kind, stream) : colsum_typed<float>(a, kind, stream);
+}
+
+cudaError_t launch_dw_join(const DwJoinArgs& a, mmf_dtype dt, cudaStream_t stream) {
+  const dim3 grid(blocks_for((size_t)a.segs * a.N * (a.K / 4), 8)), block(kThreads);
+  return dt == MMF_BF16 ? launch_pdl(dw_join_kernel<bf16>, grid, block, 0, stream, a)
+                        : launch_pdl(dw_join_kernel<float>, grid, block, 0, stream, a);
+}
+
+cudaError_t launch_loss_join(const LossArgs& a, int* status, cudaStream_t stream) {
+  cudaError_t e = launch_pdl(loss_rows_kernel, dim3(ceil_div(a.M, kJoinRows)), dim3(kThreads), 0, stream, a, status);
+  if (e != cudaSuccess || a.reduction == MMF_REDUCE_NONE) return e;
+  return launch_pdl(loss_reduce_kernel, dim3(1), dim3(1024), 0, stream, a);
+}
+
+}  // namespace mmf

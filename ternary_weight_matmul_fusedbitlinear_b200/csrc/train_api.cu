@@ -1,0 +1,831 @@
+// Host side of the training entry points (BitLinear, GLU, LM-head loss):
+// argument validation, workspace carving and launch sequences.
+#include "api_common.cuh"
+
+using namespace mmf;
+
+namespace {
+
+constexpr int kMaxSplits = 32;                   // fp32 slices of one split product
+constexpr size_t kPieceBytes = size_t(256) << 20;   // gradient of the logits held at once
+
+int pad(int v, int to) { return (v + to - 1) / to * to; }
+int planes_of(mmf_dtype dt) { return dt == MMF_BF16 ? 1 : 3; }
+int plane_rows_of(int M, mmf_dtype dt) { return dt == MMF_BF16 ? M : pad(M, 128); }
+
+mmf_status check_kept(const mmf_act8* k, const char* what) {
+  if (k == nullptr) return fail(MMF_ERR_INVALID_ARG, "%s: null kept activations", what);
+  if (!k->q || !k->scale || !k->qsum || !k->rinv) return fail(MMF_ERR_INVALID_ARG, "%s: null kept buffer", what);
+  if (!aligned16(k->q) || !aligned16(k->scale) || !aligned16(k->qsum) || !aligned16(k->rinv))
+    return fail(MMF_ERR_MISALIGNED, "%s: kept buffers", what);
+  return MMF_OK;
+}
+
+mmf_status check_common(const char* what, mmf_dtype dt, int M) {
+  if (!dtype_ok(dt)) return fail(MMF_ERR_INVALID_ARG, "%s: bad dtype %d", what, (int)dt);
+  if (M < 0) return fail(MMF_ERR_INVALID_ARG, "%s: M=%d", what, M);
+  if (!tma_available()) return fail(MMF_ERR_CUDA, "%s: no tensor-map encoder in this driver", what);
+  return MMF_OK;
+}
+
+// Layers of one input: same shape, same gain.
+mmf_status check_lins(const mmf_tlinear* lins, int n, const char* what) {
+  if (lins == nullptr || n < 1 || n > 3) return fail(MMF_ERR_INVALID_ARG, "%s: %d layers (1 to 3)", what, n);
+  for (int i = 0; i < n; ++i) {
+    const mmf_status st = check_tlinear(&lins[i], what);
+    if (st != MMF_OK) return st;
+    if (lins[i].N != lins[0].N || lins[i].K != lins[0].K)
+      return fail(MMF_ERR_UNSUPPORTED_SHAPE, "%s: layers of one input must have one shape", what);
+    if (lins[i].gain != lins[0].gain)
+      return fail(MMF_ERR_UNSUPPORTED_SHAPE, "%s: layers of one input must share one gain", what);
+  }
+  if ((long long)n * lins[0].N > (1 << 28) || lins[0].K > (1 << 20))
+    return fail(MMF_ERR_UNSUPPORTED_SHAPE, "%s: %d x %d is too large", what, lins[0].N, lins[0].K);
+  return MMF_OK;
+}
+
+mmf_status check_ptrs(const char* what, std::initializer_list<const void*> needed,
+                      std::initializer_list<const void*> optional) {
+  for (const void* p : needed)
+    if (p == nullptr) return fail(MMF_ERR_INVALID_ARG, "%s: null pointer", what);
+  for (const void* p : needed)
+    if (!aligned16(p)) return fail(MMF_ERR_MISALIGNED, "%s: pointer not 16-byte aligned", what);
+  for (const void* p : optional)
+    if (p != nullptr && !aligned16(p)) return fail(MMF_ERR_MISALIGNED, "%s: pointer not 16-byte aligned", what);
+  return MMF_OK;
+}
+
+mmf_status zero(void* p, size_t bytes, cudaStream_t s) {
+  if (p != nullptr && bytes != 0) MMF_CUDA(cudaMemsetAsync(p, 0, bytes, s), "zero gradient");
+  return MMF_OK;
+}
+
+// Forward: codes of x into `kept`, then the contraction that reads them.
+mmf_status quant_keep(const void* x, mmf_dtype dt, int M, int K, const float* gain, float eps, const mmf_act8& k,
+                      cudaStream_t s) {
+  MMF_CUDA(timed("rmsnorm_quant", s,
+                 [&] {
+                   return launch_rmsnorm_quant(x, dt, M, K, gain, eps, k.q, k.scale, k.qsum, status_word(), s, nullptr,
+                                               0, k.rinv);
+                 }),
+           "rmsnorm_quant");
+  return MMF_OK;
+}
+
+// From this many tokens on a training forward first writes the codes one byte
+// per weight, which the contraction loads directly (about 1.5x its speed);
+// below, that launch costs more than it saves.
+constexpr int kUnpackMinTokens = 1024;
+
+// ---------------------------------------------------------------- the two products of a backward
+
+// An operand gradient G [M, cols], as bf16 planes: dy itself, or prepared ones.
+struct Grad {
+  const void* g;
+  int ld, plane_rows, planes;
+  bool over_s;   // holds G / s: dx^ puts s back per row, dW multiplies by the codes themselves
+};
+
+struct Splits {
+  int dx, dw;
+};
+
+// Workspace of the products for an input [M, K] and `cols` gradient columns.
+size_t dxh_floats(int M, int K, int splits) { return (size_t)splits * bgemm_slice_rows(M) * K; }
+int dx_splits(int M, int K, int cols, mmf_dtype dt) { return bgemm_splits(M, K, cols, planes_of(dt), kMaxSplits); }
+int dw_splits(int M, int K, int cols, mmf_dtype dt) { return bgemm_splits(cols, K, M, planes_of(dt), kMaxSplits); }
+size_t dw_floats(int M, int K, int cols, mmf_dtype dt) {
+  const int s = dw_splits(M, K, cols, dt);
+  return s > 1 ? (size_t)s * bgemm_slice_rows(cols) * K : 0;
+}
+
+// dx^ (+)= gamma G[:, col0 : col0 + cols] W over `splits` slices.
+mmf_status run_dx(const Grad& G, int col0, int cols, const void* wb, int M, int K, const float* gamma,
+                  const float* scale, int splits, bool accumulate, float* dxh, cudaStream_t s) {
+  BGemmArgs b = {};
+  b.dw = false;
+  b.a = static_cast<const char*>(G.g) + (size_t)col0 * 2;
+  b.lda = G.ld;
+  b.a_plane = G.plane_rows;
+  b.planes = G.planes;
+  b.b = wb;
+  b.ldb = K;
+  b.I = M;
+  b.J = K;
+  b.R = cols;
+  b.splits = splits;
+  b.slice_rows = bgemm_slice_rows(M);
+  b.out[0] = dxh;
+  b.out_f32 = true;
+  b.accumulate = accumulate;
+  b.gamma = gamma;
+  b.row_scale = G.over_s ? scale : nullptr;
+  MMF_CUDA(timed("bgemm_dx", s, [&] { return launch_bgemm_tc(b, status_word(), s); }), "gradient of the input");
+  return MMF_OK;
+}
+
+// dW[seg] = G^T Q / fold(inv_gamma[seg]) for nseg segments of N rows, their columns `pitch` apart.
+mmf_status run_dw(const Grad& G, int nseg, int N, int pitch, const void* qb, int M, int K,
+                  const float* const* inv_gamma, void* const* dw, float* part, mmf_dtype dt, cudaStream_t s) {
+  const int cols = nseg == 1 ? N : nseg * pitch;
+  BGemmArgs b = {};
+  b.dw = true;
+  b.a = G.g;
+  b.lda = G.ld;
+  b.a_plane = G.plane_rows;
+  b.planes = G.planes;
+  b.b = qb;
+  b.ldb = K;
+  b.I = cols;
+  b.J = K;
+  b.R = M;
+  b.splits = dw_splits(M, K, cols, dt);
+  b.slice_rows = bgemm_slice_rows(cols);
+  b.seg_rows = N;
+  b.seg_pitch = nseg == 1 ? b.slice_rows : pitch;
+  if (b.splits > 1) {
+    b.out[0] = part;
+    b.out_f32 = true;
+  } else {
+    for (int i = 0; i < nseg; ++i) {
+      b.out[i] = dw[i];
+      b.inv_gamma[i] = inv_gamma ? inv_gamma[i] : nullptr;
+    }
+    b.out_f32 = dt == MMF_F32;
+  }
+  MMF_CUDA(timed("bgemm_dw", s, [&] { return launch_bgemm_tc(b, status_word(), s); }), "gradient of the weights");
+  if (b.splits > 1) {
+    DwJoinArgs j = {};
+    j.part = part;
+    j.slices = b.splits;
+    j.slice_rows = b.slice_rows;
+    j.segs = nseg;
+    j.seg_pitch = nseg == 1 ? b.slice_rows : pitch;
+    j.N = N;
+    j.K = K;
+    for (int i = 0; i < nseg; ++i) {
+      j.out[i] = dw[i];
+      j.inv_gamma[i] = inv_gamma ? inv_gamma[i] : nullptr;
+    }
+    MMF_CUDA(timed("dw_join", s, [&] { return launch_dw_join(j, dt, s); }), "joining weight gradients");
+  }
+  return MMF_OK;
+}
+
+NormBackArgs norm_args(float* dxh, int slices, int M, int K, const mmf_act8& k, const float* gain, const void* x) {
+  NormBackArgs n = {};
+  n.dxh = dxh;
+  n.slices = slices;
+  n.slice_rows = bgemm_slice_rows(M);
+  n.M = M;
+  n.K = K;
+  n.q = k.q;
+  n.scale = k.scale;
+  n.rinv = k.rinv;
+  n.gain = gain;
+  n.x = x;
+  return n;
+}
+
+// dx and dgain from dx^.
+mmf_status run_norm(NormBackArgs n, const void* dres, void* dx, void* dgain, float* colpart, mmf_dtype dt,
+                    cudaStream_t s) {
+  n.dres = dres;
+  n.dx = dx;
+  if (dx != nullptr)
+    MMF_CUDA(timed("norm_back", s, [&] { return launch_norm_back(n, false, dt, s); }), "norm backward");
+  if (dgain != nullptr) {
+    ColSumArgs c = {};
+    c.M = n.M;
+    c.segs = 1;
+    c.N = c.pitch = n.K;
+    c.nb = n;
+    c.out[0] = dgain;
+    c.part = colpart;
+    MMF_CUDA(timed("colsum", s, [&] { return launch_colsum(c, ColSum::kGain, dt, s); }), "gain gradient");
+  }
+  return MMF_OK;
+}
+
+// ---------------------------------------------------------------- BitLinear
+
+// A caller's gradient [M, nlin, N] is the operand as it lies when its rows and
+// layers start on TMA's 16 bytes (and each layer's rows of dW on a 32-row
+// box); fp32 ones, and the others, are written to padded bf16 planes first.
+struct LinearPlan {
+  bool copy;
+  int pitch, cols, planes, rows;
+};
+LinearPlan linear_plan(int nlin, int N, int M, mmf_dtype dt) {
+  LinearPlan p;
+  p.copy = dt == MMF_F32 || N % 8 != 0 || (nlin > 1 && N % 32 != 0);
+  p.pitch = !p.copy ? N : pad(N, nlin > 1 ? 32 : 8);
+  p.cols = nlin * p.pitch;
+  p.planes = planes_of(dt);
+  p.rows = plane_rows_of(M, dt);
+  return p;
+}
+
+struct LinearWs {
+  void *wb, *qb, *gb;
+  float *dxh, *part, *colpart;
+};
+LinearWs carve_linear(Carver& c, int nlin, int N, int K, int M, mmf_dtype dt) {
+  const LinearPlan p = linear_plan(nlin, N, M, dt);
+  LinearWs w;
+  w.wb = c.take<char>((size_t)p.cols * K * 2);
+  w.qb = c.take<char>((size_t)M * K * 2);
+  w.gb = c.take<char>(p.copy ? (size_t)p.planes * p.rows * p.cols * 2 : 0);
+  w.dxh = c.take<float>(dxh_floats(M, K, dx_splits(M, K, p.pitch, dt)));
+  w.part = c.take<float>(dw_floats(M, K, nlin == 1 ? N : p.cols, dt));
+  w.colpart = c.take<float>(std::max(colsum_ws_floats(M, K), colsum_ws_floats(M, nlin * N)));
+  return w;
+}
+
+// The backward of nlin layers; also writes dx^ only (stat: into cmean) for the
+// GLU's down projection, whose norm's gradient the next kernel applies.
+mmf_status linear_backward(const mmf_tlinear* lins, int nlin, const mmf_act8& kept, const void* x, const void* dy,
+                           const void* dres, mmf_dtype dt, int M, const mmf_linear_grads& g, const LinearWs& w,
+                           float* cmean, cudaStream_t s) {
+  const int N = lins[0].N, K = lins[0].K;
+  const LinearPlan lp = linear_plan(nlin, N, M, dt);
+  const bool want_dxh = g.dx != nullptr || g.dgain != nullptr || cmean != nullptr;
+  bool want_dw = false;
+  void* dw[3] = {};
+  for (int i = 0; i < nlin; ++i) {
+    dw[i] = g.dw[i];
+    want_dw = want_dw || dw[i] != nullptr;
+  }
+  PrepArgs pa = {};
+  pa.M = M;
+  pa.scale = kept.scale;
+  pa.dy_dt = dt;
+  if (want_dxh) {
+    for (int i = 0; i < nlin; ++i) pa.w[i] = lins[i].packed;
+    pa.nseg = nlin;
+    pa.N = N;
+    pa.w_pitch = lp.pitch;
+    pa.K = K;
+    pa.wb = w.wb;
+  }
+  if (want_dw) {
+    pa.q = kept.q;
+    pa.qK = K;
+    pa.q_scaled = dt == MMF_BF16;   // fp32: the gradient's planes carry 1 / s instead
+    pa.qb = w.qb;
+  }
+  if (lp.copy && (want_dxh || want_dw)) {
+    pa.dy = dy;
+    pa.g_seg = nlin;
+    pa.g_N = N;
+    pa.g_pitch = lp.pitch;
+    pa.g_planes = lp.planes;
+    pa.g_rows = lp.rows;
+    pa.g_scaled = dt == MMF_F32;
+    pa.gb = w.gb;
+  }
+  if (want_dxh || want_dw)
+    MMF_CUDA(timed("train_prep", s, [&] { return launch_train_prep(pa, s); }), "operands");
+  Grad G;
+  G.g = lp.copy ? w.gb : dy;
+  G.ld = lp.cols;
+  G.plane_rows = lp.rows;
+  G.planes = lp.planes;
+  G.over_s = dt == MMF_F32;
+  mmf_status r = MMF_OK;
+  if (want_dxh) {
+    const int sp = dx_splits(M, K, lp.pitch, dt);
+    for (int i = 0; i < nlin && r == MMF_OK; ++i)
+      r = run_dx(G, i * lp.pitch, lp.pitch, static_cast<const char*>(w.wb) + (size_t)i * lp.pitch * K * 2, M, K,
+                 lins[i].gamma, kept.scale, sp, i > 0, w.dxh, s);
+    if (r != MMF_OK) return r;
+    NormBackArgs n = norm_args(w.dxh, sp, M, K, kept, lins[0].gain, x);
+    if (cmean != nullptr) {
+      n.cmean = cmean;
+      MMF_CUDA(timed("norm_stat", s, [&] { return launch_norm_back(n, true, dt, s); }), "norm backward");
+      n.slices = 1;
+    }
+    r = run_norm(n, dres, g.dx, g.dgain, w.colpart, dt, s);
+  }
+  if (r == MMF_OK && want_dw) r = run_dw(G, nlin, N, lp.pitch, w.qb, M, K, nullptr, dw, w.part, dt, s);
+  if (r != MMF_OK) return r;
+  bool want_db = false;
+  for (int i = 0; i < nlin; ++i) want_db = want_db || g.dbias[i] != nullptr;
+  if (want_db) {
+    ColSumArgs c = {};
+    c.src = dy;
+    c.M = M;
+    c.segs = nlin;
+    c.N = c.pitch = N;
+    for (int i = 0; i < nlin; ++i) c.out[i] = g.dbias[i];
+    c.part = w.colpart;
+    MMF_CUDA(timed("colsum", s, [&] { return launch_colsum(c, ColSum::kGrad, dt, s); }), "bias gradient");
+  }
+  return MMF_OK;
+}
+
+mmf_status check_grads(const mmf_linear_grads* g, int n, const char* what) {
+  if (g == nullptr) return fail(MMF_ERR_INVALID_ARG, "%s: null gradients", what);
+  mmf_status r = check_ptrs(what, {}, {g->dx, g->dgain});
+  for (int i = 0; i < n && r == MMF_OK; ++i) r = check_ptrs(what, {}, {g->dw[i], g->dbias[i]});
+  return r;
+}
+
+mmf_status zero_grads(const mmf_linear_grads& g, int n, int N, int K, mmf_dtype dt, cudaStream_t s) {
+  mmf_status r = zero(g.dgain, (size_t)K * elem_bytes(dt), s);
+  for (int i = 0; i < n && r == MMF_OK; ++i) {
+    r = zero(g.dw[i], (size_t)N * K * elem_bytes(dt), s);
+    if (r == MMF_OK) r = zero(g.dbias[i], (size_t)N * elem_bytes(dt), s);
+  }
+  return r;
+}
+
+}  // namespace
+
+extern "C" size_t mmf_bitlinear_train_ws_size(int32_t nlin, int32_t N, int32_t K) {
+  if (nlin < 1 || nlin > 3 || N < 0 || K < 0) return 0;
+  return round_up((size_t)nlin * N * K, 256) + 1024;
+}
+
+extern "C" mmf_status mmf_bitlinear_train(const mmf_tlinear* lins, int32_t nlin, const void* x, mmf_dtype dtype,
+                                          int32_t M, void* y, float eps, const mmf_act8* kept, void* ws,
+                                          size_t ws_bytes, void* stream) {
+  const char* what = "mmf_bitlinear_train";
+  mmf_status r = check_lins(lins, nlin, what);
+  if (r == MMF_OK) r = check_common(what, dtype, M);
+  if (r != MMF_OK) return r;
+  if (!(eps > 0.0f)) return fail(MMF_ERR_INVALID_ARG, "%s: eps must be > 0", what);
+  if (M == 0) return MMF_OK;
+  if ((r = check_ptrs(what, {x, y, ws}, {})) != MMF_OK || (r = check_kept(kept, what)) != MMF_OK) return r;
+  const int N = lins[0].N, K = lins[0].K;
+  if (ws_bytes < mmf_bitlinear_train_ws_size(nlin, N, K))
+    return fail(MMF_ERR_WORKSPACE, "%s: ws_bytes=%zu < %zu", what, ws_bytes, mmf_bitlinear_train_ws_size(nlin, N, K));
+  cudaStream_t s = as_stream(stream);
+  if ((r = quant_keep(x, dtype, M, K, lins[0].gain, eps, *kept, s)) != MMF_OK) return r;
+  const mmf_tlinear* segs[3] = {&lins[0], &lins[nlin > 1 ? 1 : 0], &lins[nlin > 2 ? 2 : 0]};
+  TGemmArgs a = gemm_args(segs, nlin, kept->q, kept->scale, kept->qsum, M, y, nlin * N, nullptr, nullptr);
+  if (M >= kUnpackMinTokens && tgemm_tc_supported(a, Epi::kStore)) {
+    Carver c(ws);
+    PrepArgs pa = {};
+    pa.dy_dt = dtype;
+    pa.nseg = nlin;
+    pa.N = pa.w_pitch = N;
+    pa.K = K;
+    for (int i = 0; i < nlin; ++i) {
+      uint8_t* u = c.take<uint8_t>((size_t)N * K);
+      pa.w[i] = lins[i].packed;
+      pa.wu[i] = a.wu[i] == nullptr ? u : nullptr;
+      if (a.wu[i] == nullptr) a.wu[i] = u;
+    }
+    MMF_CUDA(timed("train_prep", s, [&] { return launch_train_prep(pa, s); }), "one-byte codes");
+  }
+  MMF_CUDA(run_gemm(a, Epi::kStore, dtype, s, "train"), "contraction");
+  return MMF_OK;
+}
+
+extern "C" size_t mmf_bitlinear_backward_ws_size(int32_t nlin, int32_t N, int32_t K, int32_t M, mmf_dtype dtype) {
+  if (nlin < 1 || nlin > 3 || N < 0 || K < 0 || M < 0 || !dtype_ok(dtype)) return 0;
+  Carver c(nullptr);
+  carve_linear(c, nlin, N, K, M, dtype);
+  return c.off + 256;
+}
+
+extern "C" mmf_status mmf_bitlinear_backward(const mmf_tlinear* lins, int32_t nlin, const mmf_act8* kept,
+                                             const void* x, const void* dy, const void* dres, mmf_dtype dtype,
+                                             int32_t M, const mmf_linear_grads* grads, void* ws, size_t ws_bytes,
+                                             void* stream) {
+  const char* what = "mmf_bitlinear_backward";
+  mmf_status r = check_lins(lins, nlin, what);
+  if (r == MMF_OK) r = check_common(what, dtype, M);
+  if (r == MMF_OK) r = check_grads(grads, nlin, what);
+  if (r != MMF_OK) return r;
+  const int N = lins[0].N, K = lins[0].K;
+  cudaStream_t s = as_stream(stream);
+  if (M == 0) return zero_grads(*grads, nlin, N, K, dtype, s);
+  if ((r = check_ptrs(what, {dy, ws}, {x, dres})) != MMF_OK || (r = check_kept(kept, what)) != MMF_OK) return r;
+  const size_t need = mmf_bitlinear_backward_ws_size(nlin, N, K, M, dtype);
+  if (ws_bytes < need) return fail(MMF_ERR_WORKSPACE, "%s: ws_bytes=%zu < %zu", what, ws_bytes, need);
+  Carver c(ws);
+  const LinearWs w = carve_linear(c, nlin, N, K, M, dtype);
+  return linear_backward(lins, nlin, *kept, x, dy, dres, dtype, M, *grads, w, nullptr, s);
+}
+
+// ------------------------------------------------------------------ GLU
+
+extern "C" size_t mmf_glu_train_ws_size(int32_t M, int32_t d, int32_t I, mmf_dtype dtype) {
+  if (M < 0 || d < 0 || I < 0 || !dtype_ok(dtype)) return 0;
+  return round_up((size_t)M * I * elem_bytes(dtype), 256) + 3 * round_up((size_t)d * I, 256) + 256;
+}
+
+extern "C" mmf_status mmf_glu_train(const mmf_tlinear* gate, const mmf_tlinear* up, const mmf_tlinear* down,
+                                    const void* x, const void* residual, void* y, int32_t M, mmf_dtype dtype,
+                                    float eps, const mmf_act8* kept_x, const mmf_act8* kept_p, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  const char* what = "mmf_glu_train";
+  if (!gate) return fail(MMF_ERR_INVALID_ARG, "%s: null gate", what);
+  const int d = gate->K, I = gate->N;
+  mmf_status r = check_glu(gate, up, down, d);
+  if (r == MMF_OK) r = check_common(what, dtype, M);
+  if (r != MMF_OK) return r;
+  if (!(eps > 0.0f)) return fail(MMF_ERR_INVALID_ARG, "%s: eps must be > 0", what);
+  if (M == 0) return MMF_OK;
+  if ((r = check_ptrs(what, {x, y, ws}, {residual})) != MMF_OK || (r = check_kept(kept_x, what)) != MMF_OK ||
+      (r = check_kept(kept_p, what)) != MMF_OK)
+    return r;
+  const size_t need = mmf_glu_train_ws_size(M, d, I, dtype);
+  if (ws_bytes < need) return fail(MMF_ERR_WORKSPACE, "%s: ws_bytes=%zu < %zu", what, ws_bytes, need);
+  cudaStream_t s = as_stream(stream);
+  Carver c(ws);
+  void* p = c.take<char>((size_t)M * I * elem_bytes(dtype));
+  const mmf_tlinear* gu[2] = {gate, up};
+  const mmf_tlinear* dn[1] = {down};
+  TGemmArgs a = gemm_args(gu, 2, kept_x->q, kept_x->scale, kept_x->qsum, M, p, I, nullptr, nullptr);
+  TGemmArgs b = gemm_args(dn, 1, kept_p->q, kept_p->scale, kept_p->qsum, M, y, d, residual, nullptr);
+  if (M >= kUnpackMinTokens) {
+    const mmf_tlinear* l[3] = {gate, up, down};
+    const uint8_t* wu[3];
+    for (int i = 0; i < 3; ++i) {
+      uint8_t* u = c.take<uint8_t>((size_t)d * I);
+      wu[i] = l[i]->codes != nullptr ? l[i]->codes : u;
+      if (l[i]->codes == nullptr)
+        MMF_CUDA(timed("unpack_codes", s, [&] { return launch_unpack_codes(l[i]->packed, l[i]->N, l[i]->K, u, s); }),
+                 "one-byte codes");
+    }
+    a.wu[0] = wu[0];
+    a.wu[1] = wu[1];
+    b.wu[0] = wu[2];
+  }
+  if ((r = quant_keep(x, dtype, M, d, gate->gain, eps, *kept_x, s)) != MMF_OK) return r;
+  MMF_CUDA(run_gemm(a, Epi::kGlu, dtype, s, "gate_up"), "contraction");
+  if ((r = quant_keep(p, dtype, M, I, down->gain, eps, *kept_p, s)) != MMF_OK) return r;
+  MMF_CUDA(run_gemm(b, Epi::kStore, dtype, s, "down"), "contraction");
+  return MMF_OK;
+}
+
+namespace {
+
+struct GluWs {
+  LinearWs down;
+  uint8_t *wu_gate, *wu_up;
+  void *wb, *qb, *dz;
+  float *cmean, *dxh, *part, *colpart;
+};
+// The down projection's scratch and the gate | up one live at different times,
+// except the down projection's dx^ (read by the recompute) - they are carved
+// one behind the other all the same.
+GluWs carve_glu(Carver& c, int M, int d, int I, mmf_dtype dt) {
+  const int Ip = pad(I, 32), rows = plane_rows_of(M, dt);
+  GluWs w;
+  w.down = carve_linear(c, 1, d, I, M, dt);
+  w.wu_gate = c.take<uint8_t>((size_t)I * d);
+  w.wu_up = c.take<uint8_t>((size_t)I * d);
+  w.wb = c.take<char>((size_t)2 * Ip * d * 2);
+  w.qb = c.take<char>((size_t)M * d * 2);
+  w.dz = c.take<char>((size_t)planes_of(dt) * rows * 2 * Ip * 2);
+  w.cmean = c.take<float>(M);
+  w.dxh = c.take<float>(dxh_floats(M, d, dx_splits(M, d, 2 * Ip, dt)));
+  w.part = c.take<float>(dw_floats(M, d, 2 * Ip, dt));
+  w.colpart = c.take<float>(std::max(colsum_ws_floats(M, d), colsum_ws_floats(M, 2 * Ip)));
+  return w;
+}
+
+}  // namespace
+
+extern "C" size_t mmf_glu_backward_ws_size(int32_t M, int32_t d, int32_t I, mmf_dtype dtype) {
+  if (M < 0 || d < 0 || I < 0 || !dtype_ok(dtype)) return 0;
+  Carver c(nullptr);
+  carve_glu(c, M, d, I, dtype);
+  return c.off + 256;
+}
+
+extern "C" mmf_status mmf_glu_backward(const mmf_tlinear* gate, const mmf_tlinear* up, const mmf_tlinear* down,
+                                       const mmf_act8* kept_x, const mmf_act8* kept_p, const void* x, const void* dy,
+                                       const void* dres, mmf_dtype dtype, int32_t M, const mmf_glu_grads* grads,
+                                       void* ws, size_t ws_bytes, void* stream) {
+  const char* what = "mmf_glu_backward";
+  if (!gate) return fail(MMF_ERR_INVALID_ARG, "%s: null gate", what);
+  const int d = gate->K, I = gate->N;
+  mmf_status r = check_glu(gate, up, down, d);
+  if (r == MMF_OK) r = check_common(what, dtype, M);
+  if (r != MMF_OK) return r;
+  if (grads == nullptr) return fail(MMF_ERR_INVALID_ARG, "%s: null gradients", what);
+  const mmf_glu_grads& g = *grads;
+  r = check_ptrs(what, {}, {g.dx, g.dw_gate, g.dw_up, g.dw_down, g.dgain, g.dgain_down, g.dbias_gate, g.dbias_up,
+                            g.dbias_down});
+  if (r != MMF_OK) return r;
+  cudaStream_t s = as_stream(stream);
+  mmf_linear_grads gd = {nullptr, {g.dw_down, nullptr, nullptr}, g.dgain_down, {g.dbias_down, nullptr, nullptr}};
+  const mmf_linear_grads gx = {g.dx, {g.dw_gate, g.dw_up, nullptr}, g.dgain, {g.dbias_gate, g.dbias_up, nullptr}};
+  if (M == 0) {
+    r = zero_grads(gd, 1, d, I, dtype, s);
+    return r == MMF_OK ? zero_grads(gx, 2, I, d, dtype, s) : r;
+  }
+  if ((r = check_ptrs(what, {dy, ws}, {x, dres})) != MMF_OK || (r = check_kept(kept_x, what)) != MMF_OK ||
+      (r = check_kept(kept_p, what)) != MMF_OK)
+    return r;
+  const size_t need = mmf_glu_backward_ws_size(M, d, I, dtype);
+  if (ws_bytes < need) return fail(MMF_ERR_WORKSPACE, "%s: ws_bytes=%zu < %zu", what, ws_bytes, need);
+  Carver c(ws);
+  const GluWs w = carve_glu(c, M, d, I, dtype);
+
+  const bool want_dxh = gx.dx != nullptr || gx.dgain != nullptr;
+  const bool want_dw = gx.dw[0] != nullptr || gx.dw[1] != nullptr;
+  const bool want_db = gx.dbias[0] != nullptr || gx.dbias[1] != nullptr;
+  const bool inner = want_dxh || want_dw || want_db;   // anything behind the product
+  // 1. the down projection: dW, its gain's and bias's gradient, dx^ of p and its row means
+  r = linear_backward(down, 1, *kept_p, nullptr, dy, nullptr, dtype, M, gd, w.down, inner ? w.cmean : nullptr, s);
+  if (r != MMF_OK || !inner) return r;
+  // 2. u, v again; du, dv over the row's scale (and times gamma, so that gate and up add up in one product)
+  const int Ip = pad(I, 32), rows = plane_rows_of(M, dtype), planes = planes_of(dtype);
+  const mmf_tlinear* gu[2] = {gate, up};
+  PrepArgs pa = {};
+  pa.M = M;
+  pa.scale = kept_x->scale;
+  pa.dy_dt = dtype;
+  pa.nseg = 2;
+  pa.N = I;
+  pa.w_pitch = Ip;
+  pa.K = d;
+  pa.wb = want_dxh ? w.wb : nullptr;
+  for (int i = 0; i < 2; ++i) {
+    pa.w[i] = gu[i]->packed;
+    pa.wu[i] = gu[i]->codes == nullptr ? (i == 0 ? w.wu_gate : w.wu_up) : nullptr;
+  }
+  if (want_dw) {
+    pa.q = kept_x->q;
+    pa.qK = d;
+    pa.qb = w.qb;
+  }
+  MMF_CUDA(timed("train_prep", s, [&] { return launch_train_prep(pa, s); }), "operands");
+  TGemmArgs a = gemm_args(gu, 2, kept_x->q, kept_x->scale, kept_x->qsum, M, w.dz, 2 * Ip, nullptr, nullptr);
+  if (a.wu[0] == nullptr) a.wu[0] = w.wu_gate;
+  if (a.wu[1] == nullptr) a.wu[1] = w.wu_up;
+  TrainEpi t = {};
+  t.dxh = w.down.dxh;
+  t.qp = kept_p->q;
+  t.sp = kept_p->scale;
+  t.rp = kept_p->rinv;
+  t.cp = w.cmean;
+  t.gain_p = down->gain;
+  t.plane_rows = rows;
+  t.plane_cols = Ip;
+  MMF_CUDA(timed("tgemm_tc:glu_back", s, [&] { return launch_tgemm_train(a, t, Epi::kGluBwd, dtype, status_word(), s); }),
+           "gradient of the product");
+  // 3. gate and up
+  Grad G;
+  G.g = w.dz;
+  G.ld = 2 * Ip;
+  G.plane_rows = rows;
+  G.planes = planes;
+  G.over_s = true;
+  const float* gam[3] = {gate->gamma, up->gamma, nullptr};
+  if (want_dxh) {
+    const int sp = dx_splits(M, d, 2 * Ip, dtype);
+    r = run_dx(G, 0, 2 * Ip, w.wb, M, d, nullptr, kept_x->scale, sp, false, w.dxh, s);
+    if (r != MMF_OK) return r;
+    r = run_norm(norm_args(w.dxh, sp, M, d, *kept_x, gate->gain, x), dres, gx.dx, gx.dgain, w.colpart, dtype, s);
+    if (r != MMF_OK) return r;
+  }
+  if (want_dw && (r = run_dw(G, 2, I, Ip, w.qb, M, d, gam, gx.dw, w.part, dtype, s)) != MMF_OK) return r;
+  if (want_db) {
+    ColSumArgs cs = {};
+    cs.src = w.dz;
+    cs.M = M;
+    cs.segs = 2;
+    cs.N = I;
+    cs.pitch = Ip;
+    cs.planes = planes;
+    cs.plane_rows = rows;
+    cs.scale = kept_x->scale;
+    for (int i = 0; i < 2; ++i) {
+      cs.inv_gamma[i] = gam[i];
+      cs.out[i] = gx.dbias[i];
+    }
+    cs.part = w.colpart;
+    MMF_CUDA(timed("colsum", s, [&] { return launch_colsum(cs, ColSum::kPlanes, dtype, s); }), "bias gradients");
+  }
+  return MMF_OK;
+}
+
+// ------------------------------------------------------------------ LM head loss
+
+namespace {
+
+int loss_slots(int V) { return ceil_div(V, 128); }
+
+struct LossWs {
+  uint8_t* wu;
+  float2* part;
+  float *zlabel, *token;
+};
+LossWs carve_loss(Carver& c, int M, int V, int K) {
+  LossWs w;
+  w.wu = c.take<uint8_t>((size_t)V * K);
+  w.part = c.take<float2>((size_t)loss_slots(V) * M);
+  w.zlabel = c.take<float>(M);
+  w.token = c.take<float>(M);
+  return w;
+}
+
+// Equal pieces of the vocabulary, whole 256-column tiles, of at most
+// kPieceBytes of gradient (but no fewer than 1024 columns).
+int piece_cols(int M, int V, mmf_dtype dt) {
+  const size_t col = (size_t)planes_of(dt) * plane_rows_of(M, dt) * 2;
+  const int most = (int)std::max<size_t>(1024, std::min<size_t>(kPieceBytes / std::max<size_t>(col, 1) / 256 * 256, 1u << 28));
+  const int pieces = ceil_div(V, most);
+  return pad(ceil_div(V, pieces), 256);
+}
+
+struct HeadWs {
+  uint8_t* wu;
+  void *wb, *qb, *dz;
+  float *dxh, *part, *colpart;
+};
+HeadWs carve_head(Carver& c, int M, int V, int K, mmf_dtype dt) {
+  const int vp = std::min(piece_cols(M, V, dt), pad(V, 32));
+  HeadWs w;
+  w.wu = c.take<uint8_t>((size_t)V * K);
+  w.wb = c.take<char>((size_t)V * K * 2);
+  w.qb = c.take<char>((size_t)M * K * 2);
+  w.dz = c.take<char>((size_t)planes_of(dt) * plane_rows_of(M, dt) * vp * 2);
+  w.dxh = c.take<float>(dxh_floats(M, K, dx_splits(M, K, std::min(vp, V), dt)));
+  size_t part = 0, col = colsum_ws_floats(M, K);
+  for (int v0 = 0; v0 < V; v0 += vp) {   // the last piece may be cut into more slices
+    part = std::max(part, dw_floats(M, K, std::min(vp, V - v0), dt));
+  }
+  col = std::max(col, colsum_ws_floats(M, vp));
+  w.part = c.take<float>(part);
+  w.colpart = c.take<float>(col);
+  return w;
+}
+
+bool reduction_ok(mmf_reduction r) { return r == MMF_REDUCE_NONE || r == MMF_REDUCE_SUM || r == MMF_REDUCE_MEAN; }
+
+}  // namespace
+
+extern "C" size_t mmf_head_loss_ws_size(int32_t M, int32_t V, int32_t K) {
+  if (M < 0 || V < 0 || K < 0) return 0;
+  Carver c(nullptr);
+  carve_loss(c, M, V, K);
+  return c.off + 256;
+}
+
+extern "C" mmf_status mmf_head_loss(const mmf_tlinear* head, const void* x, mmf_dtype dtype, int32_t M,
+                                    const int32_t* labels, int32_t ignore_index, mmf_reduction reduction, float eps,
+                                    float* loss, const mmf_act8* kept, float* lse, float* count, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  const char* what = "mmf_head_loss";
+  mmf_status r = check_lins(head, 1, what);
+  if (r == MMF_OK) r = check_common(what, dtype, M);
+  if (r != MMF_OK) return r;
+  if (!reduction_ok(reduction)) return fail(MMF_ERR_INVALID_ARG, "%s: bad reduction %d", what, (int)reduction);
+  if (!(eps > 0.0f)) return fail(MMF_ERR_INVALID_ARG, "%s: eps must be > 0", what);
+  const bool reduce = reduction != MMF_REDUCE_NONE;
+  cudaStream_t s = as_stream(stream);
+  if (reduce && (r = check_ptrs(what, {loss, count}, {})) != MMF_OK) return r;
+  if (M == 0) return reduce ? zero(loss, sizeof(float), s) : MMF_OK;
+  if ((r = check_ptrs(what, {x, labels, loss, lse, ws}, {})) != MMF_OK || (r = check_kept(kept, what)) != MMF_OK)
+    return r;
+  const int V = head->N, K = head->K;
+  const size_t need = mmf_head_loss_ws_size(M, V, K);
+  if (ws_bytes < need) return fail(MMF_ERR_WORKSPACE, "%s: ws_bytes=%zu < %zu", what, ws_bytes, need);
+  Carver c(ws);
+  const LossWs w = carve_loss(c, M, V, K);
+  if ((r = quant_keep(x, dtype, M, K, head->gain, eps, *kept, s)) != MMF_OK) return r;
+  if (head->codes == nullptr)
+    MMF_CUDA(timed("unpack_codes", s, [&] { return launch_unpack_codes(head->packed, V, K, w.wu, s); }),
+             "one-byte codes");
+  const mmf_tlinear* seg[1] = {head};
+  TGemmArgs a = gemm_args(seg, 1, kept->q, kept->scale, kept->qsum, M, nullptr, 0, nullptr, nullptr);
+  for (auto& u : a.wu) u = head->codes != nullptr ? head->codes : w.wu;
+  TrainEpi t = {};
+  t.labels = labels;
+  t.vocab = V;
+  t.part = w.part;
+  t.zlabel = w.zlabel;
+  MMF_CUDA(timed("tgemm_tc:lse", s, [&] { return launch_tgemm_train(a, t, Epi::kLse, dtype, status_word(), s); }),
+           "logits");
+  LossArgs l = {};
+  l.part = w.part;
+  l.slots = loss_slots(V);
+  l.M = M;
+  l.vocab = V;
+  l.zlabel = w.zlabel;
+  l.labels = labels;
+  l.ignore_index = ignore_index;
+  l.lse = lse;
+  l.token = reduce ? w.token : loss;
+  l.reduction = reduction;
+  l.loss = loss;
+  l.count = count;
+  MMF_CUDA(timed("loss_join", s, [&] { return launch_loss_join(l, status_word(), s); }), "loss");
+  return MMF_OK;
+}
+
+extern "C" size_t mmf_head_loss_backward_ws_size(int32_t M, int32_t V, int32_t K, mmf_dtype dtype) {
+  if (M < 0 || V < 1 || K < 0 || !dtype_ok(dtype)) return 0;
+  Carver c(nullptr);
+  carve_head(c, M, V, K, dtype);
+  return c.off + 256;
+}
+
+extern "C" mmf_status mmf_head_loss_backward(const mmf_tlinear* head, const mmf_act8* kept, const void* x,
+                                             const int32_t* labels, const float* lse, const float* count,
+                                             const float* dloss, int32_t ignore_index, mmf_reduction reduction,
+                                             mmf_dtype dtype, int32_t M, const mmf_linear_grads* grads, void* ws,
+                                             size_t ws_bytes, void* stream) {
+  const char* what = "mmf_head_loss_backward";
+  mmf_status r = check_lins(head, 1, what);
+  if (r == MMF_OK) r = check_common(what, dtype, M);
+  if (r == MMF_OK) r = check_grads(grads, 1, what);
+  if (r != MMF_OK) return r;
+  if (!reduction_ok(reduction)) return fail(MMF_ERR_INVALID_ARG, "%s: bad reduction %d", what, (int)reduction);
+  const int V = head->N, K = head->K;
+  cudaStream_t s = as_stream(stream);
+  if (M == 0) return zero_grads(*grads, 1, V, K, dtype, s);
+  if ((r = check_ptrs(what, {labels, lse, ws}, {x, dloss})) != MMF_OK || (r = check_kept(kept, what)) != MMF_OK)
+    return r;
+  if (reduction == MMF_REDUCE_MEAN && count == nullptr) return fail(MMF_ERR_INVALID_ARG, "%s: null count", what);
+  const size_t need = mmf_head_loss_backward_ws_size(M, V, K, dtype);
+  if (ws_bytes < need) return fail(MMF_ERR_WORKSPACE, "%s: ws_bytes=%zu < %zu", what, ws_bytes, need);
+  Carver c(ws);
+  const HeadWs w = carve_head(c, M, V, K, dtype);
+  const int vp = std::min(piece_cols(M, V, dtype), pad(V, 32)), rows = plane_rows_of(M, dtype);
+  const bool want_dxh = grads->dx != nullptr || grads->dgain != nullptr, want_dw = grads->dw[0] != nullptr;
+  const bool want_db = grads->dbias[0] != nullptr;
+  if (!want_dxh && !want_dw && !want_db) return MMF_OK;
+  PrepArgs pa = {};
+  pa.M = M;
+  pa.scale = kept->scale;
+  pa.dy_dt = dtype;
+  pa.w[0] = head->packed;
+  pa.nseg = want_dxh || head->codes == nullptr ? 1 : 0;
+  pa.N = pa.w_pitch = V;
+  pa.K = K;
+  pa.wb = want_dxh ? w.wb : nullptr;
+  pa.wu[0] = head->codes == nullptr ? w.wu : nullptr;
+  if (want_dw) {
+    pa.q = kept->q;
+    pa.qK = K;
+    pa.qb = w.qb;
+  }
+  MMF_CUDA(timed("train_prep", s, [&] { return launch_train_prep(pa, s); }), "operands");
+  const uint8_t* wu = head->codes != nullptr ? head->codes : w.wu;
+  const mmf_tlinear* seg[1] = {head};
+  const int sp = dx_splits(M, K, std::min(vp, V), dtype);
+  for (int v0 = 0; v0 < V; v0 += vp) {
+    const int n = std::min(vp, V - v0);
+    TGemmArgs a = gemm_args(seg, 1, kept->q, kept->scale, kept->qsum, M, w.dz, vp, nullptr, nullptr);
+    a.N = n;
+    for (auto& u : a.wu) u = wu + (size_t)v0 * K;
+    if (head->bias != nullptr)
+      for (auto& b : a.bias) b = head->bias + v0;
+    TrainEpi t = {};
+    t.labels = labels;
+    t.col0 = v0;
+    t.vocab = V;
+    t.lse = lse;
+    t.dloss = dloss;
+    t.count = reduction == MMF_REDUCE_MEAN ? count : nullptr;
+    t.per_token = reduction == MMF_REDUCE_NONE;
+    t.ignore_index = ignore_index;
+    t.plane_rows = rows;
+    t.plane_cols = pad(n, 32);
+    MMF_CUDA(timed("tgemm_tc:dz", s, [&] { return launch_tgemm_train(a, t, Epi::kDz, dtype, status_word(), s); }),
+             "gradient of the logits");
+    Grad G;
+    G.g = w.dz;
+    G.ld = vp;
+    G.plane_rows = rows;
+    G.planes = planes_of(dtype);
+    G.over_s = true;
+    if (want_dxh) {
+      // the last piece may have fewer reduction steps than slices: it adds to the first ones only
+      const int steps = G.planes * ceil_div(n, 64);
+      r = run_dx(G, 0, n, static_cast<const char*>(w.wb) + (size_t)v0 * K * 2, M, K, head->gamma, kept->scale,
+                 std::min(sp, steps), v0 > 0, w.dxh, s);
+      if (r != MMF_OK) return r;
+    }
+    if (want_dw) {
+      void* dw[3] = {static_cast<char*>(grads->dw[0]) + (size_t)v0 * K * elem_bytes(dtype), nullptr, nullptr};
+      if ((r = run_dw(G, 1, n, n, w.qb, M, K, nullptr, dw, w.part, dtype, s)) != MMF_OK) return r;
+    }
+    if (want_db) {
+      ColSumArgs cs = {};
+      cs.src = w.dz;
+      cs.M = M;
+      cs.segs = 1;
+      cs.N = n;
+      cs.pitch = vp;
+      cs.planes = G.planes;
+      cs.plane_rows = rows;
+      cs.scale = kept->scale;
+      cs.out[0] = static_cast<char*>(grads->dbias[0]) + (size_t)v0 * elem_bytes(dtype);
+      cs.part = w.colpart;
+      MMF_CUDA(timed("colsum", s, [&] { return launch_colsum(cs, ColSum::kPlanes, dtype, s); }), "bias gradient");
+    }
+  }
+  if (!want_dxh) return MMF_OK;
+  return run_norm(norm_args(w.dxh, sp, M, K, *kept, head->gain, x), nullptr, grads->dx, grads->dgain, w.colpart, dtype,
+                  s);
+}

@@ -1,0 +1,416 @@
+"""The training operators against their definitions in 64 bits, and as they are used together.
+
+Tolerances (normwise, |got - want|_2 / |want|_2) are counted in rounding steps: a
+bf16 result carries half a step of its own, at most 2^-8 of each value, and at
+most one operand rounded to bf16 on the way (xt for a caller's gradient, dz / s,
+du / s, dv / s): the two together stay below 2 * 2^-8. fp32 results: products of
+24-bit operands summed in fp32; a sum of n terms in blocks of 16 loses at most
+one step (2^-23) of the running sum per block, and fewer than 256 blocks follow
+one another in these cases: 256 * 2^-23 = 2^-15.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+
+pytestmark = pytest.mark.gpu
+
+mmf = pytest.importorskip("ternary_weight_matmul_fusedbitlinear_b200")
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+TOL = {"bf16": 2 * 2.0 ** -8, "f32": 2.0 ** -15}
+EPS = 1e-6
+
+
+def rel(got, want):
+    got = got.double()
+    n = want.norm()
+    return float((got - want).norm() / n) if n > 0 else float(got.norm())
+
+
+def near(got, want, dtype, what):
+    assert got.shape == want.shape, what
+    assert torch.isfinite(got).all(), what
+    e = rel(got, want)
+    assert e <= TOL[dtype], f"{what}: {e:.2e} > {TOL[dtype]:.2e}"
+
+
+class Layer:
+    """A ternary layer and its codes in fp64."""
+
+    def __init__(self, g, n, k, gain=None, bias=False, std=0.02):
+        W = torch.randn(n, k, generator=g, device="cuda") * std
+        b = torch.randn(n, generator=g, device="cuda") * 0.1 if bias else None
+        self.lin = mmf.quantize_weights(W, gain, b)
+        codes = mmf.unpack_codes(self.lin).codes
+        self.w = codes.double() - 1
+        self.gamma = self.lin.gamma[0].double()
+        self.gain, self.bias = gain, b
+
+
+def make(seed, m, k, n, dtype, gain=False, bias=False, layers=1, std=0.02, zero_gain=False):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    gn = 1 + 0.2 * torch.randn(k, generator=g, device="cuda") if gain else None
+    if zero_gain:
+        gn[:: 7] = 0.0
+    ls = [Layer(g, n, k, gn, bias, std) for _ in range(layers)]
+    x = torch.randn(m, k, generator=g, device="cuda").to(DT[dtype])
+    return g, ls, x
+
+
+def kept64(kept):
+    return kept.q.double() / kept.scale.double()[:, None]
+
+
+def back64(layers, kept, dys, x=None):
+    """dx, dws, dgain, dbias of BitLinear layers on one input from the formulas, in fp64."""
+    xt, rinv = kept64(kept), kept.rinv.double()[:, None]
+    gain = layers[0].gain
+    gd = torch.ones(xt.shape[1], dtype=torch.float64, device="cuda") if gain is None else gain.double()
+    dxh = sum(l.gamma * (d @ l.w) for l, d in zip(layers, dys))
+    if x is None:
+        n = torch.where(gd == 0, torch.zeros_like(xt), xt / gd)
+        c = (dxh * xt).mean(1, keepdim=True)
+    else:
+        n = x.double() * rinv
+        c = (dxh * n * gd).mean(1, keepdim=True)
+    return rinv * (gd * dxh - n * c), [d.t() @ xt for d in dys], (dxh * n).sum(0), [d.sum(0) for d in dys]
+
+
+def through(l, kept):
+    y = l.gamma * (kept64(kept) @ l.w.t())
+    return y if l.bias is None else y + l.bias.double()
+
+
+# ---------------------------------------------------------------- BitLinear
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,k,n,layers", [(1, 256, 256, 1), (5, 16, 3, 1), (130, 272, 777, 1), (257, 1024, 129, 2),
+                                          (64, 512, 96, 3), (300, 80, 100, 3), (1537, 640, 320, 1),
+                                          (2049, 256, 512, 3)])
+@pytest.mark.parametrize("gain,bias,keep_x", [(False, False, False), (True, True, False), (True, False, True)])
+def test_bitlinear_train_and_backward(m, k, n, layers, dtype, gain, bias, keep_x):
+    g, ls, x = make(m + k + n, m, k, n, dtype, gain, bias, layers)
+    lins = [l.lin for l in ls]
+    y, kept = mmf.bitlinear_train(lins, x)
+    for i, lin in enumerate(lins):   # the same codes and outputs as the inference call
+        yi, q, s, _ = mmf.bitlinear(lin, x, debug=True)
+        assert torch.equal(q, kept.q) and torch.equal(s, kept.scale)
+        near(y[:, i], through(ls[i], kept), dtype, f"y{i}")
+        assert rel(y[:, i], yi.double()) <= 2.0 ** -8
+    assert torch.equal(kept.qsum, kept.q.sum(1, dtype=torch.int32))
+    ms = (x.double() ** 2).mean(1)
+    assert torch.allclose(kept.rinv.double(), (ms + EPS).rsqrt(), rtol=2.0 ** -21)
+    dy = torch.randn(m, layers, n, generator=g, device="cuda").to(DT[dtype])
+    got = mmf.bitlinear_backward(lins, kept, dy, x=x if keep_x else None)
+    dx, dws, dgain, dbias = back64(ls, kept, [dy[:, i].double() for i in range(layers)], x if keep_x else None)
+    near(got.dx, dx, dtype, "dx")
+    for i in range(layers):
+        near(got.dw[i], dws[i], dtype, f"dw{i}")
+        if bias:
+            near(got.dbias[i], dbias[i], dtype, f"dbias{i}")
+    assert (got.dgain is None) == (not gain)
+    if gain:
+        near(got.dgain, dgain, dtype, "dgain")
+    mmf.check()
+
+
+def test_backward_order_does_not_change_from_run_to_run():
+    g, ls, x = make(3, 300, 512, 640, "bf16", True, True)
+    _, kept = mmf.bitlinear_train(ls[0].lin, x)
+    dy = torch.randn(300, 640, generator=g, device="cuda").bfloat16()
+    a, b = (mmf.bitlinear_backward(ls[0].lin, kept, dy) for _ in range(2))
+    for u, v in zip((a.dx, a.dw[0], a.dgain, a.dbias[0]), (b.dx, b.dw[0], b.dgain, b.dbias[0])):
+        assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_zero_rows_zero_gains_and_a_residual(dtype):
+    g, ls, x = make(11, 70, 128, 144, dtype, gain=True, zero_gain=True)
+    x[::9] = 0
+    lin = ls[0].lin
+    _, kept = mmf.bitlinear_train(lin, x)
+    dy = torch.randn(70, 144, generator=g, device="cuda").to(DT[dtype])
+    dres = torch.randn(70, 128, generator=g, device="cuda").to(DT[dtype]) * 30
+    for keep in (None, x):
+        dx, dws, dgain, _ = back64(ls, kept, [dy.double()], keep)
+        got = mmf.bitlinear_backward(lin, kept, dy, x=keep, dres=dres)
+        near(got.dx, dx + dres.double(), dtype, "dx")
+        near(got.dgain, dgain, dtype, "dgain")
+        near(got.dw[0], dws[0], dtype, "dw")
+
+
+def test_empty_batch():
+    _, ls, _ = make(1, 1, 64, 48, "bf16", True, True)
+    lin = ls[0].lin
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    y, kept = mmf.bitlinear_train(lin, x)
+    assert y.shape == (0, 48)
+    got = mmf.bitlinear_backward(lin, kept, y)
+    for t in (got.dw[0], got.dgain, got.dbias[0]):
+        assert torch.count_nonzero(t) == 0
+    loss, hk = mmf.head_loss(lin, x, torch.empty(0, dtype=torch.int32, device="cuda"))
+    assert float(loss) == 0.0
+    assert mmf.head_loss_backward(lin, hk, torch.empty(0, dtype=torch.int32, device="cuda")).dx.shape == (0, 64)
+
+
+def test_gradient_of_the_input_against_differences():
+    """dx by central differences of the forward with its roundings left out: y(x) = gamma xhat(x) W^T."""
+    g, ls, x = make(21, 3, 64, 32, "f32", gain=True)
+    lin = ls[0].lin
+    _, kept = mmf.bitlinear_train(lin, x)
+    dy = torch.randn(3, 32, generator=g, device="cuda")
+    dx = mmf.bitlinear_backward(lin, kept, dy, x=x).dx.double()
+
+    def f(v):
+        n = v * (v.square().mean(1, keepdim=True) + EPS).rsqrt()
+        return (ls[0].gamma * (n * ls[0].gain.double()) @ ls[0].w.t() * dy.double()).sum(1)
+
+    xd, h = x.double(), 1e-5
+    want = torch.empty_like(xd)
+    for k in range(64):
+        e = torch.zeros_like(xd)
+        e[:, k] = h
+        want[:, k] = (f(xd + e) - f(xd - e)) / (2 * h)
+    # central differences: h^2 |f'''| / 6 ~ 1e-10, cancellation 2^-52 / h ~ 2e-11 of |f| ~ 10
+    assert rel(dx, want) <= TOL["f32"]
+
+
+# ---------------------------------------------------------------- GLU
+
+def glu64(gate, up, down, kept, dy, x=None):
+    kx, kp = kept
+    u, v = through(gate, kx), through(up, kx)
+    sg = torch.sigmoid(u)
+    dp, dwd, dgd, dbd = back64([down], kp, [dy.double()])
+    du, dv = dp * v * sg * (1 + u * (1 - sg)), dp * u * sg
+    dx, dws, dg, db = back64([gate, up], kx, [du, dv], x)
+    return dx, dws + dwd, [dg, dgd], db + dbd
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,d,inner", [(1, 256, 768), (7, 16, 16), (130, 272, 400), (513, 128, 1040), (1100, 320, 208)])
+@pytest.mark.parametrize("gain,bias,keep_x", [(False, False, False), (True, True, False), (True, False, True)])
+def test_glu_train_and_backward(m, d, inner, dtype, gain, bias, keep_x):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m + d)
+    gx = 1 + 0.2 * torch.randn(d, generator=g, device="cuda") if gain else None
+    gp = 1 + 0.2 * torch.randn(inner, generator=g, device="cuda") if gain else None
+    gate, up = Layer(g, inner, d, gx, bias, 0.1), Layer(g, inner, d, gx, bias, 0.1)
+    down = Layer(g, d, inner, gp, bias)
+    x = torch.randn(m, d, generator=g, device="cuda").to(DT[dtype])
+    res = torch.randn(m, d, generator=g, device="cuda").to(DT[dtype])
+    y, kept = mmf.glu_train(gate.lin, up.lin, down.lin, x, residual=res)
+    near(y, through(down, kept[1]) + res.double(), dtype, "y")
+    p = torch.nn.functional.silu(through(gate, kept[0])) * through(up, kept[0])
+    step = float((1.0 / kept[1].scale.double()).max())   # codes of p: half a step, and what p's own storage moves
+    n = p * kept[1].rinv.double()[:, None] * (1 if gp is None else gp.double())
+    assert float((kept64(kept[1]) - n).abs().max()) <= 0.5 * step + 2.0 ** -7 * float(n.abs().max())
+    dy = torch.randn(m, d, generator=g, device="cuda").to(DT[dtype])
+    got = mmf.glu_backward(gate.lin, up.lin, down.lin, kept, dy, x=x if keep_x else None, dres=dy)
+    dx, dws, dgs, dbs = glu64(gate, up, down, kept, dy, x if keep_x else None)
+    near(got.dx, dx + dy.double(), dtype, "dx")
+    for i, name in enumerate(("gate", "up", "down")):
+        near(got.dw[i], dws[i], dtype, f"dw {name}")
+        if bias:
+            near(got.dbias[i], dbs[i], dtype, f"dbias {name}")
+    if gain:
+        near(got.dgain[0], dgs[0], dtype, "dgain")
+        near(got.dgain[1], dgs[1], dtype, "dgain down")
+    mmf.check()
+
+
+# ---------------------------------------------------------------- loss
+
+def loss64(head, kept, labels, reduction, ignore=-100):
+    z = through(head, kept)
+    V = z.shape[1]
+    on = (labels != ignore) & (labels >= 0) & (labels < V)
+    lab = torch.where(on, labels, torch.zeros_like(labels)).long()
+    lse = torch.logsumexp(z, 1)
+    per = torch.where(on, lse - z.gather(1, lab[:, None])[:, 0], torch.zeros_like(lse))
+    count = max(1, int(on.sum()))
+    total = {"none": per, "sum": per.sum(), "mean": per.sum() / count}[reduction]
+    dz = torch.exp(z - lse[:, None])
+    dz[torch.arange(len(lab)), lab] -= 1
+    dz *= (on.double() / (count if reduction == "mean" else 1))[:, None]
+    return total, dz
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,k,V", [(1, 256, 1000), (3, 16, 5), (130, 256, 1003), (65, 512, 4097), (300, 144, 257),
+                                   (700, 128, 32000)])
+@pytest.mark.parametrize("reduction,gain,bias", [("mean", False, False), ("sum", True, True), ("none", False, True)])
+def test_head_loss(m, k, V, dtype, reduction, gain, bias):
+    g, (head,), x = make(m + V, m, k, V, dtype, gain, bias, std=0.2)
+    labels = torch.randint(0, V, (m,), generator=g, device="cuda", dtype=torch.int32)
+    labels[1::5] = -100
+    labels[:1] = V - 1
+    loss, kept = mmf.head_loss(head.lin, x, labels, reduction=reduction)
+    total, dz = loss64(head, kept.act, labels, reduction)
+    assert loss.shape == total.shape and loss.dtype == torch.float32
+    # logits in fp32: a few steps of |z| < 64 each, 2^-24 * 64 * 4 = 2^-16 per token
+    assert float((loss.double() - total).abs().max()) <= 2.0 ** -16 * (m if reduction == "sum" else 1)
+    dl = torch.rand(m if reduction == "none" else 1, generator=g, device="cuda") + 0.5
+    got = mmf.head_loss_backward(head.lin, kept, labels, dl, reduction=reduction)
+    dz = dz * (dl.double()[:, None] if reduction == "none" else dl.double())
+    dx, dws, dgain, dbias = back64([head], kept.act, [dz])
+    near(got.dx, dx, dtype, "dx")
+    near(got.dw[0], dws[0], dtype, "dw")
+    if gain:
+        near(got.dgain, dgain, dtype, "dgain")
+    if bias:
+        near(got.dbias[0], dbias[0], dtype, "dbias")
+    assert torch.count_nonzero(got.dx[1::5]) == 0   # ignored rows
+    mmf.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_masked_vocabulary_entries_and_ignored_batches(dtype):
+    """A bias of -inf takes an entry out of the softmax; a batch of ignored labels has no loss and no gradient."""
+    g, (head,), x = make(5, 40, 64, 300, dtype, bias=True, std=0.2)
+    head.bias[7::11] = float("-inf")
+    head.bias[130:256] = torch.finfo(torch.float32).min
+    labels = torch.full((40,), 3, dtype=torch.int32, device="cuda")
+    loss, kept = mmf.head_loss(head.lin, x, labels)
+    total, dz = loss64(head, kept.act, labels, "mean")
+    assert abs(float(loss) - float(total)) <= 2.0 ** -16
+    got = mmf.head_loss_backward(head.lin, kept, labels)
+    dx, dws, _, dbias = back64([head], kept.act, [dz])
+    near(got.dx, dx, dtype, "dx")
+    near(got.dw[0], dws[0], dtype, "dw")
+    near(got.dbias[0], dbias[0], dtype, "dbias")
+    assert torch.count_nonzero(got.dw[0][7::11]) == 0
+    labels.fill_(-100)
+    for how in ("mean", "sum", "none"):
+        loss, kept = mmf.head_loss(head.lin, x, labels, reduction=how)
+        got = mmf.head_loss_backward(head.lin, kept, labels, reduction=how)
+        assert torch.count_nonzero(loss) == 0
+        assert all(torch.count_nonzero(t) == 0 for t in (got.dx, got.dw[0], got.dbias[0]))
+    mmf.check()
+
+
+def test_labels_outside_the_vocabulary_are_left_out_and_reported():
+    g, (head,), x = make(6, 9, 64, 100, "bf16", std=0.2)
+    labels = torch.randint(0, 100, (9,), generator=g, device="cuda", dtype=torch.int32)
+    labels[2], labels[5] = 100, -7
+    loss, kept = mmf.head_loss(head.lin, x, labels)
+    total, dz = loss64(head, kept.act, labels, "mean")
+    assert abs(float(loss) - float(total)) <= 2.0 ** -16
+    got = mmf.head_loss_backward(head.lin, kept, labels)
+    near(got.dx, back64([head], kept.act, [dz])[0], "bf16", "dx")
+    with pytest.raises(mmf.MMFError, match="label"):
+        mmf.check()
+    mmf.check()
+
+
+def test_vocabulary_in_pieces():
+    """More gradient of the logits than is held at once: several pieces, the last one shorter and odd."""
+    m, k, V = 8200, 64, 20011
+    g, (head,), x = make(8, m, k, V, "bf16", bias=True, std=0.2)
+    labels = torch.randint(0, V, (m,), generator=g, device="cuda", dtype=torch.int32)
+    loss, kept = mmf.head_loss(head.lin, x, labels)
+    total, dz = loss64(head, kept.act, labels, "mean")
+    assert abs(float(loss) - float(total)) <= 2.0 ** -16
+    got = mmf.head_loss_backward(head.lin, kept, labels)
+    dx, dws, _, dbias = back64([head], kept.act, [dz])
+    near(got.dx, dx, "bf16", "dx")
+    near(got.dw[0], dws[0], "bf16", "dw")
+    near(got.dbias[0], dbias[0], "bf16", "dbias")
+
+
+# ---------------------------------------------------------------- use
+
+def _step(p, ids, labels):
+    """Loss and gradients of one block and a head, forward and backward: embed, f|c|g, scan, o, GLU, head."""
+    B, T = ids.shape
+    d = p["table"].shape[1]
+    x = mmf.embed(p["table"], ids)
+    fcg = [p[n].lin for n in ("f", "c", "g")]
+    pre, k1 = mmf.bitlinear_train(fcg, x)
+    h0 = torch.zeros(B, d, device="cuda")
+    og, hs = mmf.mlgru_scan_states(pre, h0.clone())
+    o, k2 = mmf.bitlinear_train(p["o"].lin, og)
+    x1 = x + o
+    y, k3 = mmf.glu_train(p["gate"].lin, p["up"].lin, p["down"].lin, x1, residual=x1)
+    loss, k4 = mmf.head_loss(p["head"].lin, y, labels)
+    g4 = mmf.head_loss_backward(p["head"].lin, k4, labels)
+    g3 = mmf.glu_backward(p["gate"].lin, p["up"].lin, p["down"].lin, k3, g4.dx, dres=g4.dx)
+    g2 = mmf.bitlinear_backward(p["o"].lin, k2, g3.dx)
+    dpre, _ = mmf.mlgru_scan_backward(pre, h0, g2.dx, hs=hs)
+    g1 = mmf.bitlinear_backward(fcg, k1, dpre, dres=g3.dx)
+    grads = dict(head=g4.dw[0], gate=g3.dw[0], up=g3.dw[1], down=g3.dw[2], o=g2.dw[0], f=g1.dw[0], c=g1.dw[1],
+                 g=g1.dw[2], x=g1.dx)
+    return loss, grads, dict(x=x, pre=pre, og=og, hs=hs, x1=x1, kept=(k1, k2, k3, k4), dpre=dpre)
+
+
+def _step64(p, st, labels, B, T):
+    """The same chain in fp64, from the codes that the forward kept."""
+    k1, k2, k3, k4 = st["kept"]
+    total, dz = loss64(p["head"], k4.act, labels.reshape(-1), "mean")
+    dy, dwh, _, _ = back64([p["head"]], k4.act, [dz])
+    dx1, dwg, _, _ = glu64(p["gate"], p["up"], p["down"], k3, dy)
+    dx1 = dx1 + dy
+    dog, dwo, _, _ = back64([p["o"]], k2, [dx1])
+    d = dy.shape[1]
+    pre = torch.stack([through(p[n], k1) for n in ("f", "c", "g")], 1).to(st["pre"].dtype)
+    res = O.mlgru_scan_backward(*[pre[:, i].reshape(B, T, d).double().cpu().numpy() for i in range(3)],
+                                np.zeros((B, d)), dog.reshape(B, T, d).cpu().numpy())
+    dpre = [torch.from_numpy(np.ascontiguousarray(a)).cuda().reshape(B * T, d) for a in res[:3]]
+    dx, dw1, _, _ = back64([p[n] for n in ("f", "c", "g")], k1, dpre)
+    dx = dx + dx1
+    return total, dict(head=dwh[0], gate=dwg[0], up=dwg[1], down=dwg[2], o=dwo[0], f=dw1[0], c=dw1[1], g=dw1[2], x=dx)
+
+
+def _model(seed, d, inner, V, dtype):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    p = {n: Layer(g, d, d) for n in ("f", "c", "g", "o")}
+    p |= {"gate": Layer(g, inner, d), "up": Layer(g, inner, d), "down": Layer(g, d, inner), "head": Layer(g, V, d, std=0.1)}
+    p["table"] = torch.randn(V, d, generator=g, device="cuda").to(DT[dtype])
+    ids = torch.randint(0, V, (2, 65), generator=g, device="cuda", dtype=torch.int32)
+    return p, ids[:, :-1].contiguous(), ids[:, 1:].contiguous()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_training_step_of_a_block_and_head(dtype):
+    """In fp32 the chain stays within the operators' own tolerance times its length; in bf16 every stage
+    rounds its output once (2^-8 at most) and at most one operand, eight stages from the loss to x."""
+    p, ids, labels = _model(31, 256, 400, 1003, dtype)
+    loss, grads, st = _step(p, ids, labels)
+    total, want = _step64(p, st, labels, *ids.shape)
+    assert abs(float(loss) - float(total)) <= 2.0 ** -16
+    for n, w in want.items():
+        got = grads[n].reshape(w.shape)
+        assert rel(got, w) <= 8 * TOL[dtype], (n, rel(got, w))
+
+
+def test_training_step_captured_and_on_another_stream():
+    """A captured step replays to the eager result, with another step's graph between, and on a side stream."""
+    p, ids, labels = _model(32, 128, 208, 500, "bf16")
+    loss, grads, _ = _step(p, ids, labels)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = _step(p, ids, labels)
+        graphs.append((gr, out))
+    ids2, lab2 = ids.clone(), labels.clone()
+    for _ in range(2):
+        for gr, _ in graphs:
+            gr.replay()
+    torch.cuda.synchronize()
+    for _, (l, gs, _) in graphs:
+        assert torch.equal(l, loss)
+        for n in grads:
+            assert torch.equal(gs[n], grads[n]), n
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        l2, g2, _ = _step(p, ids2, lab2)
+    side.synchronize()
+    assert torch.equal(l2, loss) and all(torch.equal(g2[n], grads[n]) for n in grads)
+    mmf.check()
