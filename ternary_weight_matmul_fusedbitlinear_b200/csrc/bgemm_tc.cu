@@ -5,25 +5,37 @@
 // ("MatMul-free language models", DataCamp blog, "Memory efficiency": the
 // models are trained with fused GPU kernels; no formula is printed, these are
 // the derivatives with the two roundings passed straight through):
-//   dx^[t, k] = gamma sum_n dy[t, n] w[n, k]        form kDx
-//   dW [n, k] = sum_t dy[t, n] q[t, k] / s[t]       form kDw
+//   dx^[t, k] = gamma sum_n dy[t, n] w[n, k]        form dx
+//   dW [n, k] = sum_t dy[t, n] q[t, k] / s[t]       form dw
 // The ternary codes w, and the int8 codes q, are exact in bf16, so the only
 // rounded operand is the gradient (or, for a caller's bf16 gradient, q / s).
-// An fp32 gradient comes as three bf16 planes g = g0 + g1 + g2 (24 bits), whose
-// products accumulate in the same tensor memory: "planes" extends the
-// reduction, plane p's rows of A starting p * a_plane rows further down.
+// An fp32 gradient comes as three bf16 planes g = g0 + g1 + g2 (24 bits); the
+// smallest plane is multiplied first.
 //
-// Operands stay as they lie in memory. For kDx the gradient is K-major (its
+// Operands stay as they lie in memory. For dx the gradient is K-major (its
 // reduction index n is contiguous); every other operand has the reduction
 // index as its row, i.e. is MN-major, which the MMA takes directly (no
 // transposed copies): a 64 x 64 box per 128-byte swizzle column block.
 //
-// Tile 128 x 256 x 64, persistent, one CTA per SM, 4-stage TMA ring of 48 KB,
-// two TMEM accumulators so that a tile's epilogue runs under the next tile's
-// main loop. The last column tile shrinks the MMA to the columns there are.
-// Too few tiles for the SMs (short batches, small matrices): the reduction is
-// cut in `splits` equal ranges, each writing its own fp32 slice for the kernel
-// that reads the result to add up in order (no atomics, same result each run).
+// What bounds it: feeding the tensor cores. A 128 x 256 tile per SM takes 48 KB
+// of operands per 64 reduction steps, 26 TB/s over the chip at the full bf16
+// rate, more than L2 delivers. CTAS = 2 therefore pairs the two SMs of a
+// cluster on a 256 x 256 tile (cta_group::2): each loads its own 128 rows of A
+// and half of B, 32 KB. Single SMs stay for products too small for pairs.
+//
+// Persistent: TMA ring (4 x 48 KB or 6 x 32 KB), two TMEM accumulators, so a
+// tile's epilogue runs under the next tile's main loop. The last column tile
+// shrinks the MMA to the columns there are. Too few tiles for the SMs: the
+// reduction is cut in `splits` ranges, each writing its own fp32 slice for the
+// kernel that reads the result to add up in order (no atomics, same result
+// each run).
+//
+// CHAIN: the reduction is cut in units (8 k-steps of one segment; 4 for fp32
+// planes) whose sums leave tensor memory one by one and are added in registers,
+// each times its segment's gamma. For several layers of one input that is the
+// sum over layers in one launch; for fp32 it bounds the error: the tensor
+// core's running sum is truncated at every step (measured 2e-8 relative per 16
+// reduction steps), the register sum is rounded.
 #include "kernels.cuh"
 #include "umma.cuh"
 
@@ -31,13 +43,17 @@ namespace mmf {
 
 namespace {
 
-constexpr int BM = 128, BN = 256, BK = 64, NS = 4;
-constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, BOX_BYTES = 64 * 64 * 2;
+constexpr int BM = 128, BN = 256, BK = 64;
+constexpr int A_BYTES = BM * BK * 2, BOX_BYTES = 64 * 64 * 2;
 constexpr int kEpiWarps = 8, kEpiWarp0 = 2;
 constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kChainF32 = 4, kChainBf16 = 8;   // k-steps per unit
 
+template <int CTAS>
 struct __align__(1024) Smem {
+  static constexpr int NS = CTAS == 2 ? 6 : 4;
+  static constexpr int B_BYTES = BN / CTAS * BK * 2;
   uint8_t a[NS][A_BYTES];
   uint8_t b[NS][B_BYTES];
   uint8_t stage[kEpiWarps][4096];   // one fp32 box of 32 x 32, or two bf16 ones
@@ -66,13 +82,54 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr) {
   return d;
 }
 
+template <int CTAS>
 __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                          uint32_t accum) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accum)
-      : "memory");
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accum)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accum)
+        : "memory");
+}
+
+// Completion of the MMAs issued so far: arrives at the barrier, in both CTAs of a pair.
+template <int CTAS>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    umma_commit(bar);
+}
+
+// Address of the pair's first CTA's copy of a shared variable.
+__device__ __forceinline__ uint32_t leader_addr(const void* p) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+
+// TMA load into this CTA's shared memory; a pair's loads all count on its first CTA's barrier.
+template <int CTAS>
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(leader_addr(bar))
+        : "memory");
+  else
+    tma_load_2d(dst, map, x, y, bar);
 }
 
 __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, const void* src, int x, int y) {
@@ -83,23 +140,54 @@ __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, const void* s
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// mbar_wait with cluster scope, for a barrier that the other CTA of the pair arrives at.
+__device__ __noinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                          long long limit) {
+  const long long t0 = clock64();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > limit) {
+      *abort_flag = 1;
+      if (status) atomicExch(status, 1);
+      return false;
+    }
+  }
+}
+
 struct KArgs {
   BGemmArgs g;
-  int i_tiles, j_tiles, nk, steps;   // nk: k-steps per plane; steps: planes * nk
+  int i_tiles, j_tiles;
+  int nk, cl, ups, units;   // k-steps per segment; k-steps per unit; units per segment and in all
   int* status;
   long long wait_cycles;
 };
 
-template <bool DW, typename OUT>
+template <bool DW, typename OUT, bool CHAIN, int CTAS>
 __global__ void __launch_bounds__(kThreads, 1)
     bgemm_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                     const __grid_constant__ CUtensorMap map_o0, const __grid_constant__ CUtensorMap map_o1,
-                    const __grid_constant__ CUtensorMap map_o2, const KArgs p) {
+                    const __grid_constant__ CUtensorMap map_o2, const __grid_constant__ KArgs p) {
+  using S = Smem<CTAS>;
+  constexpr int NS = S::NS;
   extern __shared__ uint8_t smem_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &sm.abort_flag;
   const int tiles = p.g.splits * p.i_tiles * p.j_tiles;
+  const int rank = CTAS == 2 ? blockIdx.x & 1 : 0;
+  const int first = blockIdx.x / CTAS, stride = gridDim.x / CTAS;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -108,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&sm.tmem_full[a], 1);
-      mbar_init(&sm.tmem_empty[a], kEpiWarps * 32);
+      mbar_init(&sm.tmem_empty[a], CTAS * kEpiWarps);
     }
     mbar_init(&sm.mma_drain, 1);
     sm.abort_flag = 0;
@@ -117,25 +205,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&map_b);
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
-                 "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (CTAS == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                   "r"(kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                   "r"(kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (CTAS == 2) cluster_sync();   // barriers of both CTAs are set up
   tc_fence_after();
   const uint32_t tmem_base = sm.tmem_base;
   pdl_trigger();
   pdl_wait();
 
-  // tile -> (split, i tile, j tile), j fastest: neighbours share their rows of A
+  // tile -> (split, i tile, j tile), j fastest: neighbours share their rows of A;
+  // its range of units
   auto place = [&](int tile, int& sp, int& it, int& jt, int& lo, int& hi) {
     jt = tile % p.j_tiles;
     it = tile / p.j_tiles % p.i_tiles;
     sp = tile / (p.j_tiles * p.i_tiles);
-    lo = (int)((long long)p.steps * sp / p.g.splits);
-    hi = (int)((long long)p.steps * (sp + 1) / p.g.splits);
+    lo = (int)((long long)p.units * sp / p.g.splits);
+    hi = (int)((long long)p.units * (sp + 1) / p.g.splits);
+  };
+  // MMA columns of a tile: a multiple of 16, for a pair of 32 (each CTA holds half of B)
+  auto cols_of = [&](int jt) {
+    const int n = min(BN, p.g.J - jt * BN);
+    return CTAS == 2 ? (n + 31) / 32 * 32 : n;
   };
 
   if (warp == 0) {
@@ -143,73 +245,121 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t n = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      for (int tile = first; tile < tiles && ok; tile += stride) {
         int sp, it, jt, lo, hi;
         place(tile, sp, it, jt, lo, hi);
-        const int boxes = min(BN / 64, ceil_div(p.g.J - jt * BN, 64));
-        for (int st = lo; st < hi; ++st, ++n) {
-          const int s = n % NS;
-          const int plane = st / p.nk, r0 = (st % p.nk) * BK;
-          if (!mbar_wait(&sm.empty[s], ((n / NS) & 1) ^ 1, abort_flag, p.status, p.wait_cycles)) { ok = false; break; }
-          mbar_arrive_expect_tx(&sm.full[s], A_BYTES + boxes * BOX_BYTES);
-          if constexpr (DW) {
-            tma_load_2d(sm.a[s], &map_a, it * BM, plane * p.g.a_plane + r0, &sm.full[s]);
-            tma_load_2d(sm.a[s] + BOX_BYTES, &map_a, it * BM + 64, plane * p.g.a_plane + r0, &sm.full[s]);
-          } else {
-            tma_load_2d(sm.a[s], &map_a, r0, plane * p.g.a_plane + it * BM, &sm.full[s]);
+        const int half = cols_of(jt) / CTAS, boxes = (half + 63) / 64;
+        const int i0 = (it * CTAS + rank) * BM, j0 = jt * BN + rank * half;
+        for (int u = lo; u < hi && ok; ++u) {
+          const int seg = CHAIN ? u / p.ups : 0;
+          const int kb0 = (u - seg * p.ups) * p.cl, kb1 = min(kb0 + p.cl, p.nk);
+          for (int pl = (CHAIN ? p.g.planes : 1) - 1; pl >= 0 && ok; --pl) {
+            for (int kb = kb0; kb < kb1; ++kb, ++n) {
+              const int s = n % NS, r0 = kb * BK;
+              if (!mbar_wait(&sm.empty[s], ((n / NS) & 1) ^ 1, abort_flag, p.status, p.wait_cycles)) { ok = false; break; }
+              if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], CTAS * (A_BYTES + boxes * BOX_BYTES));
+              if constexpr (DW) {
+                load_box<CTAS>(sm.a[s], &map_a, i0, pl * p.g.a_plane + r0, &sm.full[s]);
+                load_box<CTAS>(sm.a[s] + BOX_BYTES, &map_a, i0 + 64, pl * p.g.a_plane + r0, &sm.full[s]);
+              } else {
+                load_box<CTAS>(sm.a[s], &map_a, seg * p.g.R + r0, pl * p.g.a_plane + i0, &sm.full[s]);
+              }
+              for (int b = 0; b < boxes; ++b)
+                load_box<CTAS>(sm.b[s] + b * BOX_BYTES, &map_b, j0 + 64 * b, seg * p.g.R + r0, &sm.full[s]);
+            }
           }
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(sm.b[s] + b * BOX_BYTES, &map_b, jt * BN + 64 * b, r0, &sm.full[s]);
         }
       }
-      // let every copy this thread issued land before the CTA can exit
-      for (uint32_t j = (n > NS ? n - NS : 0); j < n; ++j) mbar_drain(&sm.full[j % NS], (j / NS) & 1, p.wait_cycles);
+      // let every copy land before the CTA (the pair) can exit
+      if (rank == 0)
+        for (uint32_t j = (n > NS ? n - NS : 0); j < n; ++j) mbar_drain(&sm.full[j % NS], (j / NS) & 1, p.wait_cycles);
+      if (CTAS == 2 && !ok) {   // gave up: the other CTA's copies count on barriers that nobody waits at any more
+        const long long t0 = clock64();
+        while (clock64() - t0 < 2000000) {
+        }
+      }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      uint32_t n = 0, tl = 0;
+    // ------------------------------------------------------------ MMA issuer (the pair's first CTA)
+    if (lane == 0 && rank == 0) {
+      uint32_t n = 0, na = 0;   // ring steps; accumulators begun
       bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++tl) {
+      for (int tile = first; tile < tiles && ok; tile += stride) {
         int sp, it, jt, lo, hi;
         place(tile, sp, it, jt, lo, hi);
-        const int acc = tl & 1;
-        if (!mbar_wait(&sm.tmem_empty[acc], ((tl >> 1) & 1) ^ 1, abort_flag, p.status, p.wait_cycles)) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * BN;
-        const uint32_t idesc = idesc_bf16(BM, min(BN, p.g.J - jt * BN), DW, true);   // J % 16 == 0
-        for (int st = lo; st < hi; ++st, ++n) {
-          const int s = n % NS;
-          if (!mbar_wait(&sm.full[s], (n / NS) & 1, abort_flag, p.status, p.wait_cycles)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t ad = DW ? desc_mn_sw128(smem_u32(sm.a[s])) : umma_desc_sw128(smem_u32(sm.a[s]));
-          const uint64_t bd = desc_mn_sw128(smem_u32(sm.b[s]));
+        const uint32_t idesc = idesc_bf16(BM * CTAS, cols_of(jt), DW, true);
+        uint32_t d_tmem = 0, accum = 0;
+        for (int u = lo; u < hi && ok; ++u) {
+          if (CHAIN || u == lo) {
+            const int acc = na & 1;
+            const bool got = CTAS == 2
+                                 ? wait_cluster(&sm.tmem_empty[acc], ((na >> 1) & 1) ^ 1, abort_flag, p.status, p.wait_cycles)
+                                 : mbar_wait(&sm.tmem_empty[acc], ((na >> 1) & 1) ^ 1, abort_flag, p.status, p.wait_cycles);
+            if (!got) { ok = false; break; }
+            tc_fence_after();
+            d_tmem = tmem_base + acc * BN;
+            accum = 0;
+          }
+          const int kb0 = CHAIN ? (u % p.ups) * p.cl : u;
+          int steps = CHAIN ? (min(kb0 + p.cl, p.nk) - kb0) * p.g.planes : 1;
+          for (; steps > 0; --steps, ++n) {
+            const int s = n % NS;
+            if (!mbar_wait(&sm.full[s], (n / NS) & 1, abort_flag, p.status, p.wait_cycles)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t ad = DW ? desc_mn_sw128(smem_u32(sm.a[s])) : umma_desc_sw128(smem_u32(sm.a[s]));
+            const uint64_t bd = desc_mn_sw128(smem_u32(sm.b[s]));
 #pragma unroll
-          for (int j = 0; j < BK / 16; ++j)   // 16 reduction steps: 2 row groups (MN-major) or 32 bytes (K-major)
-            umma_f16(d_tmem, ad + (uint64_t)(DW ? 128 * j : 2 * j), bd + (uint64_t)(128 * j), idesc,
-                     (st > lo) || (j > 0));
-          umma_commit(&sm.empty[s]);
+            for (int j = 0; j < BK / 16; ++j) {   // 16 reduction steps: 2 row groups (MN-major) or 32 bytes (K-major)
+              umma_f16<CTAS>(d_tmem, ad + (uint64_t)(DW ? 128 * j : 2 * j), bd + (uint64_t)(128 * j), idesc, accum);
+              accum = 1;
+            }
+            commit<CTAS>(&sm.empty[s]);
+          }
+          if (ok && (CHAIN || u == hi - 1)) {
+            commit<CTAS>(&sm.tmem_full[na & 1]);
+            ++na;
+          }
         }
-        if (ok) umma_commit(&sm.tmem_full[acc]);
       }
-      umma_commit(&sm.mma_drain);
+      // every MMA this thread issued has finished before TMEM can be released
+      if constexpr (CTAS == 2)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                         smem_u32(&sm.mma_drain))
+                     : "memory");
+      else
+        umma_commit(&sm.mma_drain);
       mbar_drain(&sm.mma_drain, 0, p.wait_cycles);
     }
   } else {
     // ------------------------------------------------------------ epilogue (8 warps)
     const int ew = warp - kEpiWarp0;
     const int quarter = warp & 3, group = ew >> 2;
-    uint32_t tl = 0;
+    const uint32_t empty_at[2] = {CTAS == 2 ? leader_addr(&sm.tmem_empty[0]) : smem_u32(&sm.tmem_empty[0]),
+                                  CTAS == 2 ? leader_addr(&sm.tmem_empty[1]) : smem_u32(&sm.tmem_empty[1])};
+    uint32_t na = 0;
     int nst = 0;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++tl) {
+    auto wait_full = [&]() {
+      const bool got = mbar_wait(&sm.tmem_full[na & 1], (na >> 1) & 1, abort_flag, p.status, p.wait_cycles);
+      __syncwarp();
+      const bool all = __all_sync(0xffffffffu, got);
+      tc_fence_after();
+      return all;
+    };
+    auto release_acc = [&]() {   // one arrival per warp, at the issuing CTA
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CTAS == 2)
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(empty_at[na & 1]) : "memory");
+        else
+          mbar_arrive(&sm.tmem_empty[na & 1]);
+      }
+      ++na;
+    };
+    for (int tile = first; tile < tiles; tile += stride) {
       int sp, it, jt, lo, hi;
       place(tile, sp, it, jt, lo, hi);
-      const int acc = tl & 1;
-      const bool got = mbar_wait(&sm.tmem_full[acc], (tl >> 1) & 1, abort_flag, p.status, p.wait_cycles);
-      __syncwarp();
-      if (!__all_sync(0xffffffffu, got)) break;
-      tc_fence_after();
-      const int i0 = it * BM + quarter * 32;   // this warp's 32 rows of the result
+      const int i0 = (it * CTAS + rank) * BM + quarter * 32;   // this warp's 32 rows of the result
       const int i = i0 + lane;
       // where the rows go: a slice of partial sums, or segment `seg` of the result
       int seg = 0, y = i0;
@@ -225,20 +375,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           sc = 1.0f / fold_gamma(*p.g.inv_gamma[seg < 3 ? seg : 0]);
       } else {
         y = sp * p.g.slice_rows + i0;
-        if (p.g.gamma != nullptr) sc = *p.g.gamma;
+        if (!CHAIN && p.g.gamma[0] != nullptr) sc = *p.g.gamma[0];
         if (p.g.row_scale != nullptr && i < p.g.I) sc *= p.g.row_scale[i];
       }
       const CUtensorMap* mo = seg == 0 ? &map_o0 : (seg == 1 ? &map_o1 : &map_o2);
       const bool rows_ok = i0 < p.g.I && seg < 3 && p.g.out[seg < 3 ? seg : 0] != nullptr;
-      const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * BN;
-      for (int c = group * 4; c < group * 4 + 4; ++c) {
-        const int j0 = jt * BN + 32 * c;
-        if (j0 >= p.g.J || !rows_ok) break;
-        uint32_t r[32];
-        tmem_ld32(tbase + 32 * c, r);
-        float out[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) out[j] = __uint_as_float(r[j]) * sc;
+      const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+      const int jg = jt * BN + group * 128;                    // this warp's first column
+
+      auto put = [&](const float (&out)[32], int j0) {
         uint8_t* buf = sm.stage[ew];
         if constexpr (sizeof(OUT) == 2) {
           if (lane == 0) bulk_wait_read_le1();
@@ -255,78 +400,181 @@ __global__ void __launch_bounds__(kThreads, 1)
           else tma_store_2d(mo, buf, j0, y);
         }
         ++nst;
+      };
+
+      if constexpr (CHAIN) {
+        float acc[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[c][j] = 0.0f;
+        bool alive = true;
+        for (int u = lo; u < hi; ++u) {
+          if (!(alive = wait_full())) break;
+          float g = sc;
+          if (!DW && p.g.gamma[u / p.ups] != nullptr) g *= *p.g.gamma[u / p.ups];
+          const uint32_t tbase = tmem_base + lanes + (na & 1) * BN + group * 128;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (jg + 32 * c < p.g.J) {
+#pragma unroll
+              for (int h = 0; h < 32; h += 16) {
+                uint32_t r[16];
+                tmem_ld16(tbase + 32 * c + h, r);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[c][h + j] = fmaf(__uint_as_float(r[j]), g, acc[c][h + j]);
+              }
+            }
+          release_acc();
+        }
+        if (!alive) break;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (rows_ok && jg + 32 * c < p.g.J) put(acc[c], jg + 32 * c);
+      } else {
+        if (!wait_full()) break;
+        const uint32_t tbase = tmem_base + lanes + (na & 1) * BN + group * 128;
+        for (int c = 0; c < 4; ++c) {
+          if (jg + 32 * c >= p.g.J || !rows_ok) break;
+          uint32_t r[32];
+          tmem_ld32(tbase + 32 * c, r);
+          float out[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) out[j] = __uint_as_float(r[j]) * sc;
+          put(out, jg + 32 * c);
+        }
+        release_acc();
       }
-      tc_fence_before();
-      mbar_arrive(&sm.tmem_empty[acc]);
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
 
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if constexpr (CTAS == 2) cluster_sync();   // the first CTA's MMAs have read this one's shared memory
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols)
-                 : "memory");
+    if constexpr (CTAS == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
   }
 }
 
-template <bool DW, typename OUT>
-cudaError_t launch_form(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap (&mo)[3], const KArgs& p,
-                        cudaStream_t stream) {
-  auto kern = bgemm_tc_kernel<DW, OUT>;
-  const size_t smem = sizeof(Smem) + 1024;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+struct Maps {
+  CUtensorMap a, b, o[3];
+};
+
+template <bool DW, typename OUT, bool CHAIN, int CTAS>
+cudaError_t launch_form(const Maps& m, const KArgs& p, cudaStream_t stream) {
+  auto kern = bgemm_tc_kernel<DW, OUT, CHAIN, CTAS>;
+  const size_t smem = sizeof(Smem<CTAS>) + 1024;
+  static SmemOptIn opt;
+  const cudaError_t e = opt.set(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const int grid = std::min(p.g.splits * p.i_tiles * p.j_tiles, num_sms());
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, stream, ma, mb, mo[0], mo[1], mo[2], p);
+  const int groups = std::min(p.g.splits * p.i_tiles * p.j_tiles, num_sms() / CTAS);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(groups * CTAS);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CTAS;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CTAS == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, m.a, m.b, m.o[0], m.o[1], m.o[2], p);
+}
+
+template <bool DW, typename OUT, bool CHAIN>
+cudaError_t launch_ctas(const Maps& m, const KArgs& p, cudaStream_t stream) {
+  return p.g.pair ? launch_form<DW, OUT, CHAIN, 2>(m, p, stream) : launch_form<DW, OUT, CHAIN, 1>(m, p, stream);
 }
 
 }  // namespace
 
-// Splits of the reduction: enough tiles for the SMs, at least 8 k-steps (512
-// reduction rows) per split so that a split's fp32 slice costs less than it
-// saves, and no more slices than `most`.
-int bgemm_splits(int I, int J, int R, int planes, int most) {
-  const long long tiles = (long long)ceil_div(I, BM) * ceil_div(J, BN);
-  const long long steps = (long long)planes * ceil_div(R, BK);
-  long long s = num_sms() / std::max(1LL, tiles);
-  s = std::min(s, steps / 8);
-  return (int)std::max(1LL, std::min(s, (long long)most));
+// Tile shape and number of splits, by a model of the time: rounds of tiles over
+// the SMs (pairs), each with its share of the reduction and a start-up, plus
+// the fp32 slices written and read again. Rates as measured on one B200.
+BGemmPlan bgemm_plan(int I, int J, int R, int planes, int nseg, int most) {
+  const bool chain = planes > 1 || nseg > 1;
+  const int cl = planes > 1 ? kChainF32 : kChainBf16;
+  const int nk = ceil_div(R, BK);
+  const int units = nseg * (chain ? ceil_div(nk, cl) : nk);
+  const double steps = (double)nk * planes * nseg;
+  BGemmPlan best = {false, 1};
+  double best_t = 1e30;
+  for (int pair = 0; pair < 2; ++pair) {
+    const double step_us = pair ? 0.48 : 0.60, start_us = 3.0;
+    const long long tiles = (long long)ceil_div(I, pair ? 2 * BM : BM) * ceil_div(J, BN);
+    const int groups = pair ? num_sms() / 2 : num_sms();
+    for (int s = 1; s <= most && s <= units; ++s) {
+      if (s > 1 && steps / s < 8) break;
+      const long long rounds = (tiles * s + groups - 1) / groups;
+      double t = rounds * (steps / s * step_us + start_us);
+      if (s > 1) t += 2.0 + (double)s * I * J * 8 / 4e6;
+      if (t < best_t) {
+        best_t = t;
+        best.pair = pair != 0;
+        best.splits = s;
+      }
+    }
+  }
+  return best;
 }
 
-int bgemm_slice_rows(int I) { return ceil_div(I, BM) * BM; }
+int bgemm_slice_rows(int I) { return ceil_div(I, 32) * 32; }
+
+int bgemm_units(int R, int planes, int nseg) {
+  const int nk = ceil_div(R, BK);
+  return nseg * (planes > 1 ? ceil_div(nk, kChainF32) : nseg > 1 ? ceil_div(nk, kChainBf16) : nk);
+}
 
 cudaError_t launch_bgemm_tc(const BGemmArgs& g, int* status, cudaStream_t stream) {
   if (g.I == 0 || g.J == 0) return cudaSuccess;
-  CUtensorMap ma, mb, mo[3];
-  const uint64_t a_rows = g.dw ? (uint64_t)(g.planes - 1) * g.a_plane + g.R : (uint64_t)(g.planes - 1) * g.a_plane + g.I;
-  const uint64_t a_cols = g.dw ? g.I : g.R;
+  Maps m;
+  const uint64_t a_rows = (uint64_t)(g.planes - 1) * g.a_plane + (g.dw ? g.R : g.I);
+  const uint64_t a_cols = g.dw ? g.I : (uint64_t)g.nseg * g.R;
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  if (!make_tma_2d(&ma, g.a, BF, 2, a_cols, a_rows, 64, g.dw ? 64 : BM, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)g.lda * 2) ||
-      !make_tma_2d(&mb, g.b, BF, 2, (uint64_t)g.J, (uint64_t)g.R, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)g.ldb * 2))
+  if (!make_tma_2d(&m.a, g.a, BF, 2, a_cols, a_rows, 64, g.dw ? 64 : BM, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)g.lda * 2) ||
+      !make_tma_2d(&m.b, g.b, BF, 2, (uint64_t)g.J, (uint64_t)g.nseg * g.R, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B,
+                   (uint64_t)g.ldb * 2))
     return cudaErrorInvalidValue;
   const bool f32 = g.out_f32;
   void* any = g.out[0] != nullptr ? g.out[0] : (g.out[1] != nullptr ? g.out[1] : g.out[2]);
   for (int i = 0; i < 3; ++i) {
-    void* base = g.out[i] != nullptr ? g.out[i] : any;   // a segment without an output is skipped
+    if (i > 0 && g.out[i] == nullptr && g.out[0] != nullptr) {   // a segment without an output is skipped
+      m.o[i] = m.o[0];
+      continue;
+    }
     const uint64_t rows = g.seg_pitch != 0 && g.splits == 1 ? (uint64_t)g.seg_rows : (uint64_t)g.splits * g.slice_rows;
-    if (!make_tma_2d(&mo[i], base, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : BF, f32 ? 4 : 2, (uint64_t)g.J, rows, 32, 32,
+    if (!make_tma_2d(&m.o[i], g.out[i] != nullptr ? g.out[i] : any,
+                     f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : BF, f32 ? 4 : 2, (uint64_t)g.J, rows, 32, 32,
                      f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
   }
+  const bool chain = g.planes > 1 || g.nseg > 1;
   KArgs p;
   p.g = g;
-  p.i_tiles = ceil_div(g.I, BM);
+  p.i_tiles = ceil_div(g.I, g.pair ? 2 * BM : BM);
   p.j_tiles = ceil_div(g.J, BN);
   p.nk = ceil_div(g.R, BK);
-  p.steps = p.nk * g.planes;
+  p.cl = !chain ? 1 : g.planes > 1 ? kChainF32 : kChainBf16;
+  p.ups = ceil_div(p.nk, p.cl);
+  p.units = g.nseg * p.ups;
   p.status = status;
   p.wait_cycles = wait_limit_cycles();
-  if (g.dw) return f32 ? launch_form<true, float>(ma, mb, mo, p, stream) : launch_form<true, bf16>(ma, mb, mo, p, stream);
-  return launch_form<false, float>(ma, mb, mo, p, stream);
+  if (g.splits < 1 || g.splits > p.units) return cudaErrorInvalidValue;
+  if (!g.dw) return chain ? launch_ctas<false, float, true>(m, p, stream) : launch_ctas<false, float, false>(m, p, stream);
+  if (chain) return launch_ctas<true, float, true>(m, p, stream);   // fp32 gradients: fp32 result
+  return f32 ? launch_ctas<true, float, false>(m, p, stream) : launch_ctas<true, bf16, false>(m, p, stream);
 }
 
 }  // namespace mmf

@@ -4,6 +4,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 #include <utility>
 
 #include "common.cuh"
@@ -41,6 +42,22 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
+
+// A kernel's opt-in to `smem` bytes of dynamic shared memory, asked for once per
+// device (one static object per kernel and size).
+struct SmemOptIn {
+  std::atomic<uint64_t> done{0};
+  cudaError_t set(const void* kern, size_t smem) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
+};
 
 // Message returned by mmf_last_error() on this host thread.
 void set_last_error(const char* msg);
@@ -144,27 +161,33 @@ cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, m
                                cudaStream_t stream);
 
 // bf16 training products (bgemm_tc.cu), D fp32 accumulated:
-//   dw = false: D[i, j] = gamma row_scale[i] sum_r A[i, r] B[r, j], A [I, R] K-major
+//   dw = false: D[i, j] = row_scale[i] sum_g gamma[g] sum_r A[i, g R + r] B[g R + r, j]
+//               over nseg segments g (nseg > 1: R a multiple of 64), A [I, nseg R]
 //   dw = true:  D[i, j] = sum_r A[r, i] B[r, j] (/ fold_gamma(inv_gamma)), A [R, I]
-// B is [R, J]; J a multiple of 16; lda, ldb multiples of 8 elements.
+// B is [nseg R, J]; J a multiple of 16; lda, ldb multiples of 8 elements.
 struct BGemmArgs {
-  bool dw;
+  bool dw, pair;            // pair: tiles of two SMs (bgemm_plan)
   const void* a;            // bf16; plane p starts p * a_plane rows further
   int lda, a_plane, planes;
   const void* b;            // bf16
   int ldb;
-  int I, J, R;
+  int I, J, R, nseg;
   int splits;               // > 1: fp32 slices [splits][slice_rows][J] at out[0], to be added up by the reader
   int slice_rows;           // dw = false, or splits > 1: bgemm_slice_rows(I)
   void* out[3];
   bool out_f32;             // dw, splits 1: fp32 or bf16 result (else always fp32)
   bool accumulate;          // fp32 output: add to what is there
   int seg_pitch, seg_rows;  // dw, splits 1: row i goes to out[i / seg_pitch] row i % seg_pitch if < seg_rows
-  const float* gamma;       // dw = false: device scalar or null
+  const float* gamma[3];    // dw = false: device scalars or null
   const float* row_scale;   // dw = false: [I] or null
   const float* inv_gamma[3];  // dw, splits 1: device scalars or null
 };
-int bgemm_splits(int I, int J, int R, int planes, int most);
+struct BGemmPlan {
+  bool pair;
+  int splits;
+};
+BGemmPlan bgemm_plan(int I, int J, int R, int planes, int nseg, int most);
+int bgemm_units(int R, int planes, int nseg);   // the most splits there can be
 int bgemm_slice_rows(int I);
 cudaError_t launch_bgemm_tc(const BGemmArgs& g, int* status, cudaStream_t stream);
 

@@ -86,25 +86,25 @@ struct Grad {
   bool over_s;   // holds G / s: dx^ puts s back per row, dW multiplies by the codes themselves
 };
 
-struct Splits {
-  int dx, dw;
-};
-
-// Workspace of the products for an input [M, K] and `cols` gradient columns.
+// Workspace of the products for an input [M, K]: a gradient of nseg segments of
+// `cols` columns for dx^, of `cols` columns in all for dW.
 size_t dxh_floats(int M, int K, int splits) { return (size_t)splits * bgemm_slice_rows(M) * K; }
-int dx_splits(int M, int K, int cols, mmf_dtype dt) { return bgemm_splits(M, K, cols, planes_of(dt), kMaxSplits); }
-int dw_splits(int M, int K, int cols, mmf_dtype dt) { return bgemm_splits(cols, K, M, planes_of(dt), kMaxSplits); }
+BGemmPlan dx_plan(int M, int K, int cols, int nseg, mmf_dtype dt) {
+  return bgemm_plan(M, K, cols, planes_of(dt), nseg, kMaxSplits);
+}
+BGemmPlan dw_plan(int M, int K, int cols, mmf_dtype dt) { return bgemm_plan(cols, K, M, planes_of(dt), 1, kMaxSplits); }
 size_t dw_floats(int M, int K, int cols, mmf_dtype dt) {
-  const int s = dw_splits(M, K, cols, dt);
+  const int s = dw_plan(M, K, cols, dt).splits;
   return s > 1 ? (size_t)s * bgemm_slice_rows(cols) * K : 0;
 }
 
-// dx^ (+)= gamma G[:, col0 : col0 + cols] W over `splits` slices.
-mmf_status run_dx(const Grad& G, int col0, int cols, const void* wb, int M, int K, const float* gamma,
-                  const float* scale, int splits, bool accumulate, float* dxh, cudaStream_t s) {
+// dx^ (+)= sum over nseg segments of gamma[g] G_g W_g, over the plan's slices.
+mmf_status run_dx(const Grad& G, int nseg, int cols, const void* wb, int M, int K, const float* const* gamma,
+                  const float* scale, const BGemmPlan& plan, bool accumulate, float* dxh, cudaStream_t s) {
   BGemmArgs b = {};
   b.dw = false;
-  b.a = static_cast<const char*>(G.g) + (size_t)col0 * 2;
+  b.pair = plan.pair;
+  b.a = G.g;
   b.lda = G.ld;
   b.a_plane = G.plane_rows;
   b.planes = G.planes;
@@ -113,12 +113,13 @@ mmf_status run_dx(const Grad& G, int col0, int cols, const void* wb, int M, int 
   b.I = M;
   b.J = K;
   b.R = cols;
-  b.splits = splits;
+  b.nseg = nseg;
+  b.splits = plan.splits;
   b.slice_rows = bgemm_slice_rows(M);
   b.out[0] = dxh;
   b.out_f32 = true;
   b.accumulate = accumulate;
-  b.gamma = gamma;
+  for (int i = 0; gamma != nullptr && i < nseg; ++i) b.gamma[i] = gamma[i];
   b.row_scale = G.over_s ? scale : nullptr;
   MMF_CUDA(timed("bgemm_dx", s, [&] { return launch_bgemm_tc(b, status_word(), s); }), "gradient of the input");
   return MMF_OK;
@@ -139,7 +140,10 @@ mmf_status run_dw(const Grad& G, int nseg, int N, int pitch, const void* qb, int
   b.I = cols;
   b.J = K;
   b.R = M;
-  b.splits = dw_splits(M, K, cols, dt);
+  b.nseg = 1;
+  const BGemmPlan plan = dw_plan(M, K, cols, dt);
+  b.pair = plan.pair;
+  b.splits = plan.splits;
   b.slice_rows = bgemm_slice_rows(cols);
   b.seg_rows = N;
   b.seg_pitch = nseg == 1 ? b.slice_rows : pitch;
@@ -210,16 +214,17 @@ mmf_status run_norm(NormBackArgs n, const void* dres, void* dx, void* dgain, flo
 // ---------------------------------------------------------------- BitLinear
 
 // A caller's gradient [M, nlin, N] is the operand as it lies when its rows and
-// layers start on TMA's 16 bytes (and each layer's rows of dW on a 32-row
-// box); fp32 ones, and the others, are written to padded bf16 planes first.
+// layers start on TMA's 16 bytes (several layers: on whole 64-step blocks of
+// the reduction); fp32 ones, and the others, are written to padded bf16 planes
+// first.
 struct LinearPlan {
   bool copy;
   int pitch, cols, planes, rows;
 };
 LinearPlan linear_plan(int nlin, int N, int M, mmf_dtype dt) {
   LinearPlan p;
-  p.copy = dt == MMF_F32 || N % 8 != 0 || (nlin > 1 && N % 32 != 0);
-  p.pitch = !p.copy ? N : pad(N, nlin > 1 ? 32 : 8);
+  p.copy = dt == MMF_F32 || N % 8 != 0 || (nlin > 1 && N % 64 != 0);
+  p.pitch = !p.copy ? N : pad(N, nlin > 1 ? 64 : 8);
   p.cols = nlin * p.pitch;
   p.planes = planes_of(dt);
   p.rows = plane_rows_of(M, dt);
@@ -236,7 +241,7 @@ LinearWs carve_linear(Carver& c, int nlin, int N, int K, int M, mmf_dtype dt) {
   w.wb = c.take<char>((size_t)p.cols * K * 2);
   w.qb = c.take<char>((size_t)M * K * 2);
   w.gb = c.take<char>(p.copy ? (size_t)p.planes * p.rows * p.cols * 2 : 0);
-  w.dxh = c.take<float>(dxh_floats(M, K, dx_splits(M, K, p.pitch, dt)));
+  w.dxh = c.take<float>(dxh_floats(M, K, dx_plan(M, K, p.pitch, nlin, dt).splits));
   w.part = c.take<float>(dw_floats(M, K, nlin == 1 ? N : p.cols, dt));
   w.colpart = c.take<float>(std::max(colsum_ws_floats(M, K), colsum_ws_floats(M, nlin * N)));
   return w;
@@ -294,10 +299,10 @@ mmf_status linear_backward(const mmf_tlinear* lins, int nlin, const mmf_act8& ke
   G.over_s = dt == MMF_F32;
   mmf_status r = MMF_OK;
   if (want_dxh) {
-    const int sp = dx_splits(M, K, lp.pitch, dt);
-    for (int i = 0; i < nlin && r == MMF_OK; ++i)
-      r = run_dx(G, i * lp.pitch, lp.pitch, static_cast<const char*>(w.wb) + (size_t)i * lp.pitch * K * 2, M, K,
-                 lins[i].gamma, kept.scale, sp, i > 0, w.dxh, s);
+    const BGemmPlan plan = dx_plan(M, K, lp.pitch, nlin, dt);
+    const int sp = plan.splits;
+    const float* gam[3] = {lins[0].gamma, lins[nlin > 1 ? 1 : 0].gamma, lins[nlin > 2 ? 2 : 0].gamma};
+    r = run_dx(G, nlin, lp.pitch, w.wb, M, K, gam, kept.scale, plan, false, w.dxh, s);
     if (r != MMF_OK) return r;
     NormBackArgs n = norm_args(w.dxh, sp, M, K, kept, lins[0].gain, x);
     if (cmean != nullptr) {
@@ -483,7 +488,7 @@ GluWs carve_glu(Carver& c, int M, int d, int I, mmf_dtype dt) {
   w.qb = c.take<char>((size_t)M * d * 2);
   w.dz = c.take<char>((size_t)planes_of(dt) * rows * 2 * Ip * 2);
   w.cmean = c.take<float>(M);
-  w.dxh = c.take<float>(dxh_floats(M, d, dx_splits(M, d, 2 * Ip, dt)));
+  w.dxh = c.take<float>(dxh_floats(M, d, dx_plan(M, d, 2 * Ip, 1, dt).splits));
   w.part = c.take<float>(dw_floats(M, d, 2 * Ip, dt));
   w.colpart = c.take<float>(std::max(colsum_ws_floats(M, d), colsum_ws_floats(M, 2 * Ip)));
   return w;
@@ -580,10 +585,10 @@ extern "C" mmf_status mmf_glu_backward(const mmf_tlinear* gate, const mmf_tlinea
   G.over_s = true;
   const float* gam[3] = {gate->gamma, up->gamma, nullptr};
   if (want_dxh) {
-    const int sp = dx_splits(M, d, 2 * Ip, dtype);
-    r = run_dx(G, 0, 2 * Ip, w.wb, M, d, nullptr, kept_x->scale, sp, false, w.dxh, s);
+    const BGemmPlan plan = dx_plan(M, d, 2 * Ip, 1, dtype);
+    r = run_dx(G, 1, 2 * Ip, w.wb, M, d, nullptr, kept_x->scale, plan, false, w.dxh, s);
     if (r != MMF_OK) return r;
-    r = run_norm(norm_args(w.dxh, sp, M, d, *kept_x, gate->gain, x), dres, gx.dx, gx.dgain, w.colpart, dtype, s);
+    r = run_norm(norm_args(w.dxh, plan.splits, M, d, *kept_x, gate->gain, x), dres, gx.dx, gx.dgain, w.colpart, dtype, s);
     if (r != MMF_OK) return r;
   }
   if (want_dw && (r = run_dw(G, 2, I, Ip, w.qb, M, d, gam, gx.dw, w.part, dtype, s)) != MMF_OK) return r;
@@ -648,7 +653,7 @@ HeadWs carve_head(Carver& c, int M, int V, int K, mmf_dtype dt) {
   w.wb = c.take<char>((size_t)V * K * 2);
   w.qb = c.take<char>((size_t)M * K * 2);
   w.dz = c.take<char>((size_t)planes_of(dt) * plane_rows_of(M, dt) * vp * 2);
-  w.dxh = c.take<float>(dxh_floats(M, K, dx_splits(M, K, std::min(vp, V), dt)));
+  w.dxh = c.take<float>(dxh_floats(M, K, dx_plan(M, K, std::min(vp, V), 1, dt).splits));
   size_t part = 0, col = colsum_ws_floats(M, K);
   for (int v0 = 0; v0 < V; v0 += vp) {   // the last piece may be cut into more slices
     part = std::max(part, dw_floats(M, K, std::min(vp, V - v0), dt));
@@ -772,7 +777,7 @@ extern "C" mmf_status mmf_head_loss_backward(const mmf_tlinear* head, const mmf_
   MMF_CUDA(timed("train_prep", s, [&] { return launch_train_prep(pa, s); }), "operands");
   const uint8_t* wu = head->codes != nullptr ? head->codes : w.wu;
   const mmf_tlinear* seg[1] = {head};
-  const int sp = dx_splits(M, K, std::min(vp, V), dtype);
+  const BGemmPlan plan = dx_plan(M, K, std::min(vp, V), 1, dtype);
   for (int v0 = 0; v0 < V; v0 += vp) {
     const int n = std::min(vp, V - v0);
     TGemmArgs a = gemm_args(seg, 1, kept->q, kept->scale, kept->qsum, M, w.dz, vp, nullptr, nullptr);
@@ -800,10 +805,11 @@ extern "C" mmf_status mmf_head_loss_backward(const mmf_tlinear* head, const mmf_
     G.planes = planes_of(dtype);
     G.over_s = true;
     if (want_dxh) {
-      // the last piece may have fewer reduction steps than slices: it adds to the first ones only
-      const int steps = G.planes * ceil_div(n, 64);
-      r = run_dx(G, 0, n, static_cast<const char*>(w.wb) + (size_t)v0 * K * 2, M, K, head->gamma, kept->scale,
-                 std::min(sp, steps), v0 > 0, w.dxh, s);
+      // the last piece may have fewer units than slices: it adds to the first ones only
+      BGemmPlan pp = plan;
+      pp.splits = std::min(plan.splits, bgemm_units(n, G.planes, 1));
+      r = run_dx(G, 1, n, static_cast<const char*>(w.wb) + (size_t)v0 * K * 2, M, K, &head->gamma, kept->scale, pp,
+                 v0 > 0, w.dxh, s);
       if (r != MMF_OK) return r;
     }
     if (want_dw) {
@@ -826,6 +832,6 @@ extern "C" mmf_status mmf_head_loss_backward(const mmf_tlinear* head, const mmf_
     }
   }
   if (!want_dxh) return MMF_OK;
-  return run_norm(norm_args(w.dxh, sp, M, K, *kept, head->gain, x), nullptr, grads->dx, grads->dgain, w.colpart, dtype,
+  return run_norm(norm_args(w.dxh, plan.splits, M, K, *kept, head->gain, x), nullptr, grads->dx, grads->dgain, w.colpart, dtype,
                   s);
 }
