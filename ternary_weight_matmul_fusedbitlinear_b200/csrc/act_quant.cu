@@ -225,10 +225,20 @@ cudaError_t launch_staged(const StagedGeom& g, const void* x, int M, int K, cons
                           float* scale, int32_t* qsum, int* status, void* fill, size_t fill_bytes, float* rinv,
                           cudaStream_t stream) {
   auto kern = rmsnorm_quant_staged_kernel<T, GAIN>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)g.smem);
+  static SmemOptIn opt;
+  cudaError_t e = opt.set(reinterpret_cast<const void*>(kern), 227 * 1024);
   if (e != cudaSuccess) return e;
-  int per_sm = 1;
-  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, g.warps * 32, g.smem);
+  // resident CTAs per SM for this geometry (the occupancy query's answer, asked for once per geometry in turn)
+  static std::atomic<uint64_t> last{0};
+  const uint64_t key = ((uint64_t)g.smem << 16) | ((uint64_t)g.warps << 8);
+  uint64_t known = last.load(std::memory_order_relaxed);
+  if ((known & ~uint64_t(0xff)) != key) {
+    int n = 1;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, g.warps * 32, g.smem);
+    known = key | (uint64_t)std::max(1, std::min(n, 255));
+    last.store(known, std::memory_order_relaxed);
+  }
+  const int per_sm = (int)(known & 0xff);
   const int grid = std::max(1, std::min(ceil_div(M, g.warps), num_sms() * std::max(per_sm, 1)));
   return launch_pdl(kern, dim3(grid), dim3(g.warps * 32), g.smem, stream, static_cast<const T*>(x), M, K, gain, eps,
                     q, scale, qsum, g.slots, g.stride, status, static_cast<uint4*>(fill), fill_bytes / 16, rinv);

@@ -32,6 +32,8 @@
 // kernel records an error in the status word, raises a CTA-wide abort flag,
 // and all roles leave their loops; nothing traps.
 #include "kernels.cuh"
+#include <cstddef>
+
 #include "umma.cuh"
 
 namespace mmf {
@@ -59,9 +61,11 @@ constexpr uint32_t kTmemCols = 512;
 // epilogue warp has 4 staging buffers, one per 32-column chunk of its half
 // tile, into which the whole tile's residual is loaded before the tile's
 // accumulator is ready.
-template <int OB, bool UNP, bool RB = false>
+// GB (GLU backward): the ring is 3 deep to make room for one fp32 box and one
+// box of codes per epilogue warp, which TMA fills ahead of the accumulator.
+template <int OB, bool UNP, bool RB = false, bool GB = false>
 struct __align__(1024) SmemLayout {
-  static constexpr int NS = RB ? 3 : (UNP ? (OB == 2 ? 4 : 3) : (OB == 2 ? 4 : 3));
+  static constexpr int NS = RB || GB ? 3 : (UNP ? (OB == 2 ? 4 : 3) : (OB == 2 ? 4 : 3));
   static constexpr int NSTG = RB ? HALF / kEpiChunk : 2;   // staging buffers per epilogue warp
   static constexpr int NBU = UNP ? NS : NB;        // int8 weight tiles: per TMA stage (UNP) or unpack ring
   static constexpr int NBP = UNP ? 1 : NS;         // packed weight tiles (unused with UNP)
@@ -70,6 +74,8 @@ struct __align__(1024) SmemLayout {
   uint8_t bu[NBU][BU_BYTES];                       // 1024-aligned: SW128 atoms
   uint8_t stage[kEpiWarps][NSTG][kStageBytes];     // epilogue staging (1024-aligned)
   uint32_t bp[NBP][UNP ? 4 : BP_BYTES / 4];
+  alignas(GB ? 1024 : 16) uint8_t gx[GB ? kEpiWarps : 1][GB ? 4096 : 16];  // GB: 32 x 32 fp32 gradients (1024-aligned)
+  alignas(GB ? 1024 : 16) uint8_t gq[GB ? kEpiWarps : 1][GB ? 1024 : 16];  // GB: 32 x 32 codes
   uint64_t tma_full[NS];
   uint64_t tma_empty[NS];
   uint64_t bu_full[NB];
@@ -110,11 +116,28 @@ __device__ __forceinline__ float exp2_fast(float z) {
   return r;
 }
 
-// 32 logits of one token in log2 units, columns n0.. of the segment (past N: -inf).
-__device__ __forceinline__ void logits32(const uint32_t (&r)[32], int qs, float sc2, const float* bias, int n0, int N,
-                                         float (&z)[32]) {
+// acc = raw - qs as a float, by integer and float adds (the conversion
+// instruction issues at an eighth of their rate): |acc| <= 127 K < 2^22 makes
+// the sum with 1.5 * 2^23 exact in the mantissa.
+constexpr int kMaxMagicK = 32768;
+__device__ __forceinline__ float acc_magic(uint32_t raw, int off) {   // off = 0x4B400000 - qs
+  return __uint_as_float(raw + (uint32_t)off) - 12582912.0f;
+}
+// 32 accumulators times sc.
+__device__ __forceinline__ void scaled32(const uint32_t (&r)[32], int qs, float sc, bool magic, float (&z)[32]) {
+  if (magic) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) z[j] = (float)((int)r[j] - qs) * sc2;
+    for (int j = 0; j < 32; ++j) z[j] = acc_magic(r[j], 0x4B400000 - qs) * sc;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) z[j] = (float)((int)r[j] - qs) * sc;
+  }
+}
+
+// 32 logits of one token in log2 units, columns n0.. of the segment (past N: -inf).
+__device__ __forceinline__ void logits32(const uint32_t (&r)[32], int qs, float sc2, bool magic, const float* bias,
+                                         int n0, int N, float (&z)[32]) {
+  scaled32(r, qs, sc2, magic, z);
   if (bias != nullptr) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
@@ -162,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const TcArgs p) {
   constexpr int OB = out_bytes<EPI, T>();
   static_assert(!RB || (EPI == Epi::kStore && OB == 2), "residual prefetch: kStore with 2-byte outputs");
-  using Smem = SmemLayout<OB, UNP, RB>;
+  using Smem = SmemLayout<OB, UNP, RB, EPI == Epi::kGluBwd>;
   constexpr int NS = Smem::NS;
   constexpr int kPlanes = sizeof(T) == 2 ? 1 : 3;   // training epilogues
   extern __shared__ uint8_t smem_raw[];
@@ -341,6 +364,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool alive = true;
     uint32_t res_pending = 0;                     // RB: this tile's residual boxes not yet waited on
+    // GLU backward: this warp's box of dx^ (map_res) and of p's codes (map_b2) for chunk cc of a tile.
+    auto load_chunk = [&](int tile, int cc) {
+      const int n0 = tile % p.n_tiles * HALF + 32 * (group * 2 + cc), y = tile / p.n_tiles * BM + quarter * 32;
+      mbar_arrive_expect_tx(&sm.res_full[ew][0], 4096 + 1024);
+      tma_load_2d(sm.gx[ew], &map_res, n0, y, &sm.res_full[ew][0]);
+      tma_load_2d(sm.gq[ew], &map_b2, n0, y, &sm.res_full[ew][0]);
+    };
+    // The first tile from `tile` on in which this warp has a chunk.
+    auto next_tile = [&](int tile) {
+      while (tile < n_tiles_total && tile % p.n_tiles * HALF + 64 * group >= p.t.plane_cols) tile += gridDim.x;
+      return tile;
+    };
+    uint32_t nload = 0;
+    if constexpr (EPI == Epi::kGluBwd) {
+      const int t0 = next_tile(blockIdx.x);
+      if (lane == 0 && t0 < n_tiles_total) load_chunk(t0, 0);
+      nload = t0 < n_tiles_total;                 // chunks begun by this warp
+    }
     for (int tile = blockIdx.x; tile < n_tiles_total && alive; tile += gridDim.x, ++tl) {
       const int mt = tile / p.n_tiles, nt = tile % p.n_tiles;
       const int acc = tl & 1;
@@ -405,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t r[32];
             tmem_ld32(tbase + group * HALF + 32 * c, r);
             float z[32];
-            logits32(r, qs, sc2, p.g.bias[0], n0, p.g.N, z);
+            logits32(r, qs, sc2, p.g.K <= kMaxMagicK, p.g.bias[0], n0, p.g.N, z);
             float cm = z[0];
 #pragma unroll
             for (int j = 1; j < 32; ++j) cm = fmaxf(cm, z[j]);
@@ -449,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t r[32];
             tmem_ld32(tbase + group * HALF + 32 * c, r);
             float z[32];
-            logits32(r, qs, sc2, p.g.bias[0], n0, p.g.N, z);
+            logits32(r, qs, sc2, p.g.K <= kMaxMagicK, p.g.bias[0], n0, p.g.N, z);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const float g = exp2_fast(z[j] - lse2) - (lab == n0 + j ? 1.0f : 0.0f);
@@ -471,50 +512,96 @@ __global__ void __launch_bounds__(kThreads, 1)
         // its norm (read through the codes of p); du, dv over the token's scale.
         const float sc_u = *p.g.gamma[0] * inv_s, sc_v = *p.g.gamma[1] * inv_s;
         const float fu = fold_gamma(*p.g.gamma[0]) * inv_s, fv = fold_gamma(*p.g.gamma[1]) * inv_s;
-        const float r_p = row_ok ? p.t.rp[m] : 0.0f, c_p = row_ok ? p.t.cp[m] : 0.0f;
-        const float inv_sp = row_ok ? 1.0f / p.t.sp[m] : 0.0f;
+        // dp = rinv_p (gain dx^ - n c): without a gain n = q / s_p, so dp = k1 dx^ - k2 q
+        const float k1 = row_ok ? p.t.rp[m] : 0.0f;
+        const float inv_sp = row_ok ? 1.0f / p.t.sp[m] : 0.0f, kc = row_ok ? k1 * p.t.cp[m] : 0.0f;
+        const bool magic = p.g.K <= kMaxMagicK;
         for (int cc = 0; cc < 2; ++cc) {
           const int c = group * 2 + cc;
           const int n0 = nt * HALF + 32 * c;
           if (n0 >= p.t.plane_cols) break;
+          const bool ok = mbar_wait(&sm.res_full[ew][0], nres & 1, abort_flag, p.status, p.wait_cycles);
+          if (!__all_sync(0xffffffffu, ok)) { alive = false; break; }
+          ++nres;
           float dp[32];
+          {
+            const uint8_t* gx = sm.gx[ew];
+            const uint4* gq = reinterpret_cast<const uint4*>(sm.gq[ew] + lane * 32);
+            const float kq = -kc * inv_sp;
 #pragma unroll
-          for (int j = 0; j < 32; j += 16) {   // N is a multiple of 16
-            if (row_ok && n0 + j < p.g.N) {
-              const size_t at = (size_t)m * p.g.N + n0 + j;
-              const int4 q16 = *reinterpret_cast<const int4*>(p.t.qp + at);
-              const int* qw = &q16.x;
+            for (int h = 0; h < 2; ++h) {
+              const uint4 q16 = gq[h];
+              const uint32_t* qw = &q16.x;
 #pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                const float4 d4 = *reinterpret_cast<const float4*>(p.t.dxh + at + e);
+              for (int e = 0; e < 4; ++e) {
+                const int j = 16 * h + 4 * e;
+                const float4 d4 = *reinterpret_cast<const float4*>(gx + lane * 128 + (((j / 4) ^ (lane & 7)) << 4));
                 const float* d = &d4.x;
+                const uint32_t u4 = qw[e] ^ 0x80808080u;   // q + 128, unsigned bytes
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                  const float xh = (float)((qw[e / 4] << (24 - 8 * b)) >> 24) * inv_sp;
-                  const float gn = p.t.gain_p != nullptr ? __ldg(p.t.gain_p + n0 + j + e + b) : 1.0f;
-                  const float n = p.t.gain_p == nullptr ? xh : (gn != 0.0f ? xh / gn : 0.0f);
-                  dp[j + e + b] = r_p * (gn * d[b] - n * c_p);
+                for (int b = 0; b < 4; ++b) {              // 2^23 + byte, less 2^23 + 128
+                  const float qf = __uint_as_float(__byte_perm(u4, 0x4B000000u, 0x7650 + b)) - 8388736.0f;
+                  dp[j + b] = fmaf(kq, qf, k1 * d[b]);
                 }
               }
-            } else {
+            }
+            if (p.t.gain_p != nullptr) {   // n = xt / gain: k1 gain dx^ - kc xt / gain
 #pragma unroll
-              for (int e = 0; e < 16; ++e) dp[j + e] = 0.0f;
+              for (int h = 0; h < 2; ++h) {
+                const uint4 q16 = gq[h];
+                const uint32_t* qw = &q16.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int j = 16 * h + 4 * e;
+                  const float4 d4 = *reinterpret_cast<const float4*>(gx + lane * 128 + (((j / 4) ^ (lane & 7)) << 4));
+                  const float* d = &d4.x;
+                  const uint32_t u4 = qw[e] ^ 0x80808080u;
+#pragma unroll
+                  for (int b = 0; b < 4; ++b) {
+                    const float qf = __uint_as_float(__byte_perm(u4, 0x4B000000u, 0x7650 + b)) - 8388736.0f;
+                    const float gn = n0 + j + b < p.g.N ? __ldg(p.t.gain_p + n0 + j + b) : 1.0f;
+                    dp[j + b] = k1 * gn * d[b] + (gn != 0.0f ? kq * qf / gn : 0.0f);
+                  }
+                }
+              }
+            }
+          }
+          __syncwarp();
+          {   // this warp's next chunk into the buffers just read
+            int tn = tile, cn = cc + 1;
+            if (cn == 2 || n0 + 32 >= p.t.plane_cols) {
+              tn = next_tile(tile + gridDim.x);
+              cn = 0;
+            }
+            if (tn < n_tiles_total) {
+              ++nload;
+              if (lane == 0) {
+                fence_proxy_async_smem();
+                load_chunk(tn, cn);
+              }
             }
           }
           uint32_t ru[32], rv[32];
           tmem_ld32(tbase + 32 * c, ru);
           tmem_ld32(tbase + HALF + 32 * c, rv);
           float du[32], dv[32];
+          scaled32(ru, qs, sc_u, magic, du);
+          scaled32(rv, qs, sc_v, magic, dv);
+          if (p.g.bias[0] != nullptr)
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float u = (float)((int)ru[j] - qs) * sc_u, v = (float)((int)rv[j] - qs) * sc_v;
-            const bool in = n0 + j < p.g.N;
-            if (p.g.bias[0] != nullptr && in) u += __ldg(p.g.bias[0] + n0 + j);
-            if (p.g.bias[1] != nullptr && in) v += __ldg(p.g.bias[1] + n0 + j);
+            for (int j = 0; j < 32; ++j)
+              if (n0 + j < p.g.N) du[j] += __ldg(p.g.bias[0] + n0 + j);
+          if (p.g.bias[1] != nullptr)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (n0 + j < p.g.N) dv[j] += __ldg(p.g.bias[1] + n0 + j);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {   // past N and M dp is 0 (boxes read zeros there), and so are du, dv
+            const float u = du[j], v = dv[j];
             const float sg = __fdividef(1.0f, 1.0f + exp2_fast(-u * kLog2e));
             const float us = u * sg;
-            du[j] = in && row_ok ? dp[j] * v * fmaf(us, 1.0f - sg, sg) * fu : 0.0f;
-            dv[j] = in && row_ok ? dp[j] * us * fv : 0.0f;
+            du[j] = dp[j] * fu * (v * fmaf(us, 1.0f - sg, sg));
+            dv[j] = dp[j] * fv * us;
           }
 #pragma unroll
           for (int pl = 0; pl < kPlanes; ++pl) {
@@ -598,6 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(&sm.tmem_empty[acc]);
     }
+    if constexpr (EPI == Epi::kGluBwd)   // a chunk begun and given up: let it land (bounded)
+      if (lane == 0 && nload > nres) mbar_drain(&sm.res_full[ew][0], nres & 1, p.wait_cycles);
     if constexpr (RB) {   // residual boxes issued for a tile that was given up: let them land (bounded)
       if (lane == 0)
         for (int c = 0; c < Smem::NSTG; ++c)
@@ -619,12 +708,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- host side
+// What TMA writes to lies on its boundaries: 128 bytes, 1024 for swizzled tiles.
+template <class S>
+constexpr bool tma_aligned() {
+  return offsetof(S, a) % 1024 == 0 && offsetof(S, bu) % 1024 == 0 && offsetof(S, stage) % 1024 == 0 &&
+         offsetof(S, bp) % 128 == 0 && offsetof(S, gx) % (sizeof(S::gx) >= 4096 ? 1024 : 16) == 0 &&
+         offsetof(S, gq) % (sizeof(S::gq) >= 1024 ? 128 : 16) == 0;
+}
+
 template <Epi EPI, typename T, bool UNP, bool RB = false>
 cudaError_t launch_mapped(const CUtensorMap& ma, const CUtensorMap (&mb)[3], const CUtensorMap& mo,
                           const CUtensorMap& mr, const TcArgs& p, cudaStream_t stream) {
-  const size_t smem = sizeof(SmemLayout<out_bytes<EPI, T>(), UNP, RB>) + 1024;
+  using Smem = SmemLayout<out_bytes<EPI, T>(), UNP, RB, EPI == Epi::kGluBwd>;
+  static_assert(tma_aligned<Smem>() && sizeof(Smem) + 1024 <= 227 * 1024, "shared memory layout");
+  const size_t smem = sizeof(Smem) + 1024;
   auto kern = tgemm_tc_kernel<EPI, T, UNP, RB>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static SmemOptIn opt;
+  cudaError_t e = opt.set(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const int tiles = p.m_tiles * p.n_tiles;
   const int grid = std::min(tiles, num_sms());
@@ -721,6 +821,14 @@ cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, m
       !make_tma_2d(&mo, a.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)a.ldo, (uint64_t)planes * t.plane_rows,
                    kEpiChunk, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
+  CUtensorMap mr = mo;
+  if (epi == Epi::kGluBwd) {   // dx^ and the codes of the down projection's input, 32 x 32 boxes
+    if (!make_tma_2d(&mr, t.dxh, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, (uint64_t)a.N, (uint64_t)a.M, 32, 32,
+                     CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tma_2d(&mb[2], t.qp, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.N, (uint64_t)a.M, 32, 32,
+                     CU_TENSOR_MAP_SWIZZLE_NONE))
+      return cudaErrorInvalidValue;
+  }
   TcArgs p;
   p.g = a;
   p.t = t;
@@ -731,13 +839,13 @@ cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, m
   p.n_tiles = is_glu(epi) ? ceil_div(a.N, HALF) : ceil_div(a.N, BN);
   const bool b = dt == MMF_BF16;
   switch (epi) {
-    case Epi::kLse: return launch_mapped<Epi::kLse, bf16, true>(ma, mb, mo, mo, p, stream);
+    case Epi::kLse: return launch_mapped<Epi::kLse, bf16, true>(ma, mb, mo, mr, p, stream);
     case Epi::kDz:
-      return b ? launch_mapped<Epi::kDz, bf16, true>(ma, mb, mo, mo, p, stream)
-               : launch_mapped<Epi::kDz, float, true>(ma, mb, mo, mo, p, stream);
+      return b ? launch_mapped<Epi::kDz, bf16, true>(ma, mb, mo, mr, p, stream)
+               : launch_mapped<Epi::kDz, float, true>(ma, mb, mo, mr, p, stream);
     case Epi::kGluBwd:
-      return b ? launch_mapped<Epi::kGluBwd, bf16, true>(ma, mb, mo, mo, p, stream)
-               : launch_mapped<Epi::kGluBwd, float, true>(ma, mb, mo, mo, p, stream);
+      return b ? launch_mapped<Epi::kGluBwd, bf16, true>(ma, mb, mo, mr, p, stream)
+               : launch_mapped<Epi::kGluBwd, float, true>(ma, mb, mo, mr, p, stream);
     default: return cudaErrorNotSupported;
   }
 }

@@ -142,90 +142,127 @@ __device__ __forceinline__ void norm4(const NormBackArgs& a, size_t at, int k, f
   }
 }
 
-// WPR warps per row (1 for many rows, 8 for few or long ones). The second pass
-// reads the row again from L1/L2, where the first one has just brought it.
-template <typename T, int WPR, bool STAT>
+// WPR warps per row, WPR * 128 * NV columns at most; the row's dx^ stays in
+// registers between the mean and the result (its codes are read again from L1).
+// NV = 0: rows of any length, read twice.
+template <typename T, int WPR, int NV, bool STAT>
 __global__ void __launch_bounds__(kThreads) norm_back_kernel(const NormBackArgs a) {
   __shared__ float red[kThreads / 32];
   pdl_trigger();
   pdl_wait();
   constexpr int kRows = kThreads / 32 / WPR, kLanes = 32 * WPR;
   const int lane = threadIdx.x % kLanes, warp = threadIdx.x >> 5;
-  for (int row0 = blockIdx.x * kRows; row0 < a.M; row0 += gridDim.x * kRows) {
-    const int row = row0 + (int)threadIdx.x / kLanes;
-    const bool in = row < a.M;
-    const size_t base = (size_t)row * a.K;
-    const float inv_s = in ? 1.0f / a.scale[row] : 0.0f, rinv = in ? a.rinv[row] : 0.0f;
-    float dot = 0.0f;
-    if (in) {
-#pragma unroll 4
+  const int row = blockIdx.x * kRows + (int)threadIdx.x / kLanes;
+  const bool in = row < a.M;
+  const size_t base = (size_t)row * a.K;
+  const float inv_s = in ? 1.0f / a.scale[row] : 0.0f, rinv = in ? a.rinv[row] : 0.0f;
+  float dot = 0.0f;
+  float keep[NV > 0 ? NV : 1][4];
+  auto mean_part = [&](int k, const float (&v)[4]) {
+    float xh[4], n[4], g[4];
+    if constexpr (STAT) {   // only the codes are read for the mean
+      const int w = *reinterpret_cast<const int*>(a.q + base + k);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xh[i] = (float)((w << (24 - 8 * i)) >> 24) * inv_s;
+      if (a.slices > 1) st4(a.dxh + base + k, v);
+    } else {
+      norm4<T>(a, base + k, k, inv_s, rinv, xh, n, g);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dot = fmaf(v[i], xh[i], dot);
+  };
+  if (in) {
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int k = (i * kLanes + lane) * 4;
+        if (k < a.K) slices4(a, base + k, keep[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int k = (i * kLanes + lane) * 4;
+        if (k < a.K) mean_part(k, keep[i]);
+      }
+    } else {
       for (int k = lane * 4; k < a.K; k += kLanes * 4) {
-        float v[4], xh[4], n[4], g[4];
-        slices4(a, base + k, v);
-        if constexpr (STAT) {   // only the codes are read for the mean
-          const int w = *reinterpret_cast<const int*>(a.q + base + k);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) xh[i] = (float)((w << (24 - 8 * i)) >> 24) * inv_s;
-          if (a.slices > 1) st4(a.dxh + base + k, v);
-        } else {
-          norm4<T>(a, base + k, k, inv_s, rinv, xh, n, g);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dot = fmaf(v[i], xh[i], dot);
+        slices4(a, base + k, keep[0]);
+        mean_part(k, keep[0]);
       }
     }
+  }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if constexpr (WPR > 1) {
-      if ((threadIdx.x & 31) == 0) red[warp] = dot;
-      __syncthreads();
-      dot = 0.0f;
-      for (int w = 0; w < WPR; ++w) dot += red[warp / WPR * WPR + w];
-      __syncthreads();
-    }
-    const float c = dot / (float)a.K;
-    if constexpr (STAT) {
-      if (in && lane == 0) a.cmean[row] = c;
-    } else if (in) {
-#pragma unroll 4
+  for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 31) == 0) red[warp] = dot;
+    __syncthreads();
+    dot = 0.0f;
+    for (int w = 0; w < WPR; ++w) dot += red[warp / WPR * WPR + w];
+  }
+  const float c = dot / (float)a.K;
+  if constexpr (STAT) {
+    if (in && lane == 0) a.cmean[row] = c;
+  } else if (in) {
+    auto write = [&](int k, const float (&v)[4]) {
+      float xh[4], n[4], g[4], o[4];
+      norm4<T>(a, base + k, k, inv_s, rinv, xh, n, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = rinv * fmaf(g[i], v[i], -n[i] * c);
+      if (a.dres != nullptr) {
+        float d[4];
+        ld4(static_cast<const T*>(a.dres) + base + k, d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += d[i];
+      }
+      st4(static_cast<T*>(a.dx) + base + k, o);
+    };
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int k = (i * kLanes + lane) * 4;
+        if (k < a.K) write(k, keep[i]);
+      }
+    } else {
       for (int k = lane * 4; k < a.K; k += kLanes * 4) {
-        float v[4], xh[4], n[4], g[4], o[4];
-        slices4(a, base + k, v);
-        norm4<T>(a, base + k, k, inv_s, rinv, xh, n, g);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = rinv * fmaf(g[i], v[i], -n[i] * c);
-        if (a.dres != nullptr) {
-          float d[4];
-          ld4(static_cast<const T*>(a.dres) + base + k, d);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] += d[i];
-        }
-        st4(static_cast<T*>(a.dx) + base + k, o);
+        slices4(a, base + k, keep[0]);
+        write(k, keep[0]);
       }
     }
   }
 }
 
 // ---------------------------------------------------------------- column sums
-constexpr int kColsPerBlock = 64, kRowLanes = kThreads / kColsPerBlock;
+constexpr int kColsPerBlock = 64, kColLanes = kColsPerBlock / 4, kRowLanes = kThreads / kColLanes;
 
+// 4 columns c.. of row t; vec: rows start on 4-element boundaries and c + 4 <= cols.
 template <ColSum KIND, typename T>
-__device__ __forceinline__ float col_term(const ColSumArgs& a, int t, int c) {
-  if constexpr (KIND == ColSum::kGrad) {
-    return to_f32(static_cast<const T*>(a.src)[(size_t)t * a.segs * a.pitch + c]);
-  } else if constexpr (KIND == ColSum::kPlanes) {
-    float v = 0.0f;
-    for (int p = 0; p < a.planes; ++p)
-      v += to_f32(static_cast<const bf16*>(a.src)[((size_t)p * a.plane_rows + t) * a.segs * a.pitch + c]);
-    return v * a.scale[t];
-  } else {
+__device__ __forceinline__ void col_terms(const ColSumArgs& a, int t, int c, int cols, bool vec, float (&v)[4]) {
+  if constexpr (KIND == ColSum::kGain) {
     const NormBackArgs& b = a.nb;
-    const size_t at = (size_t)t * b.K + c;
-    float v = b.dxh[at];
-    for (int s = 1; s < b.slices; ++s) v += b.dxh[(size_t)s * b.slice_rows * b.K + at];
-    if (b.x != nullptr) return v * to_f32(static_cast<const T*>(b.x)[at]) * b.rinv[t];
-    const float g = b.gain != nullptr ? b.gain[c] : 1.0f;
-    return g != 0.0f ? v * ((float)b.q[at] / b.scale[t] / g) : 0.0f;
+    float xh[4], n[4], g[4];
+    const size_t at = (size_t)t * b.K + c;   // K is a multiple of 16
+    slices4(b, at, v);
+    norm4<T>(b, at, c, 1.0f / b.scale[t], b.rinv[t], xh, n, g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] *= n[i];
+  } else if constexpr (KIND == ColSum::kPlanes) {   // pitch is a multiple of 32
+    const float s = a.scale[t];
+    v[0] = v[1] = v[2] = v[3] = 0.0f;
+    for (int p = a.planes - 1; p >= 0; --p) {
+      float w[4];
+      ld4(static_cast<const bf16*>(a.src) + ((size_t)p * a.plane_rows + t) * cols + c, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += w[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] *= s;
+  } else {
+    const T* src = static_cast<const T*>(a.src) + (size_t)t * cols + c;
+    if (vec) {
+      ld4(src, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = c + i < cols ? to_f32(src[i]) : 0.0f;
+    }
   }
 }
 
@@ -237,28 +274,36 @@ __device__ __forceinline__ void col_store(const ColSumArgs& a, int c, float v) {
   static_cast<T*>(a.out[seg])[n] = from_f32<T>(v);
 }
 
-// Block (x: 64 columns, y: a range of rows); a thread sums every 4th row of its
-// column, the four are added in order. One range writes the result, several
+// Block (x: 64 columns, y: a range of rows); a thread sums every 16th row of 4
+// columns, the 16 are added in order. One range writes the result, several
 // write partial sums.
 template <ColSum KIND, typename T>
 __global__ void __launch_bounds__(kThreads) colsum_kernel(const ColSumArgs a, int cols, int rows_per) {
   __shared__ float red[kRowLanes][kColsPerBlock];
   pdl_trigger();
   pdl_wait();
-  const int c = blockIdx.x * kColsPerBlock + threadIdx.x % kColsPerBlock, rl = threadIdx.x / kColsPerBlock;
+  const int c = blockIdx.x * kColsPerBlock + threadIdx.x % kColLanes * 4, rl = threadIdx.x / kColLanes;
   const int t0 = blockIdx.y * rows_per, t1 = min(a.M, t0 + rows_per);
-  float sum = 0.0f;
+  const bool vec = cols % 4 == 0;
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c < cols) {
 #pragma unroll 4
-    for (int t = t0 + rl; t < t1; t += kRowLanes) sum += col_term<KIND, T>(a, t, c);
+    for (int t = t0 + rl; t < t1; t += kRowLanes) {
+      float v[4];
+      col_terms<KIND, T>(a, t, c, cols, vec, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] += v[i];
+    }
   }
-  red[rl][threadIdx.x % kColsPerBlock] = sum;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) red[rl][threadIdx.x % kColLanes * 4 + i] = sum[i];
   __syncthreads();
-  if (rl == 0 && c < cols) {
+  const int cc = blockIdx.x * kColsPerBlock + threadIdx.x;
+  if (threadIdx.x < kColsPerBlock && cc < cols) {
     float v = red[0][threadIdx.x];
     for (int i = 1; i < kRowLanes; ++i) v += red[i][threadIdx.x];
-    if (gridDim.y == 1) col_store<T>(a, c, v);
-    else a.part[(size_t)blockIdx.y * cols + c] = v;
+    if (gridDim.y == 1) col_store<T>(a, cc, v);
+    else a.part[(size_t)blockIdx.y * cols + cc] = v;
   }
 }
 
@@ -273,10 +318,11 @@ __global__ void __launch_bounds__(kThreads) colsum_join_kernel(const ColSumArgs 
   col_store<T>(a, c, v);
 }
 
-// Row ranges: at least 64 rows each, about two blocks per SM in all.
+// Row ranges: at least 256 rows each (16 per thread; below that one launch is
+// quicker than two), about two blocks per SM in all.
 int colsum_parts(int M, int cols) {
   const int want = std::max(1, 2 * 148 / ceil_div(cols, kColsPerBlock));
-  return std::max(1, std::min(want, ceil_div(M, 64)));
+  return std::max(1, std::min(want, ceil_div(M, 256)));
 }
 
 // ---------------------------------------------------------------- joining slices of dW
@@ -403,22 +449,27 @@ cudaError_t launch_train_prep(const PrepArgs& a, cudaStream_t stream) {
                              : launch_pdl(train_prep_kernel<float>, grid, dim3(kThreads), 0, stream, u);
 }
 
-template <typename T>
-static cudaError_t norm_back_typed(const NormBackArgs& a, bool stat, cudaStream_t stream) {
-  // one warp per row once there are enough rows for every SM's warps
-  const bool warp_rows = a.M >= num_sms() * 16 && a.K <= 4096;
-  const dim3 grid(warp_rows ? std::min(ceil_div(a.M, 8), num_sms() * 8) : std::min(a.M, num_sms() * 8));
-  const dim3 block(kThreads);
-  if (stat)
-    return warp_rows ? launch_pdl(norm_back_kernel<T, 1, true>, grid, block, 0, stream, a)
-                     : launch_pdl(norm_back_kernel<T, 8, true>, grid, block, 0, stream, a);
-  return warp_rows ? launch_pdl(norm_back_kernel<T, 1, false>, grid, block, 0, stream, a)
-                   : launch_pdl(norm_back_kernel<T, 8, false>, grid, block, 0, stream, a);
+template <typename T, bool STAT>
+static cudaError_t norm_back_typed(const NormBackArgs& a, cudaStream_t stream) {
+  // As few warps per row as hold it at 16 columns a thread; all 8 when there
+  // are too few rows to fill the SMs otherwise.
+  int wpr = a.K <= 512 ? 1 : a.K <= 1024 ? 2 : a.K <= 2048 ? 4 : 8;
+  if (a.M < num_sms() * 8) wpr = 8;
+  const dim3 grid(ceil_div(a.M, 8 / wpr)), block(kThreads);
+  if (a.K > 8192) return launch_pdl(norm_back_kernel<T, 8, 0, STAT>, grid, block, 0, stream, a);
+  if (a.K > 4096) return launch_pdl(norm_back_kernel<T, 8, 8, STAT>, grid, block, 0, stream, a);
+  switch (wpr) {
+    case 1: return launch_pdl(norm_back_kernel<T, 1, 4, STAT>, grid, block, 0, stream, a);
+    case 2: return launch_pdl(norm_back_kernel<T, 2, 4, STAT>, grid, block, 0, stream, a);
+    case 4: return launch_pdl(norm_back_kernel<T, 4, 4, STAT>, grid, block, 0, stream, a);
+    default: return launch_pdl(norm_back_kernel<T, 8, 4, STAT>, grid, block, 0, stream, a);
+  }
 }
 
 cudaError_t launch_norm_back(const NormBackArgs& a, bool stat, mmf_dtype dt, cudaStream_t stream) {
   if (a.M == 0) return cudaSuccess;
-  return dt == MMF_BF16 ? norm_back_typed<bf16>(a, stat, stream) : norm_back_typed<float>(a, stat, stream);
+  if (stat) return dt == MMF_BF16 ? norm_back_typed<bf16, true>(a, stream) : norm_back_typed<float, true>(a, stream);
+  return dt == MMF_BF16 ? norm_back_typed<bf16, false>(a, stream) : norm_back_typed<float, false>(a, stream);
 }
 
 size_t colsum_ws_floats(int M, int cols) {

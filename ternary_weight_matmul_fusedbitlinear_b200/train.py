@@ -22,18 +22,62 @@ from typing import NamedTuple, Optional, Sequence, Union
 import torch
 
 from . import _lib as L
-from .api import DEFAULT_EPS, TLinear, _dtype, _need_cuda, _stream, _workspace
+from .api import _DT, DEFAULT_EPS, TLinear
 
 _REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
+_P3 = L.c_vp * 3
+_byref = ctypes.byref
 
 
-class Act8(NamedTuple):
+class Act8:
     """A layer's input [M, K] as its forward kept it: int8 codes q [M, K] with x^ = q / scale,
-    scale [M], qsum [M] (int32 sums of the codes) and rinv [M] (1 / rms)."""
-    q: torch.Tensor
-    scale: torch.Tensor
-    qsum: torch.Tensor
-    rinv: torch.Tensor
+    scale [M], qsum [M] (int32 sums of the codes) and rinv [M] (1 / rms).
+
+    Made by the training forwards (one buffer for all four), or from four tensors."""
+
+    __slots__ = ("_parts", "_buf", "_m", "_k")
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor, qsum: torch.Tensor, rinv: torch.Tensor):
+        if q.dim() != 2 or any(t.shape != q.shape[:1] for t in (scale, qsum, rinv)):
+            raise ValueError("kept activations are q [M, K] and scale, qsum, rinv [M]")
+        if q.dtype != torch.int8 or qsum.dtype != torch.int32 or scale.dtype != torch.float32 or \
+                rinv.dtype != torch.float32:
+            raise ValueError("kept activations must be int8 codes, float32 scale and rinv, int32 qsum")
+        _check(q.get_device(), q, scale, qsum, rinv)
+        self._parts, self._buf = (q, scale, qsum, rinv), None
+        self._m, self._k = q.shape
+
+    @classmethod
+    def _new(cls, m: int, k: int, device: torch.device) -> "Act8":
+        me = cls.__new__(cls)
+        me._parts, me._m, me._k = None, m, k
+        me._buf = torch.empty(_pad16(m * k) + 3 * _pad16(4 * m), dtype=torch.int8, device=device)
+        return me
+
+    def _tensors(self):
+        if self._parts is None:
+            m, k = self._m, self._k
+            at, step = _pad16(m * k), _pad16(4 * m)
+            rows = [self._buf[at + i * step: at + i * step + 4 * m] for i in range(3)]
+            self._parts = (self._buf[:m * k].view(m, k), rows[0].view(torch.float32), rows[1].view(torch.int32),
+                           rows[2].view(torch.float32))
+        return self._parts
+
+    q = property(lambda self: self._tensors()[0])
+    scale = property(lambda self: self._tensors()[1])
+    qsum = property(lambda self: self._tensors()[2])
+    rinv = property(lambda self: self._tensors()[3])
+
+    def _c(self, m: int, k: int, device: int) -> L.Act8:
+        if self._m != m or self._k != k:
+            raise ValueError(f"kept activations are of {self._m} rows of {self._k}, not {m} of {k}")
+        if self._buf is not None:
+            if self._buf.get_device() != device:
+                raise ValueError("all tensors must be on one device")
+            p, at, step = self._buf.data_ptr(), _pad16(m * k), _pad16(4 * m)
+            return L.Act8(p, p + at, p + at + step, p + at + 2 * step)
+        _check(device, *self._parts)
+        return L.Act8(*[t.data_ptr() for t in self._parts])
 
 
 class HeadKept(NamedTuple):
@@ -61,35 +105,60 @@ class GluGrads(NamedTuple):
     dbias: list
 
 
-def _on(device: torch.device):
-    """Run on `device`, whichever one is current."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _pad16(n: int) -> int:
+    return (n + 15) // 16 * 16
+
+
+def _on(index: int):
+    """Run on device `index`, whichever one is current."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
+def _stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _same_device(first: torch.Tensor, *ts: Optional[torch.Tensor]) -> None:
-    _need_cuda(first, *ts)
+def _check(index: int, *ts: Optional[torch.Tensor]) -> None:
+    """Contiguous CUDA tensors on device `index`."""
+    if index < 0:
+        raise ValueError("mmf needs CUDA tensors (there is no CPU path)")
     for t in ts:
-        if t is not None and t.device != first.device:
-            raise ValueError("all tensors must be on one device")
+        if t is not None:
+            if t.get_device() != index:
+                raise ValueError("all tensors must be on one CUDA device")
+            if not t.is_contiguous():
+                raise ValueError("mmf needs contiguous tensors")
 
 
-def _layer_tensors(lins: Sequence[TLinear]) -> list:
-    return [t for lin in lins for t in (lin.packed, lin.gamma, lin.gain, lin.bias, lin.codes)]
+def _code(dtype: torch.dtype) -> int:
+    c = _DT.get(dtype)
+    if c is None:
+        raise ValueError(f"unsupported activation dtype {dtype}")
+    return c
+
+
+def _layers(lins: Union[TLinear, Sequence[TLinear]], index: int) -> list:
+    out = [lins] if isinstance(lins, TLinear) else list(lins)
+    if not 1 <= len(out) <= 3:
+        raise ValueError("1 to 3 layers share one input")
+    _on_device(out, index)
+    return out
+
+
+def _on_device(lins: Sequence[TLinear], index: int) -> None:
+    for lin in lins:
+        _check(index, lin.packed, lin.gamma, lin.gain, lin.bias, lin.codes)
+        for t in (lin.gain, lin.bias):
+            if t is not None and t.dtype != torch.float32:
+                raise ValueError("gains and biases are float32")
 
 
 def _c_layers(lins: Sequence[TLinear]):
     return (L.TLinear * len(lins))(*[lin.c() for lin in lins])
-
-
-def _layers(lins: Union[TLinear, Sequence[TLinear]]) -> list:
-    out = [lins] if isinstance(lins, TLinear) else list(lins)
-    if not 1 <= len(out) <= 3:
-        raise ValueError("1 to 3 layers share one input")
-    return out
 
 
 def _rows(x: torch.Tensor, width: int, what: str) -> int:
@@ -98,29 +167,21 @@ def _rows(x: torch.Tensor, width: int, what: str) -> int:
     return x.numel() // width
 
 
-def _new_kept(m: int, k: int, device: torch.device) -> Act8:
-    rows = torch.empty(3, max(4, (m + 3) // 4 * 4), dtype=torch.float32, device=device)   # 16-byte aligned rows
-    return Act8(torch.empty(m, k, dtype=torch.int8, device=device), rows[0, :m], rows[1, :m].view(torch.int32),
-                rows[2, :m])
-
-
-def _c_kept(kept: Act8, m: int, k: int, like: torch.Tensor) -> L.Act8:
-    q, s, qs, r = kept
-    if q.shape != (m, k) or s.shape != (m,) or qs.shape != (m,) or r.shape != (m,):
-        raise ValueError(f"kept activations must be those of an input of {m} rows of {k}")
-    if q.dtype != torch.int8 or qs.dtype != torch.int32 or s.dtype != torch.float32 or r.dtype != torch.float32:
-        raise ValueError("kept activations must be int8 codes, float32 scale and rinv, int32 qsum")
-    _same_device(like, q, s, qs, r)
-    return L.Act8(q.data_ptr(), s.data_ptr(), qs.data_ptr(), r.data_ptr())
-
-
-def _like(t: Optional[torch.Tensor], ref: torch.Tensor, what: str) -> None:
-    if t is not None and (t.numel() != ref.numel() or t.dtype != ref.dtype):
+def _like(t: Optional[torch.Tensor], numel: int, dtype: torch.dtype, what: str) -> None:
+    if t is not None and (t.numel() != numel or t.dtype != dtype):
         raise ValueError(f"{what} must have the shape and dtype of the input")
 
 
-def _bytes(ws: torch.Tensor) -> int:
-    return ws.numel() * ws.element_size()
+def _scratch(nbytes: int, device: torch.device, ws: Optional[torch.Tensor]):
+    """(address, bytes, tensor) of the caller's workspace, or of a new one."""
+    if ws is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return ws.data_ptr(), nbytes, ws
+    _check(device.index, ws)
+    have = ws.numel() * ws.element_size()
+    if have < nbytes:
+        raise ValueError(f"workspace too small: {have} < {nbytes}")
+    return ws.data_ptr(), have, ws
 
 
 # ---------------------------------------------------------------- BitLinear
@@ -130,22 +191,19 @@ def bitlinear_train(lins: Union[TLinear, Sequence[TLinear]], x: torch.Tensor, ep
     """Training forward of 1 to 3 layers of one shape and gain on x [..., K] (mmf_bitlinear_train).
 
     Returns (y, kept): y [..., N] for a layer, [..., n, N] for a sequence of n; kept: Act8."""
-    ls = _layers(lins)
-    _same_device(x, *_layer_tensors(ls))
+    idx, dev, dt = x.get_device(), x.device, x.dtype
+    _check(idx, x)
+    ls = _layers(lins, idx)
     n, N, K = len(ls), ls[0].N, ls[0].K
     m = _rows(x, K, "x")
-    dev = x.device
-    lead = x.shape[:-1]
-    y = torch.empty(*lead, N, dtype=x.dtype, device=dev) if isinstance(lins, TLinear) else \
-        torch.empty(*lead, n, N, dtype=x.dtype, device=dev)
-    kept = _new_kept(m, K, dev)
+    code = _code(dt)
+    y = torch.empty(x.shape[:-1] + ((N,) if isinstance(lins, TLinear) else (n, N)), dtype=dt, device=dev)
+    kept = Act8._new(m, K, dev)
     lib = L.load()
-    w = _workspace(lib.mmf_bitlinear_train_ws_size(n, N, K), dev, ws)
-    ck = _c_kept(kept, m, K, x)
-    with _on(dev):
-        L.check(lib.mmf_bitlinear_train(_c_layers(ls), n, x.data_ptr(), _dtype(x), m, y.data_ptr(), eps,
-                                        ctypes.byref(ck), w.data_ptr(), _bytes(w), _stream(dev)),
-                "mmf_bitlinear_train")
+    wp, wn, _keep = _scratch(lib.mmf_bitlinear_train_ws_size(n, N, K), dev, ws)
+    with _on(idx):
+        L.check(lib.mmf_bitlinear_train(_c_layers(ls), n, x.data_ptr(), code, m, y.data_ptr(), eps,
+                                        _byref(kept._c(m, K, idx)), wp, wn, _stream(idx)), "mmf_bitlinear_train")
     return y, kept
 
 
@@ -156,8 +214,9 @@ def bitlinear_backward(lins: Union[TLinear, Sequence[TLinear]], kept: Act8, dy: 
 
     x: the forward's input, for layers whose gain comes near 0 (otherwise read from the codes);
     dres: added to dx, e.g. the gradient that reaches x along a residual."""
-    ls = _layers(lins)
-    _same_device(dy, x, dres, *_layer_tensors(ls))
+    idx, dev, dt = dy.get_device(), dy.device, dy.dtype
+    _check(idx, dy, x, dres)
+    ls = _layers(lins, idx)
     n, N, K = len(ls), ls[0].N, ls[0].K
     one = isinstance(lins, TLinear)
     m = _rows(dy, N, "dy")
@@ -165,51 +224,43 @@ def bitlinear_backward(lins: Union[TLinear, Sequence[TLinear]], kept: Act8, dy: 
         if dy.dim() < 2 or dy.shape[-2] != n:
             raise ValueError(f"dy must be [..., {n}, {N}], got {tuple(dy.shape)}")
         m //= n
-    dev, dt = dy.device, dy.dtype
-    code = _dtype(dy)
-    dx = torch.empty(*dy.shape[:-1 if one else -2], K, dtype=dt, device=dev)
-    _like(x, dx, "x")
-    _like(dres, dx, "dres")
-    ck = _c_kept(kept, m, K, dy)
-    dw = [torch.empty(N, K, dtype=dt, device=dev) for _ in ls]
-    dgain = torch.empty(K, dtype=dt, device=dev) if ls[0].gain is not None else None
-    dbias = [torch.empty(N, dtype=dt, device=dev) if lin.bias is not None else None for lin in ls]
-    fill = [None] * (3 - n)
-    cg = L.LinearGrads(dx.data_ptr(), (L.c_vp * 3)(*[t.data_ptr() for t in dw], *fill), _p(dgain),
-                       (L.c_vp * 3)(*[_p(t) for t in dbias], *fill))
+    code = _code(dt)
+    _like(x, m * K, dt, "x")
+    _like(dres, m * K, dt, "dres")
+    dx = torch.empty(dy.shape[:-1 if one else -2] + (K,), dtype=dt, device=dev)
+    dw = [torch.empty((N, K), dtype=dt, device=dev) for _ in ls]
+    dgain = None if ls[0].gain is None else torch.empty(K, dtype=dt, device=dev)
+    dbias = [None if lin.bias is None else torch.empty(N, dtype=dt, device=dev) for lin in ls]
+    cg = L.LinearGrads(dx.data_ptr(), _P3(*[t.data_ptr() for t in dw]), _p(dgain), _P3(*[_p(t) for t in dbias]))
     lib = L.load()
-    w = _workspace(lib.mmf_bitlinear_backward_ws_size(n, N, K, m, code), dev, ws)
-    with _on(dev):
-        L.check(lib.mmf_bitlinear_backward(_c_layers(ls), n, ctypes.byref(ck), _p(x), dy.data_ptr(), _p(dres), code, m,
-                                           ctypes.byref(cg), w.data_ptr(), _bytes(w), _stream(dev)),
+    wp, wn, _keep = _scratch(lib.mmf_bitlinear_backward_ws_size(n, N, K, m, code), dev, ws)
+    with _on(idx):
+        L.check(lib.mmf_bitlinear_backward(_c_layers(ls), n, _byref(kept._c(m, K, idx)), _p(x), dy.data_ptr(),
+                                           _p(dres), code, m, _byref(cg), wp, wn, _stream(idx)),
                 "mmf_bitlinear_backward")
     return LinearGrads(dx, dw, dgain, dbias)
 
 
 # ---------------------------------------------------------------- GLU
 
-def _glu_layers(gate: TLinear, up: TLinear, down: TLinear):
-    ls = [gate, up, down]
-    return ls, [ctypes.byref(lin.c()) for lin in ls]
-
-
 def glu_train(gate: TLinear, up: TLinear, down: TLinear, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
               eps: float = DEFAULT_EPS, ws: Optional[torch.Tensor] = None):
     """glu() that keeps the codes of x and of the product: (y, (kept_x, kept_p)) (mmf_glu_train)."""
-    ls, cl = _glu_layers(gate, up, down)
-    _same_device(x, residual, *_layer_tensors(ls))
+    idx, dev, dt = x.get_device(), x.device, x.dtype
+    _check(idx, x, residual)
+    _on_device((gate, up, down), idx)
     d, inner = gate.K, gate.N
     m = _rows(x, d, "x")
-    _like(residual, x, "residual")
-    dev, code = x.device, _dtype(x)
+    code = _code(dt)
+    _like(residual, m * d, dt, "residual")
     y = torch.empty_like(x)
-    kx, kp = _new_kept(m, d, dev), _new_kept(m, inner, dev)
+    kx, kp = Act8._new(m, d, dev), Act8._new(m, inner, dev)
     lib = L.load()
-    w = _workspace(lib.mmf_glu_train_ws_size(m, d, inner, code), dev, ws)
-    with _on(dev):
-        L.check(lib.mmf_glu_train(*cl, x.data_ptr(), _p(residual), y.data_ptr(), m, code, eps,
-                                  ctypes.byref(_c_kept(kx, m, d, x)), ctypes.byref(_c_kept(kp, m, inner, x)),
-                                  w.data_ptr(), _bytes(w), _stream(dev)), "mmf_glu_train")
+    wp, wn, _keep = _scratch(lib.mmf_glu_train_ws_size(m, d, inner, code), dev, ws)
+    with _on(idx):
+        L.check(lib.mmf_glu_train(_byref(gate.c()), _byref(up.c()), _byref(down.c()), x.data_ptr(), _p(residual),
+                                  y.data_ptr(), m, code, eps, _byref(kx._c(m, d, idx)), _byref(kp._c(m, inner, idx)),
+                                  wp, wn, _stream(idx)), "mmf_glu_train")
     return y, (kx, kp)
 
 
@@ -218,35 +269,39 @@ def glu_backward(gate: TLinear, up: TLinear, down: TLinear, kept, dy: torch.Tens
     """Gradients of glu_train for dy [..., d] (mmf_glu_backward); kept, x, dres as in bitlinear_backward.
 
     With residual=x in the forward, pass dres=dy."""
-    ls, cl = _glu_layers(gate, up, down)
-    _same_device(dy, x, dres, *_layer_tensors(ls))
+    idx, dev, dt = dy.get_device(), dy.device, dy.dtype
+    _check(idx, dy, x, dres)
+    ls = (gate, up, down)
+    _on_device(ls, idx)
     d, inner = gate.K, gate.N
     m = _rows(dy, d, "dy")
-    _like(x, dy, "x")
-    _like(dres, dy, "dres")
-    dev, dt, code = dy.device, dy.dtype, _dtype(dy)
-    kx, kp = (_c_kept(k, m, n, dy) for k, n in zip(kept, (d, inner)))
+    code = _code(dt)
+    _like(x, m * d, dt, "x")
+    _like(dres, m * d, dt, "dres")
+    kx, kp = kept
     dx = torch.empty_like(dy)
-    dw = [torch.empty(lin.N, lin.K, dtype=dt, device=dev) for lin in ls]
-    dgain = [torch.empty(lin.K, dtype=dt, device=dev) if lin.gain is not None else None for lin in (gate, down)]
-    dbias = [torch.empty(lin.N, dtype=dt, device=dev) if lin.bias is not None else None for lin in ls]
+    dw = [torch.empty((lin.N, lin.K), dtype=dt, device=dev) for lin in ls]
+    dgain = [None if lin.gain is None else torch.empty(lin.K, dtype=dt, device=dev) for lin in (gate, down)]
+    dbias = [None if lin.bias is None else torch.empty(lin.N, dtype=dt, device=dev) for lin in ls]
     cg = L.GluGrads(dx.data_ptr(), *[t.data_ptr() for t in dw], *[_p(t) for t in dgain], *[_p(t) for t in dbias])
     lib = L.load()
-    w = _workspace(lib.mmf_glu_backward_ws_size(m, d, inner, code), dev, ws)
-    with _on(dev):
-        L.check(lib.mmf_glu_backward(*cl, ctypes.byref(kx), ctypes.byref(kp), _p(x), dy.data_ptr(), _p(dres), code, m,
-                                     ctypes.byref(cg), w.data_ptr(), _bytes(w), _stream(dev)), "mmf_glu_backward")
+    wp, wn, _keep = _scratch(lib.mmf_glu_backward_ws_size(m, d, inner, code), dev, ws)
+    with _on(idx):
+        L.check(lib.mmf_glu_backward(_byref(gate.c()), _byref(up.c()), _byref(down.c()), _byref(kx._c(m, d, idx)),
+                                     _byref(kp._c(m, inner, idx)), _p(x), dy.data_ptr(), _p(dres), code, m, _byref(cg),
+                                     wp, wn, _stream(idx)), "mmf_glu_backward")
     return GluGrads(dx, dw, dgain, dbias)
 
 
 # ---------------------------------------------------------------- LM head loss
 
-def _head_args(head: TLinear, labels: torch.Tensor, m: int, reduction: str) -> int:
-    if reduction not in _REDUCTIONS:
+def _head_args(labels: torch.Tensor, m: int, reduction: str) -> int:
+    red = _REDUCTIONS.get(reduction)
+    if red is None:
         raise ValueError(f"reduction must be one of {sorted(_REDUCTIONS)}")
     if labels.dtype != torch.int32 or labels.numel() != m:
         raise ValueError(f"labels must be int32, one per token ({m})")
-    return _REDUCTIONS[reduction]
+    return red
 
 
 def head_loss(head: TLinear, x: torch.Tensor, labels: torch.Tensor, ignore_index: int = -100,
@@ -254,20 +309,22 @@ def head_loss(head: TLinear, x: torch.Tensor, labels: torch.Tensor, ignore_index
     """Softmax cross entropy of the logits head(x) against int32 labels, without storing the logits
     (mmf_head_loss): (loss, kept). loss is a float32 scalar ("mean" over the counted tokens, "sum") or the
     per-token losses in labels' shape ("none"); kept: HeadKept for head_loss_backward."""
-    _same_device(x, labels, *_layer_tensors([head]))
-    m = _rows(x, head.K, "x")
-    red = _head_args(head, labels, m, reduction)
-    dev = x.device
+    idx, dev = x.get_device(), x.device
+    _check(idx, x, labels)
+    _on_device((head,), idx)
+    N, K = head.N, head.K
+    m = _rows(x, K, "x")
+    red = _head_args(labels, m, reduction)
+    code = _code(x.dtype)
     loss = torch.empty(labels.shape if red == 0 else (), dtype=torch.float32, device=dev)
-    kept = HeadKept(_new_kept(m, head.K, dev), torch.empty(m, dtype=torch.float32, device=dev),
+    kept = HeadKept(Act8._new(m, K, dev), torch.empty(m, dtype=torch.float32, device=dev),
                     torch.empty(1, dtype=torch.float32, device=dev), x.dtype)
     lib = L.load()
-    w = _workspace(lib.mmf_head_loss_ws_size(m, head.N, head.K), dev, ws)
-    with _on(dev):
-        L.check(lib.mmf_head_loss(ctypes.byref(head.c()), x.data_ptr(), _dtype(x), m, labels.data_ptr(), ignore_index,
-                                  red, eps, loss.data_ptr(), ctypes.byref(_c_kept(kept.act, m, head.K, x)),
-                                  kept.lse.data_ptr(), kept.count.data_ptr(), w.data_ptr(), _bytes(w), _stream(dev)),
-                "mmf_head_loss")
+    wp, wn, _keep = _scratch(lib.mmf_head_loss_ws_size(m, N, K), dev, ws)
+    with _on(idx):
+        L.check(lib.mmf_head_loss(_byref(head.c()), x.data_ptr(), code, m, labels.data_ptr(), ignore_index, red, eps,
+                                  loss.data_ptr(), _byref(kept.act._c(m, K, idx)), kept.lse.data_ptr(),
+                                  kept.count.data_ptr(), wp, wn, _stream(idx)), "mmf_head_loss")
     return loss, kept
 
 
@@ -277,27 +334,26 @@ def head_loss_backward(head: TLinear, kept: HeadKept, labels: torch.Tensor, dlos
     """Gradients of head_loss for dloss (float32: one value, or one per token for "none"; None: 1), in the dtype
     of the forward's input (mmf_head_loss_backward); labels, ignore_index and reduction as there, x as in
     bitlinear_backward."""
-    _same_device(labels, dloss, x, kept.lse, kept.count, *_layer_tensors([head]))
+    idx, dev, dt = labels.get_device(), labels.device, kept.dtype
+    _check(idx, labels, dloss, x, kept.lse, kept.count)
+    _on_device((head,), idx)
     m, N, K = labels.numel(), head.N, head.K
-    red = _head_args(head, labels, m, reduction)
-    dev, dt = labels.device, kept.dtype
+    red = _head_args(labels, m, reduction)
+    code = _code(dt)
     if dloss is not None and (dloss.dtype != torch.float32 or dloss.numel() != (m if red == 0 else 1)):
         raise ValueError("dloss must be float32, one value (one per token for reduction 'none')")
     if kept.lse.numel() != m:
         raise ValueError("kept must come from head_loss on the same tokens")
-    ck = _c_kept(kept.act, m, K, labels)
-    dx = torch.empty(*labels.shape, K, dtype=dt, device=dev)
-    _like(x, dx, "x")
-    code = _dtype(dx)
-    dw = torch.empty(N, K, dtype=dt, device=dev)
-    dgain = torch.empty(K, dtype=dt, device=dev) if head.gain is not None else None
-    dbias = torch.empty(N, dtype=dt, device=dev) if head.bias is not None else None
-    cg = L.LinearGrads(dx.data_ptr(), (L.c_vp * 3)(dw.data_ptr()), _p(dgain), (L.c_vp * 3)(_p(dbias)))
+    _like(x, m * K, dt, "x")
+    dx = torch.empty(labels.shape + (K,), dtype=dt, device=dev)
+    dw = torch.empty((N, K), dtype=dt, device=dev)
+    dgain = None if head.gain is None else torch.empty(K, dtype=dt, device=dev)
+    dbias = None if head.bias is None else torch.empty(N, dtype=dt, device=dev)
+    cg = L.LinearGrads(dx.data_ptr(), _P3(dw.data_ptr()), _p(dgain), _P3(_p(dbias)))
     lib = L.load()
-    w = _workspace(lib.mmf_head_loss_backward_ws_size(m, N, K, code), dev, ws)
-    with _on(dev):
-        L.check(lib.mmf_head_loss_backward(ctypes.byref(head.c()), ctypes.byref(ck), _p(x), labels.data_ptr(),
+    wp, wn, _keep = _scratch(lib.mmf_head_loss_backward_ws_size(m, N, K, code), dev, ws)
+    with _on(idx):
+        L.check(lib.mmf_head_loss_backward(_byref(head.c()), _byref(kept.act._c(m, K, idx)), _p(x), labels.data_ptr(),
                                            kept.lse.data_ptr(), kept.count.data_ptr(), _p(dloss), ignore_index, red,
-                                           code, m, ctypes.byref(cg), w.data_ptr(), _bytes(w), _stream(dev)),
-                "mmf_head_loss_backward")
+                                           code, m, _byref(cg), wp, wn, _stream(idx)), "mmf_head_loss_backward")
     return LinearGrads(dx, [dw], dgain, [dbias])
