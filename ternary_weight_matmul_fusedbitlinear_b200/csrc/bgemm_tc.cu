@@ -30,7 +30,10 @@
 // kernel that reads the result to add up in order (no atomics, same result
 // each run).
 //
-// CHAIN: the reduction is cut in units (8 k-steps of one segment; 4 for fp32
+// One launch can run both products of a backward, dx's tiles before dw's: small
+// ones share the SMs, one start-up and one launch.
+//
+// Chained products: the reduction is cut in units (8 k-steps of one segment; 4 for fp32
 // planes) whose sums leave tensor memory one by one and are added in registers,
 // each times its segment's gamma. For several layers of one input that is the
 // sum over layers in one launch; for fp32 it bounds the error: the tensor
@@ -166,26 +169,39 @@ __device__ __noinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volati
   }
 }
 
-struct KArgs {
-  BGemmArgs g;
+// What the kernel reads of a product (BGemmArgs without its operands).
+struct ProbArgs {
+  int a_plane, planes, I, J, R, splits, slice_rows, seg_pitch;
+  bool out_f32, accumulate;
+  const void* out[3];
+  const float *gamma[3], *inv_gamma[3], *row_scale;
+};
+struct Prob {
+  ProbArgs g;
   int i_tiles, j_tiles;
   int nk, cl, ups, units;   // k-steps per segment; k-steps per unit; units per segment and in all
+};
+struct KArgs {
+  Prob pr[2];               // dx, dw
+  int tiles0, tiles;        // dx's tiles; all tiles
   int* status;
   long long wait_cycles;
 };
+struct Maps {
+  CUtensorMap a[2], b[2], o[4];   // outputs: dx, then dw's segments
+};
 
-template <bool DW, typename OUT, bool CHAIN, int CTAS>
+// KIND 0: nothing chained; 1: dx chained (several layers); 2: both (fp32 planes).
+// MODE 0: dx alone, 1: dw alone, 2: both.
+template <int KIND, int CTAS, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
-    bgemm_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                    const __grid_constant__ CUtensorMap map_o0, const __grid_constant__ CUtensorMap map_o1,
-                    const __grid_constant__ CUtensorMap map_o2, const __grid_constant__ KArgs p) {
+    bgemm_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ KArgs p) {
   using S = Smem<CTAS>;
   constexpr int NS = S::NS;
   extern __shared__ uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &sm.abort_flag;
-  const int tiles = p.g.splits * p.i_tiles * p.j_tiles;
   const int rank = CTAS == 2 ? blockIdx.x & 1 : 0;
   const int first = blockIdx.x / CTAS, stride = gridDim.x / CTAS;
 
@@ -201,8 +217,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.mma_drain, 1);
     sm.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    prefetch_tmap(&map_a);
-    prefetch_tmap(&map_b);
+    const int d = MODE == 2 ? (first < p.tiles0 ? 0 : 1) : MODE;
+    prefetch_tmap(&maps.a[d]);
+    prefetch_tmap(&maps.b[d]);
   }
   if (warp == 1) {
     if constexpr (CTAS == 2) {
@@ -225,18 +242,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   pdl_wait();
 
-  // tile -> (split, i tile, j tile), j fastest: neighbours share their rows of A;
-  // its range of units
-  auto place = [&](int tile, int& sp, int& it, int& jt, int& lo, int& hi) {
-    jt = tile % p.j_tiles;
-    it = tile / p.j_tiles % p.i_tiles;
-    sp = tile / (p.j_tiles * p.i_tiles);
-    lo = (int)((long long)p.units * sp / p.g.splits);
-    hi = (int)((long long)p.units * (sp + 1) / p.g.splits);
+  // tile -> product, (split, i tile, j tile), j fastest: neighbours share their
+  // rows of A; its range of units; whether units are drained one by one
+  struct Place {
+    bool dw, chain;
+    int sp, it, jt, lo, hi;
+  };
+  auto place = [&](int tile) {
+    Place t;
+    t.dw = MODE == 2 ? tile >= p.tiles0 : MODE == 1;
+    const Prob& q = p.pr[t.dw];
+    const int id = MODE == 2 && t.dw ? tile - p.tiles0 : tile;
+    t.jt = id % q.j_tiles;
+    t.it = id / q.j_tiles % q.i_tiles;
+    t.sp = id / (q.j_tiles * q.i_tiles);
+    t.lo = (int)((long long)q.units * t.sp / q.g.splits);
+    t.hi = (int)((long long)q.units * (t.sp + 1) / q.g.splits);
+    t.chain = KIND == 2 || (KIND == 1 && !t.dw);
+    return t;
   };
   // MMA columns of a tile: a multiple of 16, for a pair of 32 (each CTA holds half of B)
-  auto cols_of = [&](int jt) {
-    const int n = min(BN, p.g.J - jt * BN);
+  auto cols_of = [&](const Prob& q, int jt) {
+    const int n = min(BN, q.g.J - jt * BN);
     return CTAS == 2 ? (n + 31) / 32 * 32 : n;
   };
 
@@ -245,27 +272,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t n = 0;
       bool ok = true;
-      for (int tile = first; tile < tiles && ok; tile += stride) {
-        int sp, it, jt, lo, hi;
-        place(tile, sp, it, jt, lo, hi);
-        const int half = cols_of(jt) / CTAS, boxes = (half + 63) / 64;
-        const int i0 = (it * CTAS + rank) * BM, j0 = jt * BN + rank * half;
-        for (int u = lo; u < hi && ok; ++u) {
-          const int seg = CHAIN ? u / p.ups : 0;
-          const int kb0 = (u - seg * p.ups) * p.cl, kb1 = min(kb0 + p.cl, p.nk);
-          for (int pl = (CHAIN ? p.g.planes : 1) - 1; pl >= 0 && ok; --pl) {
+      for (int tile = first; tile < p.tiles && ok; tile += stride) {
+        const Place t = place(tile);
+        const Prob& q = p.pr[t.dw];
+        const CUtensorMap *ma = &maps.a[t.dw], *mb = &maps.b[t.dw];
+        const int half = cols_of(q, t.jt) / CTAS, boxes = (half + 63) / 64;
+        const int i0 = (t.it * CTAS + rank) * BM, j0 = t.jt * BN + rank * half;
+        for (int u = t.lo; u < t.hi && ok; ++u) {
+          const int seg = t.chain ? u / q.ups : 0;
+          const int kb0 = (u - seg * q.ups) * q.cl, kb1 = min(kb0 + q.cl, q.nk);
+          for (int pl = q.g.planes - 1; pl >= 0 && ok; --pl) {
             for (int kb = kb0; kb < kb1; ++kb, ++n) {
               const int s = n % NS, r0 = kb * BK;
               if (!mbar_wait(&sm.empty[s], ((n / NS) & 1) ^ 1, abort_flag, p.status, p.wait_cycles)) { ok = false; break; }
               if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], CTAS * (A_BYTES + boxes * BOX_BYTES));
-              if constexpr (DW) {
-                load_box<CTAS>(sm.a[s], &map_a, i0, pl * p.g.a_plane + r0, &sm.full[s]);
-                load_box<CTAS>(sm.a[s] + BOX_BYTES, &map_a, i0 + 64, pl * p.g.a_plane + r0, &sm.full[s]);
+              if (t.dw) {
+                load_box<CTAS>(sm.a[s], ma, i0, pl * q.g.a_plane + r0, &sm.full[s]);
+                load_box<CTAS>(sm.a[s] + BOX_BYTES, ma, i0 + 64, pl * q.g.a_plane + r0, &sm.full[s]);
               } else {
-                load_box<CTAS>(sm.a[s], &map_a, seg * p.g.R + r0, pl * p.g.a_plane + i0, &sm.full[s]);
+                load_box<CTAS>(sm.a[s], ma, seg * q.g.R + r0, pl * q.g.a_plane + i0, &sm.full[s]);
               }
               for (int b = 0; b < boxes; ++b)
-                load_box<CTAS>(sm.b[s] + b * BOX_BYTES, &map_b, j0 + 64 * b, seg * p.g.R + r0, &sm.full[s]);
+                load_box<CTAS>(sm.b[s] + b * BOX_BYTES, mb, j0 + 64 * b, seg * q.g.R + r0, &sm.full[s]);
             }
           }
         }
@@ -284,13 +312,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && rank == 0) {
       uint32_t n = 0, na = 0;   // ring steps; accumulators begun
       bool ok = true;
-      for (int tile = first; tile < tiles && ok; tile += stride) {
-        int sp, it, jt, lo, hi;
-        place(tile, sp, it, jt, lo, hi);
-        const uint32_t idesc = idesc_bf16(BM * CTAS, cols_of(jt), DW, true);
+      for (int tile = first; tile < p.tiles && ok; tile += stride) {
+        const Place t = place(tile);
+        const Prob& q = p.pr[t.dw];
+        const uint32_t idesc = idesc_bf16(BM * CTAS, cols_of(q, t.jt), t.dw, true);
+        // 16 reduction steps: 2 row groups (MN-major) or 32 bytes (K-major)
+        const uint32_t astep = t.dw ? 128 : 2;
         uint32_t d_tmem = 0, accum = 0;
-        for (int u = lo; u < hi && ok; ++u) {
-          if (CHAIN || u == lo) {
+        for (int u = t.lo; u < t.hi && ok; ++u) {
+          if (t.chain || u == t.lo) {
             const int acc = na & 1;
             const bool got = CTAS == 2
                                  ? wait_cluster(&sm.tmem_empty[acc], ((na >> 1) & 1) ^ 1, abort_flag, p.status, p.wait_cycles)
@@ -300,22 +330,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             d_tmem = tmem_base + acc * BN;
             accum = 0;
           }
-          const int kb0 = CHAIN ? (u % p.ups) * p.cl : u;
-          int steps = CHAIN ? (min(kb0 + p.cl, p.nk) - kb0) * p.g.planes : 1;
+          const int kb0 = t.chain ? (u % q.ups) * q.cl : u;
+          int steps = t.chain ? (min(kb0 + q.cl, q.nk) - kb0) * q.g.planes : 1;
           for (; steps > 0; --steps, ++n) {
             const int s = n % NS;
             if (!mbar_wait(&sm.full[s], (n / NS) & 1, abort_flag, p.status, p.wait_cycles)) { ok = false; break; }
             tc_fence_after();
-            const uint64_t ad = DW ? desc_mn_sw128(smem_u32(sm.a[s])) : umma_desc_sw128(smem_u32(sm.a[s]));
+            const uint64_t ad = t.dw ? desc_mn_sw128(smem_u32(sm.a[s])) : umma_desc_sw128(smem_u32(sm.a[s]));
             const uint64_t bd = desc_mn_sw128(smem_u32(sm.b[s]));
 #pragma unroll
-            for (int j = 0; j < BK / 16; ++j) {   // 16 reduction steps: 2 row groups (MN-major) or 32 bytes (K-major)
-              umma_f16<CTAS>(d_tmem, ad + (uint64_t)(DW ? 128 * j : 2 * j), bd + (uint64_t)(128 * j), idesc, accum);
+            for (int j = 0; j < BK / 16; ++j) {
+              umma_f16<CTAS>(d_tmem, ad + (uint64_t)(astep * j), bd + (uint64_t)(128 * j), idesc, accum);
               accum = 1;
             }
             commit<CTAS>(&sm.empty[s]);
           }
-          if (ok && (CHAIN || u == hi - 1)) {
+          if (ok && (t.chain || u == t.hi - 1)) {
             commit<CTAS>(&sm.tmem_full[na & 1]);
             ++na;
           }
@@ -338,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   CTAS == 2 ? leader_addr(&sm.tmem_empty[1]) : smem_u32(&sm.tmem_empty[1])};
     uint32_t na = 0;
     int nst = 0;
+    bool last_bf16 = false;
     auto wait_full = [&]() {
       const bool got = mbar_wait(&sm.tmem_full[na & 1], (na >> 1) & 1, abort_flag, p.status, p.wait_cycles);
       __syncwarp();
@@ -356,67 +387,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++na;
     };
-    for (int tile = first; tile < tiles; tile += stride) {
-      int sp, it, jt, lo, hi;
-      place(tile, sp, it, jt, lo, hi);
-      const int i0 = (it * CTAS + rank) * BM + quarter * 32;   // this warp's 32 rows of the result
+    for (int tile = first; tile < p.tiles; tile += stride) {
+      const Place t = place(tile);
+      const Prob& q = p.pr[t.dw];
+      const int i0 = (t.it * CTAS + rank) * BM + quarter * 32;   // this warp's 32 rows of the result
       const int i = i0 + lane;
-      // where the rows go: a slice of partial sums, or segment `seg` of the result
-      int seg = 0, y = i0;
+      // where the rows go: a slice of partial sums, or segment `seg` of dW
+      int seg = 0, y = t.sp * q.g.slice_rows + i0;
       float sc = 1.0f;
-      if constexpr (DW) {
-        if (p.g.splits > 1 || p.g.seg_pitch == 0) {
-          y = sp * p.g.slice_rows + i0;
-        } else {
-          seg = i0 / p.g.seg_pitch;
-          y = i0 - seg * p.g.seg_pitch;
+      bool rows_ok = i0 < q.g.I;
+      if (t.dw) {
+        if (q.g.splits == 1) {
+          seg = i0 / q.g.seg_pitch;
+          y = i0 - seg * q.g.seg_pitch;
+          rows_ok = rows_ok && seg < 3 && q.g.out[seg < 3 ? seg : 0] != nullptr;
+          if (rows_ok && q.g.inv_gamma[seg] != nullptr) sc = 1.0f / fold_gamma(*q.g.inv_gamma[seg]);
         }
-        if (p.g.splits == 1 && p.g.inv_gamma[seg < 3 ? seg : 0] != nullptr)
-          sc = 1.0f / fold_gamma(*p.g.inv_gamma[seg < 3 ? seg : 0]);
       } else {
-        y = sp * p.g.slice_rows + i0;
-        if (!CHAIN && p.g.gamma[0] != nullptr) sc = *p.g.gamma[0];
-        if (p.g.row_scale != nullptr && i < p.g.I) sc *= p.g.row_scale[i];
+        if (!t.chain && q.g.gamma[0] != nullptr) sc = *q.g.gamma[0];
+        if (q.g.row_scale != nullptr && i < q.g.I) sc *= q.g.row_scale[i];
       }
-      const CUtensorMap* mo = seg == 0 ? &map_o0 : (seg == 1 ? &map_o1 : &map_o2);
-      const bool rows_ok = i0 < p.g.I && seg < 3 && p.g.out[seg < 3 ? seg : 0] != nullptr;
+      const CUtensorMap* mo = &maps.o[t.dw ? 1 + (rows_ok ? seg : 0) : 0];
+      const bool f32 = q.g.out_f32;
       const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-      const int jg = jt * BN + group * 128;                    // this warp's first column
+      const int jg = t.jt * BN + group * 128;                    // this warp's first column
 
+      // One staging area per warp: an fp32 box, or two bf16 ones. Boxes of both
+      // sizes may follow one another, so a bf16 box waits for all but the last
+      // store only when that was a bf16 one too.
       auto put = [&](const float (&out)[32], int j0) {
         uint8_t* buf = sm.stage[ew];
-        if constexpr (sizeof(OUT) == 2) {
-          if (lane == 0) bulk_wait_read_le1();
-          buf += (nst & 1) * 2048;
-        } else {
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        const bool two = !f32 && last_bf16;
+        if (lane == 0) {
+          if (two) bulk_wait_read_le1();
+          else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         }
         __syncwarp();
-        stage_row(buf, lane, out, (OUT*)nullptr);
+        if (f32) {
+          stage_row(buf, lane, out, (float*)nullptr);
+        } else {
+          buf += (nst & 1) * 2048;
+          stage_row(buf, lane, out, (bf16*)nullptr);
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (sizeof(OUT) == 4 && p.g.accumulate) tma_add_2d(mo, buf, j0, y);
+          if (f32 && q.g.accumulate) tma_add_2d(mo, buf, j0, y);
           else tma_store_2d(mo, buf, j0, y);
         }
+        last_bf16 = !f32;
         ++nst;
       };
 
-      if constexpr (CHAIN) {
+      if (KIND > 0 && t.chain) {
         float acc[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int j = 0; j < 32; ++j) acc[c][j] = 0.0f;
         bool alive = true;
-        for (int u = lo; u < hi; ++u) {
+        for (int u = t.lo; u < t.hi; ++u) {
           if (!(alive = wait_full())) break;
           float g = sc;
-          if (!DW && p.g.gamma[u / p.ups] != nullptr) g *= *p.g.gamma[u / p.ups];
+          if (!t.dw && q.g.gamma[u / q.ups] != nullptr) g *= *q.g.gamma[u / q.ups];
           const uint32_t tbase = tmem_base + lanes + (na & 1) * BN + group * 128;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (jg + 32 * c < p.g.J) {
+            if (jg + 32 * c < q.g.J) {
 #pragma unroll
               for (int h = 0; h < 32; h += 16) {
                 uint32_t r[16];
@@ -430,12 +467,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!alive) break;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          if (rows_ok && jg + 32 * c < p.g.J) put(acc[c], jg + 32 * c);
-      } else {
+          if (rows_ok && jg + 32 * c < q.g.J) put(acc[c], jg + 32 * c);
+      } else if (KIND < 2) {
         if (!wait_full()) break;
         const uint32_t tbase = tmem_base + lanes + (na & 1) * BN + group * 128;
         for (int c = 0; c < 4; ++c) {
-          if (jg + 32 * c >= p.g.J || !rows_ok) break;
+          if (jg + 32 * c >= q.g.J || !rows_ok) break;
           uint32_t r[32];
           tmem_ld32(tbase + 32 * c, r);
           float out[32];
@@ -464,18 +501,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-struct Maps {
-  CUtensorMap a, b, o[3];
-};
-
-template <bool DW, typename OUT, bool CHAIN, int CTAS>
+template <int KIND, int CTAS, int MODE>
 cudaError_t launch_form(const Maps& m, const KArgs& p, cudaStream_t stream) {
-  auto kern = bgemm_tc_kernel<DW, OUT, CHAIN, CTAS>;
+  auto kern = bgemm_tc_kernel<KIND, CTAS, MODE>;
   const size_t smem = sizeof(Smem<CTAS>) + 1024;
+  static_assert(sizeof(Smem<CTAS>) + 1024 <= 227 * 1024, "shared memory");
   static SmemOptIn opt;
   const cudaError_t e = opt.set(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const int groups = std::min(p.g.splits * p.i_tiles * p.j_tiles, num_sms() / CTAS);
+  const int groups = std::min(p.tiles, num_sms() / CTAS);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(groups * CTAS);
   cfg.blockDim = dim3(kThreads);
@@ -490,40 +524,97 @@ cudaError_t launch_form(const Maps& m, const KArgs& p, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CTAS == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, m.a, m.b, m.o[0], m.o[1], m.o[2], p);
+  return cudaLaunchKernelEx(&cfg, kern, m, p);
 }
 
-template <bool DW, typename OUT, bool CHAIN>
-cudaError_t launch_ctas(const Maps& m, const KArgs& p, cudaStream_t stream) {
-  return p.g.pair ? launch_form<DW, OUT, CHAIN, 2>(m, p, stream) : launch_form<DW, OUT, CHAIN, 1>(m, p, stream);
+template <int KIND, int CTAS>
+cudaError_t launch_mode(int mode, const Maps& m, const KArgs& p, cudaStream_t stream) {
+  if constexpr (KIND != 1)
+    if (mode == 1) return launch_form<KIND, CTAS, 1>(m, p, stream);
+  return mode == 0 ? launch_form<KIND, CTAS, 0>(m, p, stream) : launch_form<KIND, CTAS, 2>(m, p, stream);
+}
+
+bool is_chain(int planes, int nseg) { return planes > 1 || nseg > 1; }
+int chain_steps(int planes, int nseg) { return !is_chain(planes, nseg) ? 1 : planes > 1 ? kChainF32 : kChainBf16; }
+
+}  // namespace
+
+namespace {
+
+// Model of one product's time on one B200: groups (SMs, or pairs) take tiles in
+// turn; a tile takes its share of the reduction and a start-up; fp32 slices are
+// written and read again. Measured: a pair 0.435 us per 64 steps of 256 x 256
+// (1.43 PFLOP/s), an SM 0.60 us of 128 x 256, 1.5 us per tile.
+struct Model {
+  bool pair;
+  int groups;
+  double step_us, tile_us;
+  explicit Model(bool two) : pair(two) {
+    groups = two ? num_sms() / 2 : num_sms();
+    step_us = two ? 0.435 : 0.60;
+    tile_us = 1.5;
+  }
+  long long tiles(const BGemmShape& s) const {
+    return (long long)ceil_div(s.I, pair ? 2 * BM : BM) * ceil_div(s.J, BN);
+  }
+  double tile_time(const BGemmShape& s, int splits) const {
+    return (double)ceil_div(s.R, BK) * s.planes * s.nseg / splits * step_us + tile_us;
+  }
+};
+double slices_us(const BGemmShape& s, int splits, bool dw) {
+  return splits == 1 ? 0.0 : (dw ? 3.0 : 0.0) + (double)splits * s.I * s.J * 8 / 4e6;
+}
+const int kTry[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32};
+bool may_split(const BGemmShape& s, int splits) {   // at least 8 k-steps in each
+  return splits == 1 || (splits <= bgemm_units(s) && ceil_div(s.R, BK) * s.planes * s.nseg >= 8 * splits);
 }
 
 }  // namespace
 
-// Tile shape and number of splits, by a model of the time: rounds of tiles over
-// the SMs (pairs), each with its share of the reduction and a start-up, plus
-// the fp32 slices written and read again. Rates as measured on one B200.
-BGemmPlan bgemm_plan(int I, int J, int R, int planes, int nseg, int most) {
-  const bool chain = planes > 1 || nseg > 1;
-  const int cl = planes > 1 ? kChainF32 : kChainBf16;
-  const int nk = ceil_div(R, BK);
-  const int units = nseg * (chain ? ceil_div(nk, cl) : nk);
-  const double steps = (double)nk * planes * nseg;
-  BGemmPlan best = {false, 1};
+// Tile shape, splits, and whether both products go in one launch: they do when
+// all their tiles run at once (small products: one launch and one start-up
+// less, a one-token backward 29 -> 16 us), and not when they take rounds (the
+// 370M GLU's 540 us in four launches, 548 us in two: the operands of both then
+// compete for L2).
+BGemmPlan bgemm_plan(const BGemmShape& dx, const BGemmShape& dw) {
+  BGemmPlan best = {};
+  best.together = true;
   double best_t = 1e30;
   for (int pair = 0; pair < 2; ++pair) {
-    const double step_us = pair ? 0.48 : 0.60, start_us = 3.0;
-    const long long tiles = (long long)ceil_div(I, pair ? 2 * BM : BM) * ceil_div(J, BN);
-    const int groups = pair ? num_sms() / 2 : num_sms();
-    for (int s = 1; s <= most && s <= units; ++s) {
-      if (s > 1 && steps / s < 8) break;
-      const long long rounds = (tiles * s + groups - 1) / groups;
-      double t = rounds * (steps / s * step_us + start_us);
-      if (s > 1) t += 2.0 + (double)s * I * J * 8 / 4e6;
-      if (t < best_t) {
-        best_t = t;
-        best.pair = pair != 0;
-        best.splits = s;
+    const Model m(pair != 0);
+    const long long n0 = m.tiles(dx), n1 = m.tiles(dw);
+    if (n0 + n1 > m.groups) continue;
+    for (int s0 : kTry) {
+      if (n0 * s0 + n1 > m.groups || !may_split(dx, s0)) break;
+      for (int s1 : kTry) {
+        if (n0 * s0 + n1 * s1 > m.groups || !may_split(dw, s1)) break;
+        const double t = std::max(m.tile_time(dx, s0), m.tile_time(dw, s1)) + slices_us(dx, s0, false) +
+                         slices_us(dw, s1, true);
+        if (t < best_t) {
+          best_t = t;
+          best.pair[0] = best.pair[1] = pair != 0;
+          best.splits[0] = s0;
+          best.splits[1] = s1;
+        }
+      }
+    }
+  }
+  if (best_t < 1e30) return best;
+  best.together = false;
+  const BGemmShape* sh[2] = {&dx, &dw};
+  for (int i = 0; i < 2; ++i) {
+    best_t = 1e30;
+    for (int pair = 0; pair < 2; ++pair) {
+      const Model m(pair != 0);
+      const long long n = m.tiles(*sh[i]);
+      for (int s : kTry) {
+        if (s > 1 && (n * s > 4 * m.groups || !may_split(*sh[i], s))) break;
+        const double t = (double)((n * s + m.groups - 1) / m.groups) * m.tile_time(*sh[i], s) + slices_us(*sh[i], s, i == 1);
+        if (t < best_t) {
+          best_t = t;
+          best.pair[i] = pair != 0;
+          best.splits[i] = s;
+        }
       }
     }
   }
@@ -532,49 +623,80 @@ BGemmPlan bgemm_plan(int I, int J, int R, int planes, int nseg, int most) {
 
 int bgemm_slice_rows(int I) { return ceil_div(I, 32) * 32; }
 
-int bgemm_units(int R, int planes, int nseg) {
-  const int nk = ceil_div(R, BK);
-  return nseg * (planes > 1 ? ceil_div(nk, kChainF32) : nseg > 1 ? ceil_div(nk, kChainBf16) : nk);
+int bgemm_units(const BGemmShape& s) {
+  return s.nseg * ceil_div(ceil_div(s.R, BK), chain_steps(s.planes, s.nseg));
 }
 
-cudaError_t launch_bgemm_tc(const BGemmArgs& g, int* status, cudaStream_t stream) {
-  if (g.I == 0 || g.J == 0) return cudaSuccess;
+cudaError_t launch_bgemm_tc(const BGemmArgs* dx, const BGemmArgs* dw, bool pair, int* status, cudaStream_t stream) {
   Maps m;
-  const uint64_t a_rows = (uint64_t)(g.planes - 1) * g.a_plane + (g.dw ? g.R : g.I);
-  const uint64_t a_cols = g.dw ? g.I : (uint64_t)g.nseg * g.R;
+  KArgs p = {};
+  const BGemmArgs* args[2] = {dx, dw};
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  if (!make_tma_2d(&m.a, g.a, BF, 2, a_cols, a_rows, 64, g.dw ? 64 : BM, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)g.lda * 2) ||
-      !make_tma_2d(&m.b, g.b, BF, 2, (uint64_t)g.J, (uint64_t)g.nseg * g.R, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B,
-                   (uint64_t)g.ldb * 2))
-    return cudaErrorInvalidValue;
-  const bool f32 = g.out_f32;
-  void* any = g.out[0] != nullptr ? g.out[0] : (g.out[1] != nullptr ? g.out[1] : g.out[2]);
-  for (int i = 0; i < 3; ++i) {
-    if (i > 0 && g.out[i] == nullptr && g.out[0] != nullptr) {   // a segment without an output is skipped
-      m.o[i] = m.o[0];
-      continue;
-    }
-    const uint64_t rows = g.seg_pitch != 0 && g.splits == 1 ? (uint64_t)g.seg_rows : (uint64_t)g.splits * g.slice_rows;
-    if (!make_tma_2d(&m.o[i], g.out[i] != nullptr ? g.out[i] : any,
-                     f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : BF, f32 ? 4 : 2, (uint64_t)g.J, rows, 32, 32,
-                     f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+  bool chain[2] = {};
+  int tiles[2] = {};
+  for (int d = 0; d < 2; ++d) {
+    if (args[d] == nullptr || args[d]->sh.I == 0 || args[d]->sh.J == 0) continue;
+    const BGemmArgs& g = *args[d];
+    const BGemmShape& s = g.sh;
+    const uint64_t a_rows = (uint64_t)(s.planes - 1) * g.a_plane + (d ? s.R : s.I);
+    const uint64_t a_cols = d ? s.I : (uint64_t)s.nseg * s.R;
+    if (!make_tma_2d(&m.a[d], g.a, BF, 2, a_cols, a_rows, 64, d ? 64 : BM, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)g.lda * 2) ||
+        !make_tma_2d(&m.b[d], g.b, BF, 2, (uint64_t)s.J, (uint64_t)s.nseg * s.R, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B,
+                     (uint64_t)g.ldb * 2))
       return cudaErrorInvalidValue;
+    for (int i = 0; i < (d ? 3 : 1); ++i) {
+      if (g.out[i] == nullptr) continue;   // a segment without an output is skipped
+      const uint64_t rows = d && g.splits == 1 ? (uint64_t)g.seg_rows : (uint64_t)g.splits * g.slice_rows;
+      if (!make_tma_2d(&m.o[d + i], g.out[i], g.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : BF, g.out_f32 ? 4 : 2,
+                       (uint64_t)s.J, rows, 32, 32, g.out_f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+        return cudaErrorInvalidValue;
+    }
+    Prob& q = p.pr[d];
+    q.g.a_plane = g.a_plane;
+    q.g.planes = s.planes;
+    q.g.I = s.I;
+    q.g.J = s.J;
+    q.g.R = s.R;
+    q.g.splits = g.splits;
+    q.g.slice_rows = g.slice_rows;
+    q.g.out_f32 = g.out_f32;
+    q.g.accumulate = g.accumulate;
+    q.g.seg_pitch = g.seg_pitch;
+    for (int i = 0; i < 3; ++i) {
+      q.g.out[i] = g.out[i];
+      q.g.gamma[i] = g.gamma[i];
+      q.g.inv_gamma[i] = g.inv_gamma[i];
+    }
+    q.g.row_scale = g.row_scale;
+    q.i_tiles = ceil_div(s.I, pair ? 2 * BM : BM);
+    q.j_tiles = ceil_div(s.J, BN);
+    q.nk = ceil_div(s.R, BK);
+    chain[d] = is_chain(s.planes, s.nseg);
+    q.cl = chain_steps(s.planes, s.nseg);
+    q.ups = ceil_div(q.nk, q.cl);
+    q.units = s.nseg * q.ups;
+    if (g.splits < 1 || g.splits > q.units) return cudaErrorInvalidValue;
+    tiles[d] = g.splits * q.i_tiles * q.j_tiles;
   }
-  const bool chain = g.planes > 1 || g.nseg > 1;
-  KArgs p;
-  p.g = g;
-  p.i_tiles = ceil_div(g.I, g.pair ? 2 * BM : BM);
-  p.j_tiles = ceil_div(g.J, BN);
-  p.nk = ceil_div(g.R, BK);
-  p.cl = !chain ? 1 : g.planes > 1 ? kChainF32 : kChainBf16;
-  p.ups = ceil_div(p.nk, p.cl);
-  p.units = g.nseg * p.ups;
+  p.tiles0 = tiles[0];
+  p.tiles = tiles[0] + tiles[1];
+  if (p.tiles == 0) return cudaSuccess;
   p.status = status;
   p.wait_cycles = wait_limit_cycles();
-  if (g.splits < 1 || g.splits > p.units) return cudaErrorInvalidValue;
-  if (!g.dw) return chain ? launch_ctas<false, float, true>(m, p, stream) : launch_ctas<false, float, false>(m, p, stream);
-  if (chain) return launch_ctas<true, float, true>(m, p, stream);   // fp32 gradients: fp32 result
-  return f32 ? launch_ctas<true, float, false>(m, p, stream) : launch_ctas<true, bf16, false>(m, p, stream);
+  const int kind = chain[1] ? 2 : chain[0] ? (args[0]->sh.planes > 1 ? 2 : 1) : 0;
+  const int mode = tiles[1] == 0 ? 0 : tiles[0] == 0 ? 1 : 2;
+  if (pair) {
+    switch (kind) {
+      case 0: return launch_mode<0, 2>(mode, m, p, stream);
+      case 1: return launch_mode<1, 2>(mode, m, p, stream);
+      default: return launch_mode<2, 2>(mode, m, p, stream);
+    }
+  }
+  switch (kind) {
+    case 0: return launch_mode<0, 1>(mode, m, p, stream);
+    case 1: return launch_mode<1, 1>(mode, m, p, stream);
+    default: return launch_mode<2, 1>(mode, m, p, stream);
+  }
 }
 
 }  // namespace mmf

@@ -161,35 +161,39 @@ cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, m
                                cudaStream_t stream);
 
 // bf16 training products (bgemm_tc.cu), D fp32 accumulated:
-//   dw = false: D[i, j] = row_scale[i] sum_g gamma[g] sum_r A[i, g R + r] B[g R + r, j]
-//               over nseg segments g (nseg > 1: R a multiple of 64), A [I, nseg R]
-//   dw = true:  D[i, j] = sum_r A[r, i] B[r, j] (/ fold_gamma(inv_gamma)), A [R, I]
+//   dx: D[i, j] = row_scale[i] sum_g gamma[g] sum_r A[i, g R + r] B[g R + r, j]
+//       over nseg segments g (nseg > 1: R a multiple of 64), A [I, nseg R]
+//   dw: D[i, j] = sum_r A[r, i] B[r, j] (/ fold_gamma(inv_gamma)), A [R, I]
 // B is [nseg R, J]; J a multiple of 16; lda, ldb multiples of 8 elements.
+struct BGemmShape {
+  int I, J, R, planes, nseg;   // I = 0: no such product
+};
 struct BGemmArgs {
-  bool dw, pair;            // pair: tiles of two SMs (bgemm_plan)
+  BGemmShape sh;
   const void* a;            // bf16; plane p starts p * a_plane rows further
-  int lda, a_plane, planes;
+  int lda, a_plane;
   const void* b;            // bf16
   int ldb;
-  int I, J, R, nseg;
   int splits;               // > 1: fp32 slices [splits][slice_rows][J] at out[0], to be added up by the reader
-  int slice_rows;           // dw = false, or splits > 1: bgemm_slice_rows(I)
+  int slice_rows;           // dx, or splits > 1: bgemm_slice_rows(I)
   void* out[3];
-  bool out_f32;             // dw, splits 1: fp32 or bf16 result (else always fp32)
+  bool out_f32;             // dx, or splits > 1: true; dw: fp32 or bf16 result
   bool accumulate;          // fp32 output: add to what is there
   int seg_pitch, seg_rows;  // dw, splits 1: row i goes to out[i / seg_pitch] row i % seg_pitch if < seg_rows
-  const float* gamma[3];    // dw = false: device scalars or null
-  const float* row_scale;   // dw = false: [I] or null
+  const float* gamma[3];    // dx: device scalars or null
+  const float* row_scale;   // dx: [I] or null
   const float* inv_gamma[3];  // dw, splits 1: device scalars or null
 };
 struct BGemmPlan {
-  bool pair;
-  int splits;
+  bool together;            // one launch for both
+  bool pair[2];             // tiles of two SMs: dx, dw
+  int splits[2];
 };
-BGemmPlan bgemm_plan(int I, int J, int R, int planes, int nseg, int most);
-int bgemm_units(int R, int planes, int nseg);   // the most splits there can be
+BGemmPlan bgemm_plan(const BGemmShape& dx, const BGemmShape& dw);
+int bgemm_units(const BGemmShape& s);   // the most splits there can be
 int bgemm_slice_rows(int I);
-cudaError_t launch_bgemm_tc(const BGemmArgs& g, int* status, cudaStream_t stream);
+// Either product, or both in one launch (null: left out).
+cudaError_t launch_bgemm_tc(const BGemmArgs* dx, const BGemmArgs* dw, bool pair, int* status, cudaStream_t stream);
 
 // Operand preparation for those products, one launch (train.cu).
 struct PrepArgs {

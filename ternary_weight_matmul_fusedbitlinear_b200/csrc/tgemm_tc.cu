@@ -61,28 +61,30 @@ constexpr uint32_t kTmemCols = 512;
 // epilogue warp has 4 staging buffers, one per 32-column chunk of its half
 // tile, into which the whole tile's residual is loaded before the tile's
 // accumulator is ready.
-// GB (GLU backward): the ring is 3 deep to make room for one fp32 box and one
-// box of codes per epilogue warp, which TMA fills ahead of the accumulator.
+// GB (GLU backward): 16 epilogue warps work on 16-column boxes; the ring is 3
+// deep to make room for one fp32 box and one box of codes per epilogue warp,
+// which TMA fills ahead of the accumulator.
 template <int OB, bool UNP, bool RB = false, bool GB = false>
 struct __align__(1024) SmemLayout {
   static constexpr int NS = RB || GB ? 3 : (UNP ? (OB == 2 ? 4 : 3) : (OB == 2 ? 4 : 3));
   static constexpr int NSTG = RB ? HALF / kEpiChunk : 2;   // staging buffers per epilogue warp
   static constexpr int NBU = UNP ? NS : NB;        // int8 weight tiles: per TMA stage (UNP) or unpack ring
   static constexpr int NBP = UNP ? 1 : NS;         // packed weight tiles (unused with UNP)
-  static constexpr int kStageBytes = 32 * kEpiChunk * OB;
+  static constexpr int EW = GB ? 16 : kEpiWarps;
+  static constexpr int kStageBytes = GB ? 1024 : 32 * kEpiChunk * OB;
   uint8_t a[NS][A_BYTES];                          // 1024-aligned: SW128 atoms
   uint8_t bu[NBU][BU_BYTES];                       // 1024-aligned: SW128 atoms
-  uint8_t stage[kEpiWarps][NSTG][kStageBytes];     // epilogue staging (1024-aligned)
+  uint8_t stage[EW][NSTG][kStageBytes];     // epilogue staging (1024-aligned)
   uint32_t bp[NBP][UNP ? 4 : BP_BYTES / 4];
-  alignas(GB ? 1024 : 16) uint8_t gx[GB ? kEpiWarps : 1][GB ? 4096 : 16];  // GB: 32 x 32 fp32 gradients (1024-aligned)
-  alignas(GB ? 1024 : 16) uint8_t gq[GB ? kEpiWarps : 1][GB ? 1024 : 16];  // GB: 32 x 32 codes
+  alignas(GB ? 1024 : 16) uint8_t gx[GB ? EW : 1][GB ? 2048 : 16];  // GB: 32 x 16 fp32 gradients
+  alignas(GB ? 1024 : 16) uint8_t gq[GB ? EW : 1][GB ? 512 : 16];   // GB: 32 x 16 codes
   uint64_t tma_full[NS];
   uint64_t tma_empty[NS];
   uint64_t bu_full[NB];
   uint64_t bu_empty[NB];
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
-  uint64_t res_full[kEpiWarps][NSTG];              // residual box landed in a staging buffer
+  uint64_t res_full[EW][NSTG];              // residual box landed in a staging buffer
   uint64_t mma_drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -116,6 +118,12 @@ __device__ __forceinline__ float exp2_fast(float z) {
   return r;
 }
 
+__device__ __forceinline__ float rcp_fast(float z) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(z));
+  return r;
+}
+
 // acc = raw - qs as a float, by integer and float adds (the conversion
 // instruction issues at an eighth of their rate): |acc| <= 127 K < 2^22 makes
 // the sum with 1.5 * 2^23 exact in the mantissa.
@@ -123,21 +131,22 @@ constexpr int kMaxMagicK = 32768;
 __device__ __forceinline__ float acc_magic(uint32_t raw, int off) {   // off = 0x4B400000 - qs
   return __uint_as_float(raw + (uint32_t)off) - 12582912.0f;
 }
-// 32 accumulators times sc.
-__device__ __forceinline__ void scaled32(const uint32_t (&r)[32], int qs, float sc, bool magic, float (&z)[32]) {
+// W accumulators times sc.
+template <int W>
+__device__ __forceinline__ void scaled(const uint32_t (&r)[W], int qs, float sc, bool magic, float (&z)[W]) {
   if (magic) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) z[j] = acc_magic(r[j], 0x4B400000 - qs) * sc;
+    for (int j = 0; j < W; ++j) z[j] = acc_magic(r[j], 0x4B400000 - qs) * sc;
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) z[j] = (float)((int)r[j] - qs) * sc;
+    for (int j = 0; j < W; ++j) z[j] = (float)((int)r[j] - qs) * sc;
   }
 }
 
 // 32 logits of one token in log2 units, columns n0.. of the segment (past N: -inf).
 __device__ __forceinline__ void logits32(const uint32_t (&r)[32], int qs, float sc2, bool magic, const float* bias,
                                          int n0, int N, float (&z)[32]) {
-  scaled32(r, qs, sc2, magic, z);
+  scaled(r, qs, sc2, magic, z);
   if (bias != nullptr) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
@@ -150,12 +159,14 @@ __device__ __forceinline__ void logits32(const uint32_t (&r)[32], int qs, float 
   }
 }
 
-// Plane `pl` of g = g0 + g1 + g2 with bf16 planes: the next 8 bits of what the planes before left.
-__device__ __forceinline__ void take_plane(float (&g)[32], float (&out)[32]) {
+// The next bf16 plane of g = g0 + g1 + g2: 8 bits of what the planes before
+// left (the last plane is rounded where it is stored).
+template <int W>
+__device__ __forceinline__ void take_plane(float (&g)[W], float (&out)[W], bool last) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    out[j] = round_to<bf16>(g[j]);
-    g[j] -= out[j];
+  for (int j = 0; j < W; ++j) {
+    out[j] = last ? g[j] : round_to<bf16>(g[j]);
+    if (!last) g[j] -= out[j];
   }
 }
 
@@ -177,8 +188,11 @@ __device__ __forceinline__ void half_source(const TcArgs& p, Epi epi, int nt, in
   }
 }
 
+// The GLU backward has 16 epilogue warps and no unpack warps.
+__host__ __device__ constexpr int threads_of(Epi e) { return e == Epi::kGluBwd ? (kEpiWarp0 + 16) * 32 : kThreads; }
+
 template <Epi EPI, typename T, bool UNP, bool RB = false>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(EPI), 1)
     tgemm_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b0,
                     const __grid_constant__ CUtensorMap map_b1, const __grid_constant__ CUtensorMap map_b2,
                     const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_res,
@@ -206,9 +220,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&sm.tmem_full[a], 1);
-      mbar_init(&sm.tmem_empty[a], kEpiWarps * 32);
+      mbar_init(&sm.tmem_empty[a], Smem::EW * 32);
     }
-    for (int w = 0; w < kEpiWarps; ++w)
+    for (int w = 0; w < Smem::EW; ++w)
       for (int c = 0; c < Smem::NSTG; ++c) mbar_init(&sm.res_full[w][c], 1);
     mbar_init(&sm.mma_drain, 1);
     sm.abort_flag = 0;
@@ -296,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit(&sm.mma_drain);
       mbar_drain(&sm.mma_drain, 0, p.wait_cycles);
     }
-  } else if (warp >= kUnpackWarp0) {
+  } else if (warp >= kEpiWarp0 + Smem::EW) {
     // ------------------------------------------------------------ unpack 2-bit codes to int8 (idle with UNP)
     if constexpr (!UNP) {
     // 512 (row, half-row) units per K-step; unit id = tid + 128 i reads the 16
@@ -340,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue (8 warps)
-    const int ew = warp - kEpiWarp0;              // 0..7
+    const int ew = warp - kEpiWarp0;              // 0..7 (GLU backward: 0..15)
     const int quarter = warp & 3;                 // TMEM lanes 32*quarter .. +31
     const int group = ew >> 2;                    // which half of the columns this warp takes
     const int row_in_tile = quarter * 32 + lane;
@@ -364,16 +378,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool alive = true;
     uint32_t res_pending = 0;                     // RB: this tile's residual boxes not yet waited on
-    // GLU backward: this warp's box of dx^ (map_res) and of p's codes (map_b2) for chunk cc of a tile.
+    // GLU backward: this warp's box of dx^ (map_res) and of p's codes (map_b2) for
+    // 16-column chunk cc (0, 1) of its 32 columns of a tile.
     auto load_chunk = [&](int tile, int cc) {
-      const int n0 = tile % p.n_tiles * HALF + 32 * (group * 2 + cc), y = tile / p.n_tiles * BM + quarter * 32;
-      mbar_arrive_expect_tx(&sm.res_full[ew][0], 4096 + 1024);
+      const int n0 = tile % p.n_tiles * HALF + 32 * group + 16 * cc, y = tile / p.n_tiles * BM + quarter * 32;
+      mbar_arrive_expect_tx(&sm.res_full[ew][0], 2048 + 512);
       tma_load_2d(sm.gx[ew], &map_res, n0, y, &sm.res_full[ew][0]);
       tma_load_2d(sm.gq[ew], &map_b2, n0, y, &sm.res_full[ew][0]);
     };
-    // The first tile from `tile` on in which this warp has a chunk.
+    // The first tile from `tile` on in which this warp has columns.
     auto next_tile = [&](int tile) {
-      while (tile < n_tiles_total && tile % p.n_tiles * HALF + 64 * group >= p.t.plane_cols) tile += gridDim.x;
+      while (tile < n_tiles_total && tile % p.n_tiles * HALF + 32 * group >= p.t.plane_cols) tile += gridDim.x;
       return tile;
     };
     uint32_t nload = 0;
@@ -499,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int pl = 0; pl < kPlanes; ++pl) {
               float out[32];
-              take_plane(z, out);
+              take_plane(z, out, pl == kPlanes - 1);
               uint8_t* buf;
               claim(buf);
               stage_row(buf, lane, out, (bf16*)nullptr);
@@ -509,111 +524,86 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else if constexpr (EPI == Epi::kGluBwd) {
         // u and v again from the codes; dp from the down projection's dx^ and
-        // its norm (read through the codes of p); du, dv over the token's scale.
-        const float sc_u = *p.g.gamma[0] * inv_s, sc_v = *p.g.gamma[1] * inv_s;
+        // its norm (read through the codes of p); du, dv over the token's scale
+        // and times gamma. Per element about 25 instructions.
         const float fu = fold_gamma(*p.g.gamma[0]) * inv_s, fv = fold_gamma(*p.g.gamma[1]) * inv_s;
-        // dp = rinv_p (gain dx^ - n c): without a gain n = q / s_p, so dp = k1 dx^ - k2 q
+        const float sc_u = *p.g.gamma[0] * inv_s, sc_v = *p.g.gamma[1] * inv_s;
+        // dp = rinv_p (gain dx^ - n c): without a gain n = q / s_p, so dp = k1 dx^ + kq q
         const float k1 = row_ok ? p.t.rp[m] : 0.0f;
-        const float inv_sp = row_ok ? 1.0f / p.t.sp[m] : 0.0f, kc = row_ok ? k1 * p.t.cp[m] : 0.0f;
+        const float kq = row_ok ? -k1 * p.t.cp[m] / p.t.sp[m] : 0.0f;
         const bool magic = p.g.K <= kMaxMagicK;
-        for (int cc = 0; cc < 2; ++cc) {
-          const int c = group * 2 + cc;
-          const int n0 = nt * HALF + 32 * c;
-          if (n0 >= p.t.plane_cols) break;
+        const int c0 = nt * HALF + 32 * group;
+        for (int cc = 0; cc < 2 && c0 < p.t.plane_cols; ++cc) {
+          const int n0 = c0 + 16 * cc;
+          const uint32_t tcol = tbase + 32 * group + 16 * cc;
           const bool ok = mbar_wait(&sm.res_full[ew][0], nres & 1, abort_flag, p.status, p.wait_cycles);
           if (!__all_sync(0xffffffffu, ok)) { alive = false; break; }
           ++nres;
-          float dp[32];
-          {
-            const uint8_t* gx = sm.gx[ew];
-            const uint4* gq = reinterpret_cast<const uint4*>(sm.gq[ew] + lane * 32);
-            const float kq = -kc * inv_sp;
+          uint32_t ru[16], rv[16];
+          tmem_ld16_begin(tcol, ru);
+          tmem_ld16_begin(tcol + HALF, rv);
+          float dp[16];
+          const uint4 q16 = *reinterpret_cast<const uint4*>(sm.gq[ew] + lane * 16);
+          const uint32_t* qw = &q16.x;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 q16 = gq[h];
-              const uint32_t* qw = &q16.x;
+          for (int e = 0; e < 4; ++e) {
+            const float4 d4 = *reinterpret_cast<const float4*>(sm.gx[ew] + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4));
+            const float* d = &d4.x;
+            const uint32_t u4 = qw[e] ^ 0x80808080u;   // q + 128, unsigned bytes
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int j = 16 * h + 4 * e;
-                const float4 d4 = *reinterpret_cast<const float4*>(gx + lane * 128 + (((j / 4) ^ (lane & 7)) << 4));
-                const float* d = &d4.x;
-                const uint32_t u4 = qw[e] ^ 0x80808080u;   // q + 128, unsigned bytes
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {              // 2^23 + byte, less 2^23 + 128
-                  const float qf = __uint_as_float(__byte_perm(u4, 0x4B000000u, 0x7650 + b)) - 8388736.0f;
-                  dp[j + b] = fmaf(kq, qf, k1 * d[b]);
-                }
-              }
-            }
-            if (p.t.gain_p != nullptr) {   // n = xt / gain: k1 gain dx^ - kc xt / gain
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint4 q16 = gq[h];
-                const uint32_t* qw = &q16.x;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int j = 16 * h + 4 * e;
-                  const float4 d4 = *reinterpret_cast<const float4*>(gx + lane * 128 + (((j / 4) ^ (lane & 7)) << 4));
-                  const float* d = &d4.x;
-                  const uint32_t u4 = qw[e] ^ 0x80808080u;
-#pragma unroll
-                  for (int b = 0; b < 4; ++b) {
-                    const float qf = __uint_as_float(__byte_perm(u4, 0x4B000000u, 0x7650 + b)) - 8388736.0f;
-                    const float gn = n0 + j + b < p.g.N ? __ldg(p.t.gain_p + n0 + j + b) : 1.0f;
-                    dp[j + b] = k1 * gn * d[b] + (gn != 0.0f ? kq * qf / gn : 0.0f);
-                  }
-                }
+            for (int b = 0; b < 4; ++b) {              // 2^23 + byte, less 2^23 + 128
+              const float qf = __uint_as_float(__byte_perm(u4, 0x4B000000u, 0x7650 + b)) - 8388736.0f;
+              if (p.t.gain_p == nullptr) {
+                dp[4 * e + b] = fmaf(kq, qf, k1 * d[b]);
+              } else {                                 // n = xt / gain
+                const float gn = n0 + 4 * e + b < p.g.N ? __ldg(p.t.gain_p + n0 + 4 * e + b) : 1.0f;
+                dp[4 * e + b] = k1 * gn * d[b] + (gn != 0.0f ? kq * qf / gn : 0.0f);
               }
             }
           }
           __syncwarp();
           {   // this warp's next chunk into the buffers just read
-            int tn = tile, cn = cc + 1;
-            if (cn == 2 || n0 + 32 >= p.t.plane_cols) {
-              tn = next_tile(tile + gridDim.x);
-              cn = 0;
-            }
+            const int tn = cc == 0 ? tile : next_tile(tile + gridDim.x);
             if (tn < n_tiles_total) {
               ++nload;
               if (lane == 0) {
                 fence_proxy_async_smem();
-                load_chunk(tn, cn);
+                load_chunk(tn, cc ^ 1);
               }
             }
           }
-          uint32_t ru[32], rv[32];
-          tmem_ld32(tbase + 32 * c, ru);
-          tmem_ld32(tbase + HALF + 32 * c, rv);
-          float du[32], dv[32];
-          scaled32(ru, qs, sc_u, magic, du);
-          scaled32(rv, qs, sc_v, magic, dv);
+          tmem_wait(ru);
+          tmem_wait(rv);
+          float du[16], dv[16];
+          scaled(ru, qs, sc_u, magic, du);
+          scaled(rv, qs, sc_v, magic, dv);
           if (p.g.bias[0] != nullptr)
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < 16; ++j)
               if (n0 + j < p.g.N) du[j] += __ldg(p.g.bias[0] + n0 + j);
           if (p.g.bias[1] != nullptr)
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < 16; ++j)
               if (n0 + j < p.g.N) dv[j] += __ldg(p.g.bias[1] + n0 + j);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {   // past N and M dp is 0 (boxes read zeros there), and so are du, dv
+          for (int j = 0; j < 16; ++j) {   // past N and M dp is 0 (boxes read zeros there), and so are du, dv
             const float u = du[j], v = dv[j];
-            const float sg = __fdividef(1.0f, 1.0f + exp2_fast(-u * kLog2e));
+            const float sg = rcp_fast(1.0f + exp2_fast(-u * kLog2e));
             const float us = u * sg;
-            du[j] = dp[j] * fu * (v * fmaf(us, 1.0f - sg, sg));
-            dv[j] = dp[j] * fv * us;
+            du[j] = dp[j] * (v * fmaf(-us, sg, sg + us)) * fu;
+            dv[j] = dp[j] * us * fv;
           }
 #pragma unroll
           for (int pl = 0; pl < kPlanes; ++pl) {
-            float out[32];
+            float out[16];
             uint8_t* buf;
-            take_plane(du, out);
+            take_plane(du, out, pl == kPlanes - 1);
             claim(buf);
-            stage_row(buf, lane, out, (bf16*)nullptr);
+            stage_row16(buf, lane, out);
             release(n0, pl * p.t.plane_rows + y0, buf);
-            take_plane(dv, out);
+            take_plane(dv, out, pl == kPlanes - 1);
             claim(buf);
-            stage_row(buf, lane, out, (bf16*)nullptr);
+            stage_row16(buf, lane, out);
             release(p.t.plane_cols + n0, pl * p.t.plane_rows + y0, buf);
           }
         }
@@ -712,8 +702,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <class S>
 constexpr bool tma_aligned() {
   return offsetof(S, a) % 1024 == 0 && offsetof(S, bu) % 1024 == 0 && offsetof(S, stage) % 1024 == 0 &&
-         offsetof(S, bp) % 128 == 0 && offsetof(S, gx) % (sizeof(S::gx) >= 4096 ? 1024 : 16) == 0 &&
-         offsetof(S, gq) % (sizeof(S::gq) >= 1024 ? 128 : 16) == 0;
+         offsetof(S, bp) % 128 == 0 && offsetof(S, gx) % (sizeof(S::gx) > 16 ? 1024 : 16) == 0 &&
+         offsetof(S, gq) % (sizeof(S::gq) > 16 ? 128 : 16) == 0;
 }
 
 template <Epi EPI, typename T, bool UNP, bool RB = false>
@@ -728,7 +718,7 @@ cudaError_t launch_mapped(const CUtensorMap& ma, const CUtensorMap (&mb)[3], con
   if (e != cudaSuccess) return e;
   const int tiles = p.m_tiles * p.n_tiles;
   const int grid = std::min(tiles, num_sms());
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, stream, ma, mb[0], mb[1], mb[2], mo, mr, p);
+  return launch_pdl(kern, dim3(grid), dim3(threads_of(EPI)), smem, stream, ma, mb[0], mb[1], mb[2], mo, mr, p);
 }
 
 template <Epi EPI, typename T, bool UNP, bool RB = false>
@@ -819,13 +809,14 @@ cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, m
   mo = ma;   // kLse stores no tile
   if (epi != Epi::kLse &&
       !make_tma_2d(&mo, a.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)a.ldo, (uint64_t)planes * t.plane_rows,
-                   kEpiChunk, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+                   epi == Epi::kGluBwd ? 16 : kEpiChunk, 32,
+                   epi == Epi::kGluBwd ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   CUtensorMap mr = mo;
-  if (epi == Epi::kGluBwd) {   // dx^ and the codes of the down projection's input, 32 x 32 boxes
-    if (!make_tma_2d(&mr, t.dxh, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, (uint64_t)a.N, (uint64_t)a.M, 32, 32,
-                     CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tma_2d(&mb[2], t.qp, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.N, (uint64_t)a.M, 32, 32,
+  if (epi == Epi::kGluBwd) {   // dx^ and the codes of the down projection's input, 32-row x 16-column boxes
+    if (!make_tma_2d(&mr, t.dxh, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, (uint64_t)a.N, (uint64_t)a.M, 16, 32,
+                     CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !make_tma_2d(&mb[2], t.qp, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.N, (uint64_t)a.M, 16, 32,
                      CU_TENSOR_MAP_SWIZZLE_NONE))
       return cudaErrorInvalidValue;
   }

@@ -142,9 +142,69 @@ __device__ __forceinline__ void norm4(const NormBackArgs& a, size_t at, int k, f
   }
 }
 
-// WPR warps per row, WPR * 128 * NV columns at most; the row's dx^ stays in
-// registers between the mean and the result (its codes are read again from L1).
-// NV = 0: rows of any length, read twice.
+// Rows of one slice, read through the codes, without a gain (most calls): every
+// load of the row is issued before the first is used, with no branch between
+// them (a loop over slices there made them wait for one another: 112 us for
+// 16384 x 2816, 6 us a load), and kept in registers. WPR warps per row of at
+// most WPR * 128 * NV columns.
+template <typename T, int WPR, int NV, bool STAT, bool RES>
+__global__ void __launch_bounds__(kThreads) norm_back_plain_kernel(const NormBackArgs a) {
+  __shared__ float red[kThreads / 32];
+  pdl_trigger();
+  pdl_wait();
+  constexpr int kRows = kThreads / 32 / WPR, kLanes = 32 * WPR;
+  const int lane = threadIdx.x % kLanes, warp = threadIdx.x >> 5;
+  const int row = min(blockIdx.x * kRows + (int)threadIdx.x / kLanes, a.M - 1);   // a tail repeats the last row
+  const size_t base = (size_t)row * a.K;
+  float v[NV][4], d[RES ? NV : 1][4];
+  int w[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int k = (i * kLanes + lane) * 4;
+    const size_t at = base + (k < a.K ? k : 0);
+    ld4(a.dxh + at, v[i]);
+    w[i] = *reinterpret_cast<const int*>(a.q + at);
+    if constexpr (RES) ld4(static_cast<const T*>(a.dres) + at, d[i]);
+  }
+  const float inv_s = 1.0f / a.scale[row], rinv = a.rinv[row];
+  float dot = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float part = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part = fmaf(v[i][j], (float)((w[i] << (24 - 8 * j)) >> 24), part);
+    dot += (i * kLanes + lane) * 4 < a.K ? part : 0.0f;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 31) == 0) red[warp] = dot;
+    __syncthreads();
+    dot = 0.0f;
+    for (int i = 0; i < WPR; ++i) dot += red[warp / WPR * WPR + i];
+  }
+  const float c = dot * inv_s / (float)a.K;
+  if constexpr (STAT) {
+    if (lane == 0) a.cmean[row] = c;
+  } else {
+    const float ci = c * inv_s;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int k = (i * kLanes + lane) * 4;
+      float o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        o[j] = rinv * fmaf(-ci, (float)((w[i] << (24 - 8 * j)) >> 24), v[i][j]);
+        if constexpr (RES) o[j] += d[i][j];
+      }
+      if (k < a.K) st4(static_cast<T*>(a.dx) + base + k, o);
+    }
+  }
+}
+
+// Any other row: slices, gain, x. WPR warps per row, WPR * 128 * NV columns at
+// most; the row's dx^ stays in registers between the mean and the result (its
+// codes are read again from L1). NV = 0: rows of any length, read twice.
 template <typename T, int WPR, int NV, bool STAT>
 __global__ void __launch_bounds__(kThreads) norm_back_kernel(const NormBackArgs a) {
   __shared__ float red[kThreads / 32];
@@ -449,21 +509,30 @@ cudaError_t launch_train_prep(const PrepArgs& a, cudaStream_t stream) {
                              : launch_pdl(train_prep_kernel<float>, grid, dim3(kThreads), 0, stream, u);
 }
 
+template <typename T, int WPR, int NV, bool STAT>
+static cudaError_t plain_rows(const NormBackArgs& a, cudaStream_t stream) {
+  const dim3 grid(ceil_div(a.M, 8 / WPR)), block(kThreads);
+  if (!STAT && a.dres != nullptr)
+    return launch_pdl(norm_back_plain_kernel<T, WPR, NV, false, true>, grid, block, 0, stream, a);
+  return launch_pdl(norm_back_plain_kernel<T, WPR, NV, STAT, false>, grid, block, 0, stream, a);
+}
+
 template <typename T, bool STAT>
 static cudaError_t norm_back_typed(const NormBackArgs& a, cudaStream_t stream) {
-  // As few warps per row as hold it at 16 columns a thread; all 8 when there
-  // are too few rows to fill the SMs otherwise.
-  int wpr = a.K <= 512 ? 1 : a.K <= 1024 ? 2 : a.K <= 2048 ? 4 : 8;
-  if (a.M < num_sms() * 8) wpr = 8;
-  const dim3 grid(ceil_div(a.M, 8 / wpr)), block(kThreads);
-  if (a.K > 8192) return launch_pdl(norm_back_kernel<T, 8, 0, STAT>, grid, block, 0, stream, a);
-  if (a.K > 4096) return launch_pdl(norm_back_kernel<T, 8, 8, STAT>, grid, block, 0, stream, a);
-  switch (wpr) {
-    case 1: return launch_pdl(norm_back_kernel<T, 1, 4, STAT>, grid, block, 0, stream, a);
-    case 2: return launch_pdl(norm_back_kernel<T, 2, 4, STAT>, grid, block, 0, stream, a);
-    case 4: return launch_pdl(norm_back_kernel<T, 4, 4, STAT>, grid, block, 0, stream, a);
-    default: return launch_pdl(norm_back_kernel<T, 8, 4, STAT>, grid, block, 0, stream, a);
+  const dim3 block(kThreads);
+  if (a.slices == 1 && a.gain == nullptr && a.x == nullptr && a.K <= 8 * 1024) {
+    // as few warps per row as hold it at 32 columns a thread; 8 when rows are few
+    const bool few = a.M < num_sms() * 8;
+    if (!few && a.K <= 1024) return plain_rows<T, 1, 8, STAT>(a, stream);
+    if (!few && a.K <= 2 * 1024) return plain_rows<T, 2, 8, STAT>(a, stream);
+    if (!few && a.K <= 4 * 1024) return plain_rows<T, 4, 8, STAT>(a, stream);
+    if (a.K <= 2 * 1024) return plain_rows<T, 8, 2, STAT>(a, stream);
+    return plain_rows<T, 8, 8, STAT>(a, stream);
   }
+  const dim3 grid(a.M);
+  if (a.K <= 2 * 1024) return launch_pdl(norm_back_kernel<T, 8, 2, STAT>, grid, block, 0, stream, a);
+  if (a.K <= 8 * 1024) return launch_pdl(norm_back_kernel<T, 8, 8, STAT>, grid, block, 0, stream, a);
+  return launch_pdl(norm_back_kernel<T, 8, 0, STAT>, grid, block, 0, stream, a);
 }
 
 cudaError_t launch_norm_back(const NormBackArgs& a, bool stat, mmf_dtype dt, cudaStream_t stream) {

@@ -6,7 +6,6 @@ using namespace mmf;
 
 namespace {
 
-constexpr int kMaxSplits = 32;                   // fp32 slices of one split product
 constexpr size_t kPieceBytes = size_t(256) << 20;   // gradient of the logits held at once
 
 int pad(int v, int to) { return (v + to - 1) / to * to; }
@@ -86,88 +85,82 @@ struct Grad {
   bool over_s;   // holds G / s: dx^ puts s back per row, dW multiplies by the codes themselves
 };
 
-// Workspace of the products for an input [M, K]: a gradient of nseg segments of
-// `cols` columns for dx^, of `cols` columns in all for dW.
-size_t dxh_floats(int M, int K, int splits) { return (size_t)splits * bgemm_slice_rows(M) * K; }
-BGemmPlan dx_plan(int M, int K, int cols, int nseg, mmf_dtype dt) {
-  return bgemm_plan(M, K, cols, planes_of(dt), nseg, kMaxSplits);
+// The products of a backward: dx^ [M, K] from nseg segments of `cols` gradient
+// columns, dW from all of them (dw_cols).
+struct Products {
+  BGemmShape dx, dw;
+  BGemmPlan plan;
+};
+Products products(int M, int K, int nseg, int cols, int dw_cols, mmf_dtype dt) {
+  Products p;
+  p.dx = {M, K, cols, planes_of(dt), nseg};
+  p.dw = {dw_cols, K, M, planes_of(dt), 1};
+  p.plan = bgemm_plan(p.dx, p.dw);
+  return p;
 }
-BGemmPlan dw_plan(int M, int K, int cols, mmf_dtype dt) { return bgemm_plan(cols, K, M, planes_of(dt), 1, kMaxSplits); }
-size_t dw_floats(int M, int K, int cols, mmf_dtype dt) {
-  const int s = dw_plan(M, K, cols, dt).splits;
-  return s > 1 ? (size_t)s * bgemm_slice_rows(cols) * K : 0;
-}
-
-// dx^ (+)= sum over nseg segments of gamma[g] G_g W_g, over the plan's slices.
-mmf_status run_dx(const Grad& G, int nseg, int cols, const void* wb, int M, int K, const float* const* gamma,
-                  const float* scale, const BGemmPlan& plan, bool accumulate, float* dxh, cudaStream_t s) {
-  BGemmArgs b = {};
-  b.dw = false;
-  b.pair = plan.pair;
-  b.a = G.g;
-  b.lda = G.ld;
-  b.a_plane = G.plane_rows;
-  b.planes = G.planes;
-  b.b = wb;
-  b.ldb = K;
-  b.I = M;
-  b.J = K;
-  b.R = cols;
-  b.nseg = nseg;
-  b.splits = plan.splits;
-  b.slice_rows = bgemm_slice_rows(M);
-  b.out[0] = dxh;
-  b.out_f32 = true;
-  b.accumulate = accumulate;
-  for (int i = 0; gamma != nullptr && i < nseg; ++i) b.gamma[i] = gamma[i];
-  b.row_scale = G.over_s ? scale : nullptr;
-  MMF_CUDA(timed("bgemm_dx", s, [&] { return launch_bgemm_tc(b, status_word(), s); }), "gradient of the input");
-  return MMF_OK;
+size_t dxh_floats(const Products& p) { return (size_t)p.plan.splits[0] * bgemm_slice_rows(p.dx.I) * p.dx.J; }
+size_t dw_floats(const Products& p) {
+  return p.plan.splits[1] > 1 ? (size_t)p.plan.splits[1] * bgemm_slice_rows(p.dw.I) * p.dw.J : 0;
 }
 
-// dW[seg] = G^T Q / fold(inv_gamma[seg]) for nseg segments of N rows, their columns `pitch` apart.
-mmf_status run_dw(const Grad& G, int nseg, int N, int pitch, const void* qb, int M, int K,
-                  const float* const* inv_gamma, void* const* dw, float* part, mmf_dtype dt, cudaStream_t s) {
-  const int cols = nseg == 1 ? N : nseg * pitch;
-  BGemmArgs b = {};
-  b.dw = true;
-  b.a = G.g;
-  b.lda = G.ld;
-  b.a_plane = G.plane_rows;
-  b.planes = G.planes;
-  b.b = qb;
-  b.ldb = K;
-  b.I = cols;
-  b.J = K;
-  b.R = M;
-  b.nseg = 1;
-  const BGemmPlan plan = dw_plan(M, K, cols, dt);
-  b.pair = plan.pair;
-  b.splits = plan.splits;
-  b.slice_rows = bgemm_slice_rows(cols);
-  b.seg_rows = N;
-  b.seg_pitch = nseg == 1 ? b.slice_rows : pitch;
-  if (b.splits > 1) {
-    b.out[0] = part;
-    b.out_f32 = true;
-  } else {
-    for (int i = 0; i < nseg; ++i) {
-      b.out[i] = dw[i];
-      b.inv_gamma[i] = inv_gamma ? inv_gamma[i] : nullptr;
-    }
-    b.out_f32 = dt == MMF_F32;
+// dx^ (+)= sum over segments of gamma[g] G_g W_g into dxh (null: not wanted);
+// dW[seg] = G^T Q / fold(inv_gamma[seg]) for dw_seg segments of N rows, their
+// columns `pitch` apart (dw null: not wanted).
+mmf_status run_products(const Products& pr, const Grad& G, const void* wb, const float* const* gamma,
+                        const float* scale, bool accumulate, float* dxh, const void* qb, int dw_seg, int N, int pitch,
+                        const float* const* inv_gamma, void* const* dw, float* part, mmf_dtype dt, cudaStream_t s) {
+  const int M = pr.dx.I, K = pr.dx.J;
+  BGemmArgs x = {}, w = {};
+  x.sh = pr.dx;
+  w.sh = pr.dw;
+  x.a = w.a = G.g;
+  x.lda = w.lda = G.ld;
+  x.a_plane = w.a_plane = G.plane_rows;
+  x.b = wb;
+  w.b = qb;
+  x.ldb = w.ldb = K;
+  x.splits = std::min(pr.plan.splits[0], bgemm_units(pr.dx));   // a shorter last piece: adds to the first slices only
+  x.slice_rows = bgemm_slice_rows(M);
+  x.out[0] = dxh;
+  x.out_f32 = true;
+  x.accumulate = accumulate;
+  for (int i = 0; gamma != nullptr && i < pr.dx.nseg; ++i) x.gamma[i] = gamma[i];
+  x.row_scale = G.over_s ? scale : nullptr;
+  w.splits = pr.plan.splits[1];
+  w.slice_rows = bgemm_slice_rows(pr.dw.I);
+  w.seg_rows = N;
+  w.seg_pitch = dw_seg == 1 ? pad(N, 32) : pitch;
+  w.out_f32 = w.splits > 1 || dt == MMF_F32;
+  bool want_dw = false;
+  for (int i = 0; dw != nullptr && i < dw_seg; ++i) {
+    want_dw = want_dw || dw[i] != nullptr;
+    if (w.splits > 1) continue;
+    w.out[i] = dw[i];
+    w.inv_gamma[i] = inv_gamma ? inv_gamma[i] : nullptr;
   }
-  MMF_CUDA(timed("bgemm_dw", s, [&] { return launch_bgemm_tc(b, status_word(), s); }), "gradient of the weights");
-  if (b.splits > 1) {
+  if (w.splits > 1) w.out[0] = part;
+  const BGemmArgs *px = dxh ? &x : nullptr, *pw = want_dw ? &w : nullptr;
+  if (pr.plan.together && px && pw) {
+    MMF_CUDA(timed("bgemm_both", s, [&] { return launch_bgemm_tc(px, pw, pr.plan.pair[0], status_word(), s); }),
+             "gradient products");
+  } else {
+    if (px)
+      MMF_CUDA(timed("bgemm_dx", s, [&] { return launch_bgemm_tc(px, nullptr, pr.plan.pair[0], status_word(), s); }),
+               "gradient of the input");
+    if (pw)
+      MMF_CUDA(timed("bgemm_dw", s, [&] { return launch_bgemm_tc(nullptr, pw, pr.plan.pair[1], status_word(), s); }),
+               "gradient of the weights");
+  }
+  if (want_dw && w.splits > 1) {
     DwJoinArgs j = {};
     j.part = part;
-    j.slices = b.splits;
-    j.slice_rows = b.slice_rows;
-    j.segs = nseg;
-    j.seg_pitch = nseg == 1 ? b.slice_rows : pitch;
+    j.slices = w.splits;
+    j.slice_rows = w.slice_rows;
+    j.segs = dw_seg;
+    j.seg_pitch = w.seg_pitch;
     j.N = N;
     j.K = K;
-    for (int i = 0; i < nseg; ++i) {
+    for (int i = 0; i < dw_seg; ++i) {
       j.out[i] = dw[i];
       j.inv_gamma[i] = inv_gamma ? inv_gamma[i] : nullptr;
     }
@@ -232,6 +225,7 @@ LinearPlan linear_plan(int nlin, int N, int M, mmf_dtype dt) {
 }
 
 struct LinearWs {
+  Products pr;
   void *wb, *qb, *gb;
   float *dxh, *part, *colpart;
 };
@@ -241,8 +235,9 @@ LinearWs carve_linear(Carver& c, int nlin, int N, int K, int M, mmf_dtype dt) {
   w.wb = c.take<char>((size_t)p.cols * K * 2);
   w.qb = c.take<char>((size_t)M * K * 2);
   w.gb = c.take<char>(p.copy ? (size_t)p.planes * p.rows * p.cols * 2 : 0);
-  w.dxh = c.take<float>(dxh_floats(M, K, dx_plan(M, K, p.pitch, nlin, dt).splits));
-  w.part = c.take<float>(dw_floats(M, K, nlin == 1 ? N : p.cols, dt));
+  w.pr = products(M, K, nlin, p.pitch, nlin == 1 ? N : p.cols, dt);
+  w.dxh = c.take<float>(dxh_floats(w.pr));
+  w.part = c.take<float>(dw_floats(w.pr));
   w.colpart = c.take<float>(std::max(colsum_ws_floats(M, K), colsum_ws_floats(M, nlin * N)));
   return w;
 }
@@ -298,22 +293,21 @@ mmf_status linear_backward(const mmf_tlinear* lins, int nlin, const mmf_act8& ke
   G.planes = lp.planes;
   G.over_s = dt == MMF_F32;
   mmf_status r = MMF_OK;
+  const float* gam[3] = {lins[0].gamma, lins[nlin > 1 ? 1 : 0].gamma, lins[nlin > 2 ? 2 : 0].gamma};
+  if (want_dxh || want_dw)
+    r = run_products(w.pr, G, w.wb, gam, kept.scale, false, want_dxh ? w.dxh : nullptr, w.qb, nlin, N, lp.pitch,
+                     nullptr, want_dw ? dw : nullptr, w.part, dt, s);
+  if (r != MMF_OK) return r;
   if (want_dxh) {
-    const BGemmPlan plan = dx_plan(M, K, lp.pitch, nlin, dt);
-    const int sp = plan.splits;
-    const float* gam[3] = {lins[0].gamma, lins[nlin > 1 ? 1 : 0].gamma, lins[nlin > 2 ? 2 : 0].gamma};
-    r = run_dx(G, nlin, lp.pitch, w.wb, M, K, gam, kept.scale, plan, false, w.dxh, s);
-    if (r != MMF_OK) return r;
-    NormBackArgs n = norm_args(w.dxh, sp, M, K, kept, lins[0].gain, x);
+    NormBackArgs n = norm_args(w.dxh, w.pr.plan.splits[0], M, K, kept, lins[0].gain, x);
     if (cmean != nullptr) {
       n.cmean = cmean;
       MMF_CUDA(timed("norm_stat", s, [&] { return launch_norm_back(n, true, dt, s); }), "norm backward");
       n.slices = 1;
     }
     r = run_norm(n, dres, g.dx, g.dgain, w.colpart, dt, s);
+    if (r != MMF_OK) return r;
   }
-  if (r == MMF_OK && want_dw) r = run_dw(G, nlin, N, lp.pitch, w.qb, M, K, nullptr, dw, w.part, dt, s);
-  if (r != MMF_OK) return r;
   bool want_db = false;
   for (int i = 0; i < nlin; ++i) want_db = want_db || g.dbias[i] != nullptr;
   if (want_db) {
@@ -471,6 +465,7 @@ namespace {
 
 struct GluWs {
   LinearWs down;
+  Products pr;
   uint8_t *wu_gate, *wu_up;
   void *wb, *qb, *dz;
   float *cmean, *dxh, *part, *colpart;
@@ -488,8 +483,9 @@ GluWs carve_glu(Carver& c, int M, int d, int I, mmf_dtype dt) {
   w.qb = c.take<char>((size_t)M * d * 2);
   w.dz = c.take<char>((size_t)planes_of(dt) * rows * 2 * Ip * 2);
   w.cmean = c.take<float>(M);
-  w.dxh = c.take<float>(dxh_floats(M, d, dx_plan(M, d, 2 * Ip, 1, dt).splits));
-  w.part = c.take<float>(dw_floats(M, d, 2 * Ip, dt));
+  w.pr = products(M, d, 1, 2 * Ip, 2 * Ip, dt);
+  w.dxh = c.take<float>(dxh_floats(w.pr));
+  w.part = c.take<float>(dw_floats(w.pr));
   w.colpart = c.take<float>(std::max(colsum_ws_floats(M, d), colsum_ws_floats(M, 2 * Ip)));
   return w;
 }
@@ -584,14 +580,16 @@ extern "C" mmf_status mmf_glu_backward(const mmf_tlinear* gate, const mmf_tlinea
   G.planes = planes;
   G.over_s = true;
   const float* gam[3] = {gate->gamma, up->gamma, nullptr};
-  if (want_dxh) {
-    const BGemmPlan plan = dx_plan(M, d, 2 * Ip, 1, dtype);
-    r = run_dx(G, 1, 2 * Ip, w.wb, M, d, nullptr, kept_x->scale, plan, false, w.dxh, s);
-    if (r != MMF_OK) return r;
-    r = run_norm(norm_args(w.dxh, plan.splits, M, d, *kept_x, gate->gain, x), dres, gx.dx, gx.dgain, w.colpart, dtype, s);
+  if (want_dxh || want_dw) {
+    r = run_products(w.pr, G, w.wb, nullptr, kept_x->scale, false, want_dxh ? w.dxh : nullptr, w.qb, 2, I, Ip, gam,
+                     want_dw ? gx.dw : nullptr, w.part, dtype, s);
     if (r != MMF_OK) return r;
   }
-  if (want_dw && (r = run_dw(G, 2, I, Ip, w.qb, M, d, gam, gx.dw, w.part, dtype, s)) != MMF_OK) return r;
+  if (want_dxh) {
+    r = run_norm(norm_args(w.dxh, w.pr.plan.splits[0], M, d, *kept_x, gate->gain, x), dres, gx.dx, gx.dgain, w.colpart,
+                 dtype, s);
+    if (r != MMF_OK) return r;
+  }
   if (want_db) {
     ColSumArgs cs = {};
     cs.src = w.dz;
@@ -642,6 +640,7 @@ int piece_cols(int M, int V, mmf_dtype dt) {
 }
 
 struct HeadWs {
+  Products pr;   // of a whole piece
   uint8_t* wu;
   void *wb, *qb, *dz;
   float *dxh, *part, *colpart;
@@ -653,14 +652,13 @@ HeadWs carve_head(Carver& c, int M, int V, int K, mmf_dtype dt) {
   w.wb = c.take<char>((size_t)V * K * 2);
   w.qb = c.take<char>((size_t)M * K * 2);
   w.dz = c.take<char>((size_t)planes_of(dt) * plane_rows_of(M, dt) * vp * 2);
-  w.dxh = c.take<float>(dxh_floats(M, K, dx_plan(M, K, std::min(vp, V), 1, dt).splits));
-  size_t part = 0, col = colsum_ws_floats(M, K);
-  for (int v0 = 0; v0 < V; v0 += vp) {   // the last piece may be cut into more slices
-    part = std::max(part, dw_floats(M, K, std::min(vp, V - v0), dt));
-  }
-  col = std::max(col, colsum_ws_floats(M, vp));
-  w.part = c.take<float>(part);
-  w.colpart = c.take<float>(col);
+  const int n = std::min(vp, V), last = V - (ceil_div(V, vp) - 1) * vp;
+  w.pr = products(M, K, 1, n, n, dt);
+  Products tail = w.pr;   // the last piece keeps the plan
+  tail.dx.R = tail.dw.I = last;
+  w.dxh = c.take<float>(dxh_floats(w.pr));
+  w.part = c.take<float>(std::max(dw_floats(w.pr), dw_floats(tail)));
+  w.colpart = c.take<float>(std::max(colsum_ws_floats(M, K), colsum_ws_floats(M, vp)));
   return w;
 }
 
@@ -777,7 +775,6 @@ extern "C" mmf_status mmf_head_loss_backward(const mmf_tlinear* head, const mmf_
   MMF_CUDA(timed("train_prep", s, [&] { return launch_train_prep(pa, s); }), "operands");
   const uint8_t* wu = head->codes != nullptr ? head->codes : w.wu;
   const mmf_tlinear* seg[1] = {head};
-  const BGemmPlan plan = dx_plan(M, K, std::min(vp, V), 1, dtype);
   for (int v0 = 0; v0 < V; v0 += vp) {
     const int n = std::min(vp, V - v0);
     TGemmArgs a = gemm_args(seg, 1, kept->q, kept->scale, kept->qsum, M, w.dz, vp, nullptr, nullptr);
@@ -804,17 +801,14 @@ extern "C" mmf_status mmf_head_loss_backward(const mmf_tlinear* head, const mmf_
     G.plane_rows = rows;
     G.planes = planes_of(dtype);
     G.over_s = true;
-    if (want_dxh) {
-      // the last piece may have fewer units than slices: it adds to the first ones only
-      BGemmPlan pp = plan;
-      pp.splits = std::min(plan.splits, bgemm_units(n, G.planes, 1));
-      r = run_dx(G, 1, n, static_cast<const char*>(w.wb) + (size_t)v0 * K * 2, M, K, &head->gamma, kept->scale, pp,
-                 v0 > 0, w.dxh, s);
+    if (want_dxh || want_dw) {
+      Products pr = w.pr;
+      pr.dx.R = pr.dw.I = n;
+      void* dw[3] = {want_dw ? static_cast<char*>(grads->dw[0]) + (size_t)v0 * K * elem_bytes(dtype) : nullptr, nullptr,
+                     nullptr};
+      r = run_products(pr, G, static_cast<const char*>(w.wb) + (size_t)v0 * K * 2, &head->gamma, kept->scale, v0 > 0,
+                       want_dxh ? w.dxh : nullptr, w.qb, 1, n, n, nullptr, dw, w.part, dtype, s);
       if (r != MMF_OK) return r;
-    }
-    if (want_dw) {
-      void* dw[3] = {static_cast<char*>(grads->dw[0]) + (size_t)v0 * K * elem_bytes(dtype), nullptr, nullptr};
-      if ((r = run_dw(G, 1, n, n, w.qb, M, K, nullptr, dw, w.part, dtype, s)) != MMF_OK) return r;
     }
     if (want_db) {
       ColSumArgs cs = {};
@@ -832,6 +826,6 @@ extern "C" mmf_status mmf_head_loss_backward(const mmf_tlinear* head, const mmf_
     }
   }
   if (!want_dxh) return MMF_OK;
-  return run_norm(norm_args(w.dxh, plan.splits, M, K, *kept, head->gain, x), nullptr, grads->dx, grads->dgain, w.colpart, dtype,
+  return run_norm(norm_args(w.dxh, w.pr.plan.splits[0], M, K, *kept, head->gain, x), nullptr, grads->dx, grads->dgain, w.colpart, dtype,
                   s);
 }
