@@ -122,17 +122,39 @@ __device__ __forceinline__ uint32_t leader_addr(const void* p) {
   return r;
 }
 
-// TMA load into this CTA's shared memory; a pair's loads all count on its first CTA's barrier.
+// TMA load into this CTA's shared memory; a pair's loads all count on its first
+// CTA's barrier (`bar`: its shared::cluster address).
 template <int CTAS>
-__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   if constexpr (CTAS == 2)
     asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
         "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(leader_addr(bar))
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
   else
-    tma_load_2d(dst, map, x, y, bar);
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// Several 64-column blocks in one load: a 3-D map {64, rows, cols / 64}.
+template <int CTAS>
+__device__ __forceinline__ void load_blocks(void* dst, const CUtensorMap* map, int y, int block, uint32_t bar) {
+  if constexpr (CTAS == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(block), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(block), "r"(bar)
+        : "memory");
 }
 
 __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, const void* src, int x, int y) {
@@ -180,6 +202,7 @@ struct Prob {
   ProbArgs g;
   int i_tiles, j_tiles;
   int nk, cl, ups, units;   // k-steps per segment; k-steps per unit; units per segment and in all
+  bool wide_a, wide_b;      // MN-major operands loaded by 64-column blocks (widths that are multiples of 64)
 };
 struct KArgs {
   Prob pr[2];               // dx, dw
@@ -261,40 +284,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     t.chain = KIND == 2 || (KIND == 1 && !t.dw);
     return t;
   };
-  // MMA columns of a tile: a multiple of 16, for a pair of 32 (each CTA holds half of B)
+  // MMA columns of a tile: a multiple of 16, for a pair of 32 (each CTA holds half
+  // of B), of 128 where B comes in blocks
   auto cols_of = [&](const Prob& q, int jt) {
     const int n = min(BN, q.g.J - jt * BN);
-    return CTAS == 2 ? (n + 31) / 32 * 32 : n;
+    return CTAS == 1 ? n : q.wide_b ? (n + 127) / 128 * 128 : (n + 31) / 32 * 32;
   };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
+    // One thread feeds the ring; its instructions per step are on the critical
+    // path (a few more of them cost 5 % of the product), hence the running
+    // stage and phase and the few wide loads.
     if (lane == 0) {
-      uint32_t n = 0;
+      int s = 0;
+      uint32_t ph = 1, n = 0;
       bool ok = true;
+      const uint32_t bar0 = CTAS == 2 ? leader_addr(&sm.full[0]) : smem_u32(&sm.full[0]);
       for (int tile = first; tile < p.tiles && ok; tile += stride) {
         const Place t = place(tile);
         const Prob& q = p.pr[t.dw];
         const CUtensorMap *ma = &maps.a[t.dw], *mb = &maps.b[t.dw];
-        const int half = cols_of(q, t.jt) / CTAS, boxes = (half + 63) / 64;
+        const int half = cols_of(q, t.jt) / CTAS;
+        const bool wide_a = q.wide_a, wide_b = q.wide_b;
+        const int boxes = wide_b ? BN / CTAS / 64 : (half + 63) / 64;
+        const uint32_t bytes = CTAS * (A_BYTES + boxes * BOX_BYTES);
         const int i0 = (t.it * CTAS + rank) * BM, j0 = t.jt * BN + rank * half;
-        for (int u = t.lo; u < t.hi && ok; ++u) {
-          const int seg = t.chain ? u / q.ups : 0;
-          const int kb0 = (u - seg * q.ups) * q.cl, kb1 = min(kb0 + q.cl, q.nk);
-          for (int pl = q.g.planes - 1; pl >= 0 && ok; --pl) {
-            for (int kb = kb0; kb < kb1; ++kb, ++n) {
-              const int s = n % NS, r0 = kb * BK;
-              if (!mbar_wait(&sm.empty[s], ((n / NS) & 1) ^ 1, abort_flag, p.status, p.wait_cycles)) { ok = false; break; }
-              if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], CTAS * (A_BYTES + boxes * BOX_BYTES));
-              if (t.dw) {
-                load_box<CTAS>(sm.a[s], ma, i0, pl * q.g.a_plane + r0, &sm.full[s]);
-                load_box<CTAS>(sm.a[s] + BOX_BYTES, ma, i0 + 64, pl * q.g.a_plane + r0, &sm.full[s]);
-              } else {
-                load_box<CTAS>(sm.a[s], ma, seg * q.g.R + r0, pl * q.g.a_plane + i0, &sm.full[s]);
+        // k-step at reduction row r of B, row (or column) ra of A
+        auto step = [&](int ra_x, int ra_y, int r) {
+          if (!mbar_try_wait(&sm.empty[s], ph) && !mbar_wait(&sm.empty[s], ph, abort_flag, p.status, p.wait_cycles))
+            return false;
+          const uint32_t bar = bar0 + 8 * s;
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], bytes);
+          if (t.dw && wide_a) {
+            load_blocks<CTAS>(sm.a[s], ma, ra_y, i0 / 64, bar);
+          } else if (t.dw) {
+            load_box<CTAS>(sm.a[s], ma, i0, ra_y, bar);
+            load_box<CTAS>(sm.a[s] + BOX_BYTES, ma, i0 + 64, ra_y, bar);
+          } else {
+            load_box<CTAS>(sm.a[s], ma, ra_x, ra_y, bar);
+          }
+          if (wide_b) {
+            load_blocks<CTAS>(sm.b[s], mb, r, j0 / 64, bar);
+          } else {
+            for (int b = 0; b < boxes; ++b) load_box<CTAS>(sm.b[s] + b * BOX_BYTES, mb, j0 + 64 * b, r, bar);
+          }
+          if (++s == NS) {
+            s = 0;
+            ph ^= 1;
+          }
+          ++n;
+          return true;
+        };
+        if (!t.chain) {
+          for (int r = t.lo * BK; r < t.hi * BK && ok; r += BK) ok = step(r, t.dw ? r : i0, r);
+        } else {
+          for (int u = t.lo; u < t.hi && ok; ++u) {
+            const int seg = u / q.ups, kb0 = (u - seg * q.ups) * q.cl, kb1 = min(kb0 + q.cl, q.nk);
+            for (int pl = q.g.planes - 1; pl >= 0 && ok; --pl)
+              for (int kb = kb0; kb < kb1 && ok; ++kb) {
+                const int r = seg * q.g.R + kb * BK;
+                ok = step(r, pl * q.g.a_plane + (t.dw ? kb * BK : i0), r);
               }
-              for (int b = 0; b < boxes; ++b)
-                load_box<CTAS>(sm.b[s] + b * BOX_BYTES, mb, j0 + 64 * b, seg * q.g.R + r0, &sm.full[s]);
-            }
           }
         }
       }
@@ -310,7 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (the pair's first CTA)
     if (lane == 0 && rank == 0) {
-      uint32_t n = 0, na = 0;   // ring steps; accumulators begun
+      int s = 0;
+      uint32_t ph = 0, na = 0;   // ring phase; accumulators begun
       bool ok = true;
       for (int tile = first; tile < p.tiles && ok; tile += stride) {
         const Place t = place(tile);
@@ -318,36 +370,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t idesc = idesc_bf16(BM * CTAS, cols_of(q, t.jt), t.dw, true);
         // 16 reduction steps: 2 row groups (MN-major) or 32 bytes (K-major)
         const uint32_t astep = t.dw ? 128 : 2;
-        uint32_t d_tmem = 0, accum = 0;
-        for (int u = t.lo; u < t.hi && ok; ++u) {
-          if (t.chain || u == t.lo) {
-            const int acc = na & 1;
-            const bool got = CTAS == 2
-                                 ? wait_cluster(&sm.tmem_empty[acc], ((na >> 1) & 1) ^ 1, abort_flag, p.status, p.wait_cycles)
-                                 : mbar_wait(&sm.tmem_empty[acc], ((na >> 1) & 1) ^ 1, abort_flag, p.status, p.wait_cycles);
-            if (!got) { ok = false; break; }
-            tc_fence_after();
-            d_tmem = tmem_base + acc * BN;
-            accum = 0;
-          }
-          const int kb0 = t.chain ? (u % q.ups) * q.cl : u;
-          int steps = t.chain ? (min(kb0 + q.cl, q.nk) - kb0) * q.g.planes : 1;
-          for (; steps > 0; --steps, ++n) {
-            const int s = n % NS;
-            if (!mbar_wait(&sm.full[s], (n / NS) & 1, abort_flag, p.status, p.wait_cycles)) { ok = false; break; }
+        // `steps` ring stages into the next accumulator
+        auto accumulate = [&](int steps) {
+          const int acc = na & 1;
+          const uint32_t eph = ((na >> 1) & 1) ^ 1;
+          const bool got = CTAS == 2 ? wait_cluster(&sm.tmem_empty[acc], eph, abort_flag, p.status, p.wait_cycles)
+                                     : mbar_wait(&sm.tmem_empty[acc], eph, abort_flag, p.status, p.wait_cycles);
+          if (!got) return false;
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + acc * BN;
+          for (int st = 0; st < steps; ++st) {
+            if (!mbar_try_wait(&sm.full[s], ph) && !mbar_wait(&sm.full[s], ph, abort_flag, p.status, p.wait_cycles))
+              return false;
             tc_fence_after();
             const uint64_t ad = t.dw ? desc_mn_sw128(smem_u32(sm.a[s])) : umma_desc_sw128(smem_u32(sm.a[s]));
             const uint64_t bd = desc_mn_sw128(smem_u32(sm.b[s]));
 #pragma unroll
-            for (int j = 0; j < BK / 16; ++j) {
-              umma_f16<CTAS>(d_tmem, ad + (uint64_t)(astep * j), bd + (uint64_t)(128 * j), idesc, accum);
-              accum = 1;
-            }
+            for (int j = 0; j < BK / 16; ++j)
+              umma_f16<CTAS>(d_tmem, ad + (uint64_t)(astep * j), bd + (uint64_t)(128 * j), idesc, st + j);
             commit<CTAS>(&sm.empty[s]);
+            if (++s == NS) {
+              s = 0;
+              ph ^= 1;
+            }
           }
-          if (ok && (t.chain || u == t.hi - 1)) {
-            commit<CTAS>(&sm.tmem_full[na & 1]);
-            ++na;
+          commit<CTAS>(&sm.tmem_full[acc]);
+          ++na;
+          return true;
+        };
+        if (!t.chain) {
+          ok = accumulate(t.hi - t.lo);
+        } else {
+          for (int u = t.lo; u < t.hi && ok; ++u) {
+            const int kb0 = (u % q.ups) * q.cl;
+            ok = accumulate((min(kb0 + q.cl, q.nk) - kb0) * q.g.planes);
           }
         }
       }
@@ -408,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (q.g.row_scale != nullptr && i < q.g.I) sc *= q.g.row_scale[i];
       }
       const CUtensorMap* mo = &maps.o[t.dw ? 1 + (rows_ok ? seg : 0) : 0];
-      const bool f32 = q.g.out_f32;
+      const bool f32 = MODE == 0 ? true : q.g.out_f32;
       const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
       const int jg = t.jt * BN + group * 128;                    // this warp's first column
 
@@ -471,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (KIND < 2) {
         if (!wait_full()) break;
         const uint32_t tbase = tmem_base + lanes + (na & 1) * BN + group * 128;
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           if (jg + 32 * c >= q.g.J || !rows_ok) break;
           uint32_t r[32];
@@ -640,10 +697,18 @@ cudaError_t launch_bgemm_tc(const BGemmArgs* dx, const BGemmArgs* dw, bool pair,
     const BGemmShape& s = g.sh;
     const uint64_t a_rows = (uint64_t)(s.planes - 1) * g.a_plane + (d ? s.R : s.I);
     const uint64_t a_cols = d ? s.I : (uint64_t)s.nseg * s.R;
-    if (!make_tma_2d(&m.a[d], g.a, BF, 2, a_cols, a_rows, 64, d ? 64 : BM, CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)g.lda * 2) ||
-        !make_tma_2d(&m.b[d], g.b, BF, 2, (uint64_t)s.J, (uint64_t)s.nseg * s.R, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B,
-                     (uint64_t)g.ldb * 2))
-      return cudaErrorInvalidValue;
+    const uint64_t b_rows = (uint64_t)s.nseg * s.R;
+    Prob& q = p.pr[d];
+    q.wide_a = d && s.I % 64 == 0;
+    q.wide_b = s.J % 64 == 0;
+    const bool ok_a = q.wide_a ? make_tma_blocks(&m.a[d], g.a, a_cols, a_rows, 64, BM / 64, (uint64_t)g.lda * 2)
+                               : make_tma_2d(&m.a[d], g.a, BF, 2, a_cols, a_rows, 64, d ? 64 : BM,
+                                             CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)g.lda * 2);
+    const bool ok_b = q.wide_b ? make_tma_blocks(&m.b[d], g.b, (uint64_t)s.J, b_rows, 64, pair ? BN / 128 : BN / 64,
+                                                 (uint64_t)g.ldb * 2)
+                               : make_tma_2d(&m.b[d], g.b, BF, 2, (uint64_t)s.J, b_rows, 64, 64,
+                                             CU_TENSOR_MAP_SWIZZLE_128B, (uint64_t)g.ldb * 2);
+    if (!ok_a || !ok_b) return cudaErrorInvalidValue;
     for (int i = 0; i < (d ? 3 : 1); ++i) {
       if (g.out[i] == nullptr) continue;   // a segment without an output is skipped
       const uint64_t rows = d && g.splits == 1 ? (uint64_t)g.seg_rows : (uint64_t)g.splits * g.slice_rows;
@@ -651,7 +716,6 @@ cudaError_t launch_bgemm_tc(const BGemmArgs* dx, const BGemmArgs* dw, bool pair,
                        (uint64_t)s.J, rows, 32, 32, g.out_f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
         return cudaErrorInvalidValue;
     }
-    Prob& q = p.pr[d];
     q.g.a_plane = g.a_plane;
     q.g.planes = s.planes;
     q.g.I = s.I;

@@ -18,6 +18,9 @@ constexpr int kQuantPartials = 592;   // CTAs of the absmean partial-sum pass (4
 bool tma_available();
 bool make_tma_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int esize, uint64_t cols,
                  uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz, uint64_t pitch_bytes = 0);
+// A 2-D bf16 array of cols % 64 == 0 columns seen as [cols / 64][rows][64], in 128-byte-swizzled boxes.
+bool make_tma_blocks(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows,
+                     uint32_t box_blocks, uint64_t pitch_bytes);
 int num_sms();
 // Bound of the kernels' device-side waits, in SM cycles: about 1 s at 2 GHz, or
 // MMF_WAIT_LIMIT_US microseconds when set (tests make waits run out quickly).
