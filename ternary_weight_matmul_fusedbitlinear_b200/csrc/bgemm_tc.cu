@@ -18,10 +18,11 @@
 // transposed copies): a 64 x 64 box per 128-byte swizzle column block.
 //
 // What bounds it: feeding the tensor cores. A 128 x 256 tile per SM takes 48 KB
-// of operands per 64 reduction steps, 26 TB/s over the chip at the full bf16
-// rate, more than L2 delivers. CTAS = 2 therefore pairs the two SMs of a
-// cluster on a 256 x 256 tile (cta_group::2): each loads its own 128 rows of A
-// and half of B, 32 KB. Single SMs stay for products too small for pairs.
+// of operands per 64 reduction steps; CTAS = 2 pairs the two SMs of a cluster on
+// a 256 x 256 tile (cta_group::2), each loading its own 128 rows of A and half
+// of B, 32 KB. 8192 x 2048 x 8192, gradient of the input: 181 us on pairs (1.52
+// PFLOP/s), 200 us on single SMs (1.38), which stay for products whose tiles
+// fill them better.
 //
 // Persistent: TMA ring (4 x 48 KB or 6 x 32 KB), two TMEM accumulators, so a
 // tile's epilogue runs under the next tile's main loop. The last column tile
@@ -600,16 +601,16 @@ namespace {
 
 // Model of one product's time on one B200: groups (SMs, or pairs) take tiles in
 // turn; a tile takes its share of the reduction and a start-up; fp32 slices are
-// written and read again. Measured: a pair 0.435 us per 64 steps of 256 x 256
-// (1.43 PFLOP/s), an SM 0.60 us of 128 x 256, 1.5 us per tile.
+// written and read again. Measured: a pair 0.32 us per 64 steps of 256 x 256,
+// an SM 0.36 us of 128 x 256, about 2 us per tile.
 struct Model {
   bool pair;
   int groups;
   double step_us, tile_us;
   explicit Model(bool two) : pair(two) {
     groups = two ? num_sms() / 2 : num_sms();
-    step_us = two ? 0.435 : 0.60;
-    tile_us = 1.5;
+    step_us = two ? 0.32 : 0.36;
+    tile_us = 2.0;
   }
   long long tiles(const BGemmShape& s) const {
     return (long long)ceil_div(s.I, pair ? 2 * BM : BM) * ceil_div(s.J, BN);

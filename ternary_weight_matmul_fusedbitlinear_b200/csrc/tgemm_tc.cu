@@ -99,6 +99,7 @@ struct TcArgs {
   int* status;
   long long wait_cycles;   // bound of every wait
   uint32_t skip_it;        // test hook: CTA 0 never loads this k-step (~0u: none)
+  bool wide_b;             // the 256 weight rows of a tile follow one another: one load
   TrainEpi t;              // training epilogues only
 };
 
@@ -247,29 +248,39 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
+    // One thread feeds the ring: its instructions per k-step are on the critical
+    // path, hence the running stage and phase and one load for a whole weight
+    // tile where its rows follow one another.
     if (lane == 0) {
       const CUtensorMap* maps[3] = {&map_b0, &map_b1, &map_b2};
-      uint32_t it = 0;
+      uint32_t it = 0, ph = 1;
+      int s = 0;
       bool ok = true;
       for (int tile = blockIdx.x; tile < n_tiles_total && ok; tile += gridDim.x) {
         const int mt = tile / p.n_tiles, nt = tile % p.n_tiles;
         int seg0, row0, seg1, row1;
         half_source(p, EPI, nt, 0, seg0, row0);
         half_source(p, EPI, nt, 1, seg1, row1);
+        const CUtensorMap *mb0 = maps[seg0], *mb1 = maps[seg1];
         for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % NS;
-          if (!mbar_wait(&sm.tma_empty[s], ((it / NS) & 1) ^ 1, abort_flag, p.status, p.wait_cycles)) { ok = false; break; }
-          if (it == p.skip_it && blockIdx.x == 0) continue;   // test hook: these copies are never issued
-          if constexpr (UNP) {   // int8 weight rows straight into the SW128 tile of this stage
-            mbar_arrive_expect_tx(&sm.tma_full[s], A_BYTES + BU_BYTES);
-            tma_load_2d(sm.a[s], &map_a, kb * BK, mt * BM, &sm.tma_full[s]);
-            tma_load_2d(sm.bu[s], maps[seg0], kb * BK, row0, &sm.tma_full[s]);
-            tma_load_2d(sm.bu[s] + HALF * BK, maps[seg1], kb * BK, row1, &sm.tma_full[s]);
-          } else {
-            mbar_arrive_expect_tx(&sm.tma_full[s], A_BYTES + BP_BYTES);
-            tma_load_2d(sm.a[s], &map_a, kb * BK, mt * BM, &sm.tma_full[s]);
-            tma_load_2d(&sm.bp[s][0], maps[seg0], kb * (BK / 16), row0, &sm.tma_full[s]);
-            tma_load_2d(&sm.bp[s][HALF * (BK / 16)], maps[seg1], kb * (BK / 16), row1, &sm.tma_full[s]);
+          if (!mbar_try_wait(&sm.tma_empty[s], ph) &&
+              !mbar_wait(&sm.tma_empty[s], ph, abort_flag, p.status, p.wait_cycles)) { ok = false; break; }
+          if (it != p.skip_it || blockIdx.x != 0) {   // test hook: these copies are never issued
+            if constexpr (UNP) {   // int8 weight rows straight into the SW128 tile of this stage
+              mbar_arrive_expect_tx(&sm.tma_full[s], A_BYTES + BU_BYTES);
+              tma_load_2d(sm.a[s], &map_a, kb * BK, mt * BM, &sm.tma_full[s]);
+              tma_load_2d(sm.bu[s], mb0, kb * BK, row0, &sm.tma_full[s]);
+              if (!p.wide_b) tma_load_2d(sm.bu[s] + HALF * BK, mb1, kb * BK, row1, &sm.tma_full[s]);
+            } else {
+              mbar_arrive_expect_tx(&sm.tma_full[s], A_BYTES + BP_BYTES);
+              tma_load_2d(sm.a[s], &map_a, kb * BK, mt * BM, &sm.tma_full[s]);
+              tma_load_2d(&sm.bp[s][0], mb0, kb * (BK / 16), row0, &sm.tma_full[s]);
+              tma_load_2d(&sm.bp[s][HALF * (BK / 16)], mb1, kb * (BK / 16), row1, &sm.tma_full[s]);
+            }
+          }
+          if (++s == NS) {
+            s = 0;
+            ph ^= 1;
           }
         }
       }
@@ -280,7 +291,8 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      uint32_t it = 0, tl = 0;
+      uint32_t it = 0, tl = 0, ph = 0;
+      int s = 0;
       bool ok = true;
       for (int tile = blockIdx.x; tile < n_tiles_total && ok; tile += gridDim.x, ++tl) {
         const int acc = tl & 1;
@@ -289,9 +301,10 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % NS, u = UNP ? s : (int)(it % NB);
+          const int u = UNP ? s : (int)(it % NB);
           if ((!UNP && !mbar_wait(&sm.bu_full[u], (it / NB) & 1, abort_flag, p.status, p.wait_cycles)) ||
-              !mbar_wait(&sm.tma_full[s], (it / NS) & 1, abort_flag, p.status, p.wait_cycles)) {
+              (!mbar_try_wait(&sm.tma_full[s], ph) &&
+               !mbar_wait(&sm.tma_full[s], ph, abort_flag, p.status, p.wait_cycles))) {
             ok = false;
             break;
           }
@@ -303,6 +316,10 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
             umma_i8(d_tmem, adesc + (uint64_t)(2 * j), bdesc + (uint64_t)(2 * j), kIdesc, (kb | j) != 0);
           umma_commit(&sm.tma_empty[s]);
           if constexpr (!UNP) umma_commit(&sm.bu_empty[u]);
+          if (++s == NS) {
+            s = 0;
+            ph ^= 1;
+          }
         }
         if (ok) umma_commit(&sm.tmem_full[acc]);
       }
@@ -758,16 +775,18 @@ cudaError_t launch_tgemm_tc(const TGemmArgs& a, Epi epi, mmf_dtype dt, int* stat
     return cudaErrorInvalidValue;
   bool unp = true;   // every segment has its one-byte copy
   for (int r = 0; r < a.nseg; ++r) unp = unp && a.wu[r] != nullptr;
+  const bool wide = unp && !is_glu(epi) && (a.nseg == 1 || a.N % BN == 0);
   for (int r = 0; r < 3; ++r) {
     const int src = r < a.nseg ? r : 0;
     const bool ok = unp ? make_tma_2d(&mb[r], a.wu[src], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.N,
-                                      BK, HALF, CU_TENSOR_MAP_SWIZZLE_128B)
+                                      BK, wide ? BN : HALF, CU_TENSOR_MAP_SWIZZLE_128B)
                         : make_tma_2d(&mb[r], a.w[src], CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, (uint64_t)(a.K / 16),
                                       (uint64_t)a.N, BK / 16, HALF, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (!ok) return cudaErrorInvalidValue;
   }
   TcArgs p = {};
   p.g = a;
+  p.wide_b = wide;
   p.status = status;
   p.wait_cycles = wait_limit_cycles();
   p.skip_it = (uint32_t)test_hook("MMF_TC_SKIP_KSTEP");
@@ -803,7 +822,7 @@ cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, m
     return cudaErrorInvalidValue;
   for (int r = 0; r < 3; ++r)
     if (!make_tma_2d(&mb[r], a.wu[r < a.nseg ? r : 0], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.N,
-                     BK, HALF, CU_TENSOR_MAP_SWIZZLE_128B))
+                     BK, is_glu(epi) ? HALF : BN, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   const int planes = dt == MMF_BF16 ? 1 : 3;
   mo = ma;   // kLse stores no tile
@@ -823,6 +842,7 @@ cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, m
   TcArgs p;
   p.g = a;
   p.t = t;
+  p.wide_b = !is_glu(epi);
   p.status = status;
   p.wait_cycles = wait_limit_cycles();
   p.skip_it = (uint32_t)test_hook("MMF_TC_SKIP_KSTEP");
