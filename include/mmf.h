@@ -318,8 +318,9 @@ typedef struct mmf_linear_grads {
   void* dbias[3];  /* [N] */
 } mmf_linear_grads;
 
-/* Scratch bytes of mmf_bitlinear_train for nlin layers N x K. */
-size_t mmf_bitlinear_train_ws_size(int32_t nlin, int32_t N, int32_t K);
+/* Scratch bytes of mmf_bitlinear_train for nlin layers N x K and M tokens; 0
+ * for few tokens (ws may then be NULL). */
+size_t mmf_bitlinear_train_ws_size(int32_t nlin, int32_t N, int32_t K, int32_t M);
 
 /* Training forward: nlin (1..3) BitLinear layers of one shape and one gain on
  * the same input, as mmf_bitlinear computes them, keeping the input's codes.

@@ -76,7 +76,7 @@ SIGNATURES = {
     "mmf_glu_ws_size": (c_sz, [c_i32, c_i32, c_i32]),
     "mmf_glu": (ctypes.c_int, [ctypes.POINTER(TLinear)] * 3 + [c_vp, c_vp, c_vp, c_i32, ctypes.c_int, c_f, c_vp,
                                                              c_sz, c_vp]),
-    "mmf_bitlinear_train_ws_size": (c_sz, [c_i32, c_i32, c_i32]),
+    "mmf_bitlinear_train_ws_size": (c_sz, [c_i32, c_i32, c_i32, c_i32]),
     "mmf_bitlinear_train": (ctypes.c_int, [c_vp, c_i32, c_vp, ctypes.c_int, c_i32, c_vp, c_f, c_vp, c_vp, c_sz, c_vp]),
     "mmf_bitlinear_backward_ws_size": (c_sz, [c_i32, c_i32, c_i32, c_i32, ctypes.c_int]),
     "mmf_bitlinear_backward": (ctypes.c_int, [c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, ctypes.c_int, c_i32, c_vp, c_vp,

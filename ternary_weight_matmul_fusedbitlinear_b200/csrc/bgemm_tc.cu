@@ -198,6 +198,8 @@ struct ProbArgs {
   bool out_f32, accumulate;
   const void* out[3];
   const float *gamma[3], *inv_gamma[3], *row_scale;
+  const int8_t* dot_q;
+  float* dot_part;
 };
 struct Prob {
   ProbArgs g;
@@ -526,17 +528,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 4; ++c)
           if (rows_ok && jg + 32 * c < q.g.J) put(acc[c], jg + 32 * c);
       } else if (KIND < 2) {
+        const bool dots = MODE == 0 && KIND == 0 && q.g.dot_q != nullptr;
+        uint4 codes[8];   // this row's codes under the tile's columns, fetched ahead of the accumulator
+        if (dots) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const bool in = i < q.g.I && jg + 16 * c < q.g.J;   // J is a multiple of 16
+            codes[c] = in ? __ldg(reinterpret_cast<const uint4*>(q.g.dot_q + (size_t)i * q.g.J + jg + 16 * c))
+                          : make_uint4(0, 0, 0, 0);
+          }
+        }
         if (!wait_full()) break;
         const uint32_t tbase = tmem_base + lanes + (na & 1) * BN + group * 128;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          if (jg + 32 * c >= q.g.J || !rows_ok) break;
-          uint32_t r[32];
-          tmem_ld32(tbase + 32 * c, r);
-          float out[32];
+        if (dots) {
+          float dot = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) out[j] = __uint_as_float(r[j]) * sc;
-          put(out, jg + 32 * c);
+          for (int c = 0; c < 4; ++c) {
+            if (jg + 32 * c < q.g.J && rows_ok) {
+              uint32_t r[32];
+              tmem_ld32(tbase + 32 * c, r);
+              float out[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                out[j] = __uint_as_float(r[j]) * sc;
+                const uint32_t w = (&codes[2 * c + j / 16].x)[j / 4 % 4];
+                if (jg + 32 * c + j / 16 * 16 < q.g.J)   // past J the accumulator was never written
+                  dot = fmaf(out[j], (float)((int)(w << (24 - 8 * (j & 3))) >> 24), dot);
+              }
+              put(out, jg + 32 * c);
+            }
+          }
+          if (i < q.g.I && jg < q.g.J) q.g.dot_part[(size_t)(2 * t.jt + group) * q.g.I + i] = dot;
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            if (jg + 32 * c >= q.g.J || !rows_ok) break;
+            uint32_t r[32];
+            tmem_ld32(tbase + 32 * c, r);
+            float out[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) out[j] = __uint_as_float(r[j]) * sc;
+            put(out, jg + 32 * c);
+          }
         }
         release_acc();
       }
@@ -733,6 +766,8 @@ cudaError_t launch_bgemm_tc(const BGemmArgs* dx, const BGemmArgs* dw, bool pair,
       q.g.inv_gamma[i] = g.inv_gamma[i];
     }
     q.g.row_scale = g.row_scale;
+    q.g.dot_q = g.dot_q;
+    q.g.dot_part = g.dot_part;
     q.i_tiles = ceil_div(s.I, pair ? 2 * BM : BM);
     q.j_tiles = ceil_div(s.J, BN);
     q.nk = ceil_div(s.R, BK);

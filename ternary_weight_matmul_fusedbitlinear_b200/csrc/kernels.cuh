@@ -186,6 +186,8 @@ struct BGemmArgs {
   const float* gamma[3];    // dx: device scalars or null
   const float* row_scale;   // dx: [I] or null
   const float* inv_gamma[3];  // dw, splits 1: device scalars or null
+  const int8_t* dot_q;      // dx of one segment and plane, splits 1: codes [I, J], or null; then
+  float* dot_part;          //   dot_part[2 jt + h][i] = sum over columns 256 jt + 128 h .. of D[i, j] dot_q[i, j]
 };
 struct BGemmPlan {
   bool together;            // one launch for both
@@ -198,7 +200,7 @@ int bgemm_slice_rows(int I);
 // Either product, or both in one launch (null: left out).
 cudaError_t launch_bgemm_tc(const BGemmArgs* dx, const BGemmArgs* dw, bool pair, int* status, cudaStream_t stream);
 
-// Operand preparation for those products, one launch (train.cu).
+// Operand preparation for those products: one or two sets in one launch (train.cu).
 struct PrepArgs {
   const uint32_t* w[3];     // packed codes per segment -> wb [nseg * w_pitch, K] bf16 (rows past N zero); null wb: none
   int nseg, N, w_pitch, K;
@@ -215,7 +217,7 @@ struct PrepArgs {
   bool g_scaled;            // times 1 / scale[m]
   void* gb;
 };
-cudaError_t launch_train_prep(const PrepArgs& a, cudaStream_t stream);
+cudaError_t launch_train_prep(const PrepArgs* const* sets, int n, cudaStream_t stream);
 
 // Backward of RMSNorm + quantisation (straight through) per row of length K:
 //   v = sum of the slices of dx^;  n = x rinv or q / (s gain);  c = mean(v x^)
@@ -232,8 +234,11 @@ struct NormBackArgs {
   float* cmean;
 };
 cudaError_t launch_norm_back(const NormBackArgs& a, bool stat, mmf_dtype dt, cudaStream_t stream);
+// The same c from the dot products that BGemmArgs::dot_part received (slots of them per row).
+cudaError_t launch_dot_join(const float* part, int slots, int M, int K, const float* scale, float* cmean,
+                            cudaStream_t stream);
 
-// Column sums over tokens, in a fixed order (two launches when the rows are split).
+// Column sums over tokens, in a fixed order.
 //   kGrad:   out[s][n] = sum_t src[t, s, n]                       (a caller's gradient in dt)
 //   kPlanes: out[s][n] = sum_t scale[t] sum_p plane_p[t, s, n] / fold_gamma(inv_gamma[s])
 //   kGain:   out[0][k] = sum_t v[t, k] n[t, k]                    (v, n as in NormBackArgs; slice 0 holds v when summed)
@@ -249,7 +254,14 @@ struct ColSumArgs {
   float* part;              // scratch, colsum_ws_floats(M, columns)
 };
 size_t colsum_ws_floats(int M, int cols);
-cudaError_t launch_colsum(const ColSumArgs& a, ColSum kind, mmf_dtype dt, cudaStream_t stream);
+constexpr int kMaxColSums = 4;
+struct ColSumList {
+  ColSumArgs a[kMaxColSums];
+  ColSum kind[kMaxColSums];
+  int n;
+};
+// One launch for all of them (a second one where rows are split).
+cudaError_t launch_colsums(const ColSumList& list, mmf_dtype dt, cudaStream_t stream);
 
 // out[seg][n][k] = sum of the slices of dW (in order) / fold_gamma(inv_gamma[seg]), in dt.
 struct DwJoinArgs {

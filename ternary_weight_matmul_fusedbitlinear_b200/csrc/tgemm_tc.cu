@@ -820,10 +820,16 @@ cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, m
   if (!make_tma_2d(&ma, a.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.M, BK, BM,
                    CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  for (int r = 0; r < 3; ++r)
-    if (!make_tma_2d(&mb[r], a.wu[r < a.nseg ? r : 0], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.N,
-                     BK, is_glu(epi) ? HALF : BN, CU_TENSOR_MAP_SWIZZLE_128B))
-      return cudaErrorInvalidValue;
+  const bool packed = a.wu[0] == nullptr;   // kLse only: 2-bit words, expanded by the kernel
+  if (packed && (epi != Epi::kLse || a.K % 64 != 0)) return cudaErrorNotSupported;
+  for (int r = 0; r < 3; ++r) {
+    const int src = r < a.nseg ? r : 0;
+    const bool ok = packed ? make_tma_2d(&mb[r], a.w[src], CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, (uint64_t)(a.K / 16),
+                                         (uint64_t)a.N, BK / 16, HALF, CU_TENSOR_MAP_SWIZZLE_NONE)
+                           : make_tma_2d(&mb[r], a.wu[src], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K,
+                                         (uint64_t)a.N, BK, is_glu(epi) ? HALF : BN, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!ok) return cudaErrorInvalidValue;
+  }
   const int planes = dt == MMF_BF16 ? 1 : 3;
   mo = ma;   // kLse stores no tile
   if (epi != Epi::kLse &&
@@ -850,7 +856,9 @@ cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, m
   p.n_tiles = is_glu(epi) ? ceil_div(a.N, HALF) : ceil_div(a.N, BN);
   const bool b = dt == MMF_BF16;
   switch (epi) {
-    case Epi::kLse: return launch_mapped<Epi::kLse, bf16, true>(ma, mb, mo, mr, p, stream);
+    case Epi::kLse:
+      return packed ? launch_mapped<Epi::kLse, bf16, false>(ma, mb, mo, mr, p, stream)
+                    : launch_mapped<Epi::kLse, bf16, true>(ma, mb, mo, mr, p, stream);
     case Epi::kDz:
       return b ? launch_mapped<Epi::kDz, bf16, true>(ma, mb, mo, mr, p, stream)
                : launch_mapped<Epi::kDz, float, true>(ma, mb, mo, mr, p, stream);

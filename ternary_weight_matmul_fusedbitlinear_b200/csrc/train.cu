@@ -19,17 +19,23 @@ struct PrepUnits {
   size_t w_units, q_units, g_units;   // 16 weights; 16 codes; 8 gradient columns
   int g_row_units;
 };
+struct PrepList {
+  PrepUnits u[2];
+};
 
 // One launch for the operands of a backward: packed codes -> bf16 (and bytes),
 // int8 codes -> bf16, the gradient -> padded bf16 planes. Each unit is one
 // 16- or 32-byte store.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) train_prep_kernel(const PrepUnits u) {
+__global__ void __launch_bounds__(kThreads) train_prep_kernel(const __grid_constant__ PrepList list) {
   pdl_trigger();
   pdl_wait();
-  const PrepArgs& a = u.a;
-  const size_t total = u.w_units + u.q_units + u.g_units;
-  for (size_t id = (size_t)blockIdx.x * kThreads + threadIdx.x; id < total; id += (size_t)gridDim.x * kThreads) {
+  const size_t total0 = list.u[0].w_units + list.u[0].q_units + list.u[0].g_units;
+  const size_t total = total0 + list.u[1].w_units + list.u[1].q_units + list.u[1].g_units;
+  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (size_t)gridDim.x * kThreads) {
+    const PrepUnits& u = list.u[i >= total0];
+    const PrepArgs& a = u.a;
+    const size_t id = i >= total0 ? i - total0 : i;
     if (id < u.w_units) {
       const int wpr = a.K / 16;
       const int row = (int)(id / wpr), j = (int)(id % wpr);
@@ -290,6 +296,20 @@ __global__ void __launch_bounds__(kThreads) norm_back_kernel(const NormBackArgs 
   }
 }
 
+// c = mean(dx^ x^) of each row from the partial sums of dx^ q that the product's
+// epilogue left, one per 128 columns.
+__global__ void __launch_bounds__(kThreads) dot_join_kernel(const float* __restrict__ part, int slots, int M, int K,
+                                                            const float* __restrict__ scale, float* __restrict__ cmean) {
+  pdl_trigger();
+  pdl_wait();
+  const int m = blockIdx.x * kThreads + threadIdx.x;
+  if (m >= M) return;
+  float s = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < slots; ++i) s += part[(size_t)i * M + m];
+  cmean[m] = s / scale[m] / (float)K;
+}
+
 // ---------------------------------------------------------------- column sums
 constexpr int kColsPerBlock = 64, kColLanes = kColsPerBlock / 4, kRowLanes = kThreads / kColLanes;
 
@@ -334,48 +354,72 @@ __device__ __forceinline__ void col_store(const ColSumArgs& a, int c, float v) {
   static_cast<T*>(a.out[seg])[n] = from_f32<T>(v);
 }
 
-// Block (x: 64 columns, y: a range of rows); a thread sums every 16th row of 4
-// columns, the 16 are added in order. One range writes the result, several
-// write partial sums.
+struct ColSumTask {
+  ColSumArgs a;
+  ColSum kind;
+  int cols, parts, rows_per, block0;   // block0: the task's first block
+};
+struct ColSumTasks {
+  ColSumTask t[kMaxColSums];
+  int n;
+};
+
 template <ColSum KIND, typename T>
-__global__ void __launch_bounds__(kThreads) colsum_kernel(const ColSumArgs a, int cols, int rows_per) {
+__device__ __forceinline__ void col_range(const ColSumArgs& a, int t0, int t1, int c, int cols, float (&sum)[4]) {
+  const bool vec = cols % 4 == 0;
+#pragma unroll 4
+  for (int t = t0; t < t1; t += kRowLanes) {
+    float v[4];
+    col_terms<KIND, T>(a, t, c, cols, vec, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] += v[i];
+  }
+}
+
+// All of a call's column sums in one launch. A block has 64 columns and a range
+// of rows of one task; a thread sums every 16th row of 4 columns, the 16 are
+// added in order. One range writes the result, several write partial sums.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) colsum_kernel(const __grid_constant__ ColSumTasks l) {
   __shared__ float red[kRowLanes][kColsPerBlock];
   pdl_trigger();
   pdl_wait();
-  const int c = blockIdx.x * kColsPerBlock + threadIdx.x % kColLanes * 4, rl = threadIdx.x / kColLanes;
-  const int t0 = blockIdx.y * rows_per, t1 = min(a.M, t0 + rows_per);
-  const bool vec = cols % 4 == 0;
+  int i = 0;
+  while (i + 1 < l.n && (int)blockIdx.x >= l.t[i + 1].block0) ++i;
+  const ColSumTask& k = l.t[i];
+  const int cb = ((int)blockIdx.x - k.block0) / k.parts, part = ((int)blockIdx.x - k.block0) % k.parts;
+  const int c = cb * kColsPerBlock + threadIdx.x % kColLanes * 4, rl = threadIdx.x / kColLanes;
+  const int t0 = part * k.rows_per, t1 = min(k.a.M, t0 + k.rows_per);
   float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (c < cols) {
-#pragma unroll 4
-    for (int t = t0 + rl; t < t1; t += kRowLanes) {
-      float v[4];
-      col_terms<KIND, T>(a, t, c, cols, vec, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum[i] += v[i];
+  if (c < k.cols) {
+    switch (k.kind) {
+      case ColSum::kGrad: col_range<ColSum::kGrad, T>(k.a, t0 + rl, t1, c, k.cols, sum); break;
+      case ColSum::kPlanes: col_range<ColSum::kPlanes, T>(k.a, t0 + rl, t1, c, k.cols, sum); break;
+      case ColSum::kGain: col_range<ColSum::kGain, T>(k.a, t0 + rl, t1, c, k.cols, sum); break;
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) red[rl][threadIdx.x % kColLanes * 4 + i] = sum[i];
+  for (int j = 0; j < 4; ++j) red[rl][threadIdx.x % kColLanes * 4 + j] = sum[j];
   __syncthreads();
-  const int cc = blockIdx.x * kColsPerBlock + threadIdx.x;
-  if (threadIdx.x < kColsPerBlock && cc < cols) {
+  const int cc = cb * kColsPerBlock + threadIdx.x;
+  if (threadIdx.x < kColsPerBlock && cc < k.cols) {
     float v = red[0][threadIdx.x];
-    for (int i = 1; i < kRowLanes; ++i) v += red[i][threadIdx.x];
-    if (gridDim.y == 1) col_store<T>(a, cc, v);
-    else a.part[(size_t)blockIdx.y * cols + cc] = v;
+    for (int j = 1; j < kRowLanes; ++j) v += red[j][threadIdx.x];
+    if (k.parts == 1) col_store<T>(k.a, cc, v);
+    else k.a.part[(size_t)part * k.cols + cc] = v;
   }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) colsum_join_kernel(const ColSumArgs a, int cols, int parts) {
+__global__ void __launch_bounds__(kThreads) colsum_join_kernel(const __grid_constant__ ColSumTasks l) {
   pdl_trigger();
   pdl_wait();
+  const ColSumTask& k = l.t[blockIdx.y];
   const int c = blockIdx.x * kThreads + threadIdx.x;
-  if (c >= cols) return;
+  if (c >= k.cols || k.parts == 1) return;
   float v = 0.0f;
-  for (int i = 0; i < parts; ++i) v += a.part[(size_t)i * cols + c];
-  col_store<T>(a, c, v);
+  for (int i = 0; i < k.parts; ++i) v += k.a.part[(size_t)i * k.cols + c];
+  col_store<T>(k.a, c, v);
 }
 
 // Row ranges: at least 256 rows each (16 per thread; below that one launch is
@@ -419,15 +463,16 @@ __global__ void __launch_bounds__(kThreads) dw_join_kernel(const DwJoinArgs a) {
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kJoinRows = 32, kJoinGroups = kThreads / kJoinRows;
 
-// 32 rows per block, 8 threads per row: thread (row, g) folds the row's slots
+__device__ __forceinline__ bool counted_label(const LossArgs& a, int l) {
+  return l != a.ignore_index && l >= 0 && l < a.vocab;
+}
+
+// 32 rows at a time, 8 threads per row: thread (row, g) folds the row's slots
 // g, g + 8, ... (slot-major, so a warp reads 32 neighbouring rows), the eight
 // are folded in order. loss_t = (lse - z_label), both in log2 units until here.
-__global__ void __launch_bounds__(kThreads) loss_rows_kernel(const LossArgs a, int* status) {
-  __shared__ float2 red[kJoinGroups][kJoinRows];
-  pdl_trigger();
-  pdl_wait();
-  const int r = threadIdx.x % kJoinRows, g = threadIdx.x / kJoinRows;
-  const int m = blockIdx.x * kJoinRows + r;
+// Returns this thread's row's loss (0 but for g = 0).
+__device__ __forceinline__ float loss_rows(const LossArgs& a, int m, int r, int g, float2 (*red)[kJoinRows],
+                                           int* status) {
   float mx = -INFINITY, sum = 0.0f;
   auto fold = [&](float2 o) {
     const float nm = fmaxf(mx, o.x);
@@ -441,17 +486,53 @@ __global__ void __launch_bounds__(kThreads) loss_rows_kernel(const LossArgs a, i
   }
   red[g][r] = make_float2(mx, sum);
   __syncthreads();
+  float loss = 0.0f;
   if (g == 0 && m < a.M) {
     for (int i = 1; i < kJoinGroups; ++i) fold(red[i][r]);
     const float lse2 = mx + log2f(sum);
     const int l = a.labels[m];
-    float loss = 0.0f;
-    if (l != a.ignore_index) {
-      if (l >= 0 && l < a.vocab) loss = (lse2 - a.zlabel[m]) * kLn2;
-      else if (status != nullptr) atomicExch(status, 9);   // reported by mmf_check; counts as ignored
-    }
+    if (counted_label(a, l)) loss = (lse2 - a.zlabel[m]) * kLn2;
+    else if (l != a.ignore_index && status != nullptr) atomicExch(status, 9);   // reported by mmf_check
     a.lse[m] = lse2 * kLn2;
     a.token[m] = loss;
+  }
+  __syncthreads();
+  return loss;
+}
+
+__device__ __forceinline__ void loss_out(const LossArgs& a, double s, int n) {
+  const float count = (float)max(1, n);
+  *a.count = count;
+  *a.loss = (float)(a.reduction == MMF_REDUCE_MEAN ? s / (double)count : s);
+}
+
+__global__ void __launch_bounds__(kThreads) loss_rows_kernel(const LossArgs a, int* status) {
+  __shared__ float2 red[kJoinGroups][kJoinRows];
+  pdl_trigger();
+  pdl_wait();
+  const int r = threadIdx.x % kJoinRows;
+  loss_rows(a, blockIdx.x * kJoinRows + r, r, threadIdx.x / kJoinRows, red, status);
+}
+
+// Few tokens: rows and reduction in one block.
+__global__ void __launch_bounds__(kThreads) loss_small_kernel(const LossArgs a, int* status) {
+  __shared__ float2 red[kJoinGroups][kJoinRows];
+  pdl_trigger();
+  pdl_wait();
+  const int r = threadIdx.x % kJoinRows, g = threadIdx.x / kJoinRows;
+  double s = 0.0;
+  int n = 0;
+  for (int m0 = 0; m0 < a.M; m0 += kJoinRows) {
+    s += (double)loss_rows(a, m0 + r, r, g, red, status);
+    n += g == 0 && m0 + r < a.M && counted_label(a, a.labels[m0 + r]);
+  }
+  if (g == 0) {   // one warp holds all of it
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      n += __shfl_xor_sync(0xffffffffu, n, o);
+    }
+    if (r == 0) loss_out(a, s, n);
   }
 }
 
@@ -466,7 +547,7 @@ __global__ void __launch_bounds__(1024) loss_reduce_kernel(const LossArgs a) {
   for (int m = threadIdx.x; m < a.M; m += 1024) {
     s += (double)a.token[m];
     const int l = a.labels[m];
-    n += l != a.ignore_index && l >= 0 && l < a.vocab;
+    n += counted_label(a, l);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -483,9 +564,7 @@ __global__ void __launch_bounds__(1024) loss_reduce_kernel(const LossArgs a) {
       s += sums[w];
       n += counts[w];
     }
-    const float count = (float)max(1, n);
-    *a.count = count;
-    *a.loss = (float)(a.reduction == MMF_REDUCE_MEAN ? s / (double)count : s);
+    loss_out(a, s, n);
   }
 }
 
@@ -495,18 +574,24 @@ int blocks_for(size_t units, int per_sm) {
 
 }  // namespace
 
-cudaError_t launch_train_prep(const PrepArgs& a, cudaStream_t stream) {
-  PrepUnits u;
-  u.a = a;
-  u.w_units = a.nseg > 0 ? (size_t)a.nseg * a.w_pitch * (a.K / 16) : 0;
-  u.q_units = a.qb != nullptr ? (size_t)a.M * (a.qK / 16) : 0;
-  u.g_row_units = a.gb != nullptr ? a.g_seg * a.g_pitch / 8 : 0;
-  u.g_units = (size_t)u.g_row_units * a.g_rows;
-  const size_t total = u.w_units + u.q_units + u.g_units;
+cudaError_t launch_train_prep(const PrepArgs* const* sets, int n, cudaStream_t stream) {
+  PrepList list = {};
+  size_t total = 0;
+  mmf_dtype dt = MMF_BF16;
+  for (int i = 0; i < n; ++i) {
+    PrepUnits& u = list.u[i];
+    const PrepArgs& a = u.a = *sets[i];
+    u.w_units = a.nseg > 0 ? (size_t)a.nseg * a.w_pitch * (a.K / 16) : 0;
+    u.q_units = a.qb != nullptr ? (size_t)a.M * (a.qK / 16) : 0;
+    u.g_row_units = a.gb != nullptr ? a.g_seg * a.g_pitch / 8 : 0;
+    u.g_units = (size_t)u.g_row_units * a.g_rows;
+    total += u.w_units + u.q_units + u.g_units;
+    if (a.gb != nullptr) dt = a.dy_dt;
+  }
   if (total == 0) return cudaSuccess;
   const dim3 grid(blocks_for(total, 8));
-  return a.dy_dt == MMF_BF16 ? launch_pdl(train_prep_kernel<bf16>, grid, dim3(kThreads), 0, stream, u)
-                             : launch_pdl(train_prep_kernel<float>, grid, dim3(kThreads), 0, stream, u);
+  return dt == MMF_BF16 ? launch_pdl(train_prep_kernel<bf16>, grid, dim3(kThreads), 0, stream, list)
+                        : launch_pdl(train_prep_kernel<float>, grid, dim3(kThreads), 0, stream, list);
 }
 
 template <typename T, int WPR, int NV, bool STAT>
@@ -541,27 +626,42 @@ cudaError_t launch_norm_back(const NormBackArgs& a, bool stat, mmf_dtype dt, cud
   return dt == MMF_BF16 ? norm_back_typed<bf16, false>(a, stream) : norm_back_typed<float, false>(a, stream);
 }
 
+cudaError_t launch_dot_join(const float* part, int slots, int M, int K, const float* scale, float* cmean,
+                            cudaStream_t stream) {
+  return launch_pdl(dot_join_kernel, dim3(ceil_div(M, kThreads)), dim3(kThreads), 0, stream, part, slots, M, K, scale,
+                    cmean);
+}
+
 size_t colsum_ws_floats(int M, int cols) {
   const int parts = colsum_parts(M, cols);
   return parts > 1 ? (size_t)parts * cols : 0;
 }
 
 template <typename T>
-static cudaError_t colsum_typed(const ColSumArgs& a, ColSum kind, cudaStream_t stream) {
-  const int cols = a.segs * a.pitch, parts = colsum_parts(a.M, cols), rows_per = ceil_div(a.M, parts);
-  const dim3 grid(ceil_div(cols, kColsPerBlock), parts), block(kThreads);
-  cudaError_t e = cudaSuccess;
-  switch (kind) {
-    case ColSum::kGrad: e = launch_pdl(colsum_kernel<ColSum::kGrad, T>, grid, block, 0, stream, a, cols, rows_per); break;
-    case ColSum::kPlanes: e = launch_pdl(colsum_kernel<ColSum::kPlanes, T>, grid, block, 0, stream, a, cols, rows_per); break;
-    case ColSum::kGain: e = launch_pdl(colsum_kernel<ColSum::kGain, T>, grid, block, 0, stream, a, cols, rows_per); break;
-  }
-  if (e != cudaSuccess || parts == 1) return e;
-  return launch_pdl(colsum_join_kernel<T>, dim3(ceil_div(cols, kThreads)), block, 0, stream, a, cols, parts);
+static cudaError_t colsum_typed(const ColSumTasks& l, int blocks, int join_cols, cudaStream_t stream) {
+  const cudaError_t e = launch_pdl(colsum_kernel<T>, dim3(blocks), dim3(kThreads), 0, stream, l);
+  if (e != cudaSuccess || join_cols == 0) return e;
+  return launch_pdl(colsum_join_kernel<T>, dim3(ceil_div(join_cols, kThreads), l.n), dim3(kThreads), 0, stream, l);
 }
 
-cudaError_t launch_colsum(const ColSumArgs& a, ColSum kind, mmf_dtype dt, cudaStream_t stream) {
-  return dt == MMF_BF16 ? colsum_typed<bf16>(a, kind, stream) : colsum_typed<float>(a, kind, stream);
+cudaError_t launch_colsums(const ColSumList& list, mmf_dtype dt, cudaStream_t stream) {
+  if (list.n == 0) return cudaSuccess;
+  ColSumTasks l = {};
+  int blocks = 0, join_cols = 0;
+  for (int i = 0; i < list.n; ++i) {
+    ColSumTask& k = l.t[i];
+    k.a = list.a[i];
+    k.kind = list.kind[i];
+    k.cols = k.a.segs * k.a.pitch;
+    k.parts = colsum_parts(k.a.M, k.cols);
+    k.rows_per = ceil_div(k.a.M, k.parts);
+    k.block0 = blocks;
+    blocks += ceil_div(k.cols, kColsPerBlock) * k.parts;
+    if (k.parts > 1) join_cols = std::max(join_cols, k.cols);
+  }
+  l.n = list.n;
+  return dt == MMF_BF16 ? colsum_typed<bf16>(l, blocks, join_cols, stream)
+                        : colsum_typed<float>(l, blocks, join_cols, stream);
 }
 
 cudaError_t launch_dw_join(const DwJoinArgs& a, mmf_dtype dt, cudaStream_t stream) {
@@ -571,6 +671,8 @@ cudaError_t launch_dw_join(const DwJoinArgs& a, mmf_dtype dt, cudaStream_t strea
 }
 
 cudaError_t launch_loss_join(const LossArgs& a, int* status, cudaStream_t stream) {
+  if (a.M <= 8 * kJoinRows && a.reduction != MMF_REDUCE_NONE)
+    return launch_pdl(loss_small_kernel, dim3(1), dim3(kThreads), 0, stream, a, status);
   cudaError_t e = launch_pdl(loss_rows_kernel, dim3(ceil_div(a.M, kJoinRows)), dim3(kThreads), 0, stream, a, status);
   if (e != cudaSuccess || a.reduction == MMF_REDUCE_NONE) return e;
   return launch_pdl(loss_reduce_kernel, dim3(1), dim3(1024), 0, stream, a);

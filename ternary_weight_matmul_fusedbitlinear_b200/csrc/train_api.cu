@@ -108,7 +108,8 @@ size_t dw_floats(const Products& p) {
 // columns `pitch` apart (dw null: not wanted).
 mmf_status run_products(const Products& pr, const Grad& G, const void* wb, const float* const* gamma,
                         const float* scale, bool accumulate, float* dxh, const void* qb, int dw_seg, int N, int pitch,
-                        const float* const* inv_gamma, void* const* dw, float* part, mmf_dtype dt, cudaStream_t s) {
+                        const float* const* inv_gamma, void* const* dw, float* part, mmf_dtype dt, cudaStream_t s,
+                        const int8_t* dot_q = nullptr, float* dot_part = nullptr) {
   const int M = pr.dx.I, K = pr.dx.J;
   BGemmArgs x = {}, w = {};
   x.sh = pr.dx;
@@ -126,6 +127,8 @@ mmf_status run_products(const Products& pr, const Grad& G, const void* wb, const
   x.accumulate = accumulate;
   for (int i = 0; gamma != nullptr && i < pr.dx.nseg; ++i) x.gamma[i] = gamma[i];
   x.row_scale = G.over_s ? scale : nullptr;
+  x.dot_q = dot_q;
+  x.dot_part = dot_part;
   w.splits = pr.plan.splits[1];
   w.slice_rows = bgemm_slice_rows(pr.dw.I);
   w.seg_rows = N;
@@ -184,23 +187,36 @@ NormBackArgs norm_args(float* dxh, int slices, int M, int K, const mmf_act8& k, 
   return n;
 }
 
-// dx and dgain from dx^.
-mmf_status run_norm(NormBackArgs n, const void* dres, void* dx, void* dgain, float* colpart, mmf_dtype dt,
-                    cudaStream_t s) {
+// dx from dx^; the gain's gradient joins the column sums.
+mmf_status run_norm(NormBackArgs n, const void* dres, void* dx, void* dgain, float* colpart, ColSumList& sums,
+                    mmf_dtype dt, cudaStream_t s) {
   n.dres = dres;
   n.dx = dx;
   if (dx != nullptr)
     MMF_CUDA(timed("norm_back", s, [&] { return launch_norm_back(n, false, dt, s); }), "norm backward");
   if (dgain != nullptr) {
-    ColSumArgs c = {};
+    ColSumArgs& c = sums.a[sums.n];
+    c = ColSumArgs{};
+    sums.kind[sums.n++] = ColSum::kGain;
     c.M = n.M;
     c.segs = 1;
     c.N = c.pitch = n.K;
     c.nb = n;
     c.out[0] = dgain;
     c.part = colpart;
-    MMF_CUDA(timed("colsum", s, [&] { return launch_colsum(c, ColSum::kGain, dt, s); }), "gain gradient");
   }
+  return MMF_OK;
+}
+
+mmf_status run_sums(ColSumList& sums, mmf_dtype dt, cudaStream_t s) {
+  if (sums.n > 0) MMF_CUDA(timed("colsum", s, [&] { return launch_colsums(sums, dt, s); }), "column sums");
+  sums.n = 0;
+  return MMF_OK;
+}
+
+mmf_status run_prep(const PrepArgs* a, const PrepArgs* b, cudaStream_t s) {
+  const PrepArgs* sets[2] = {a, b};
+  MMF_CUDA(timed("train_prep", s, [&] { return launch_train_prep(sets, b != nullptr ? 2 : 1, s); }), "operands");
   return MMF_OK;
 }
 
@@ -227,9 +243,10 @@ LinearPlan linear_plan(int nlin, int N, int M, mmf_dtype dt) {
 struct LinearWs {
   Products pr;
   void *wb, *qb, *gb;
-  float *dxh, *part, *colpart;
+  float *dxh, *part, *colpart, *dots;
+  size_t gain_floats;   // the gain's share of colpart; the biases' follow
 };
-LinearWs carve_linear(Carver& c, int nlin, int N, int K, int M, mmf_dtype dt) {
+LinearWs carve_linear(Carver& c, int nlin, int N, int K, int M, mmf_dtype dt, bool dots = false) {
   const LinearPlan p = linear_plan(nlin, N, M, dt);
   LinearWs w;
   w.wb = c.take<char>((size_t)p.cols * K * 2);
@@ -238,24 +255,17 @@ LinearWs carve_linear(Carver& c, int nlin, int N, int K, int M, mmf_dtype dt) {
   w.pr = products(M, K, nlin, p.pitch, nlin == 1 ? N : p.cols, dt);
   w.dxh = c.take<float>(dxh_floats(w.pr));
   w.part = c.take<float>(dw_floats(w.pr));
-  w.colpart = c.take<float>(std::max(colsum_ws_floats(M, K), colsum_ws_floats(M, nlin * N)));
+  w.gain_floats = colsum_ws_floats(M, K);
+  w.colpart = c.take<float>(w.gain_floats + colsum_ws_floats(M, nlin * N));
+  w.dots = c.take<float>(dots ? (size_t)2 * ceil_div(K, 256) * M : 0);
   return w;
 }
 
-// The backward of nlin layers; also writes dx^ only (stat: into cmean) for the
-// GLU's down projection, whose norm's gradient the next kernel applies.
-mmf_status linear_backward(const mmf_tlinear* lins, int nlin, const mmf_act8& kept, const void* x, const void* dy,
-                           const void* dres, mmf_dtype dt, int M, const mmf_linear_grads& g, const LinearWs& w,
-                           float* cmean, cudaStream_t s) {
+// The operands of nlin layers' backward.
+PrepArgs linear_prep(const mmf_tlinear* lins, int nlin, const mmf_act8& kept, const void* dy, mmf_dtype dt, int M,
+                     bool want_dxh, bool want_dw, const LinearWs& w) {
   const int N = lins[0].N, K = lins[0].K;
   const LinearPlan lp = linear_plan(nlin, N, M, dt);
-  const bool want_dxh = g.dx != nullptr || g.dgain != nullptr || cmean != nullptr;
-  bool want_dw = false;
-  void* dw[3] = {};
-  for (int i = 0; i < nlin; ++i) {
-    dw[i] = g.dw[i];
-    want_dw = want_dw || dw[i] != nullptr;
-  }
   PrepArgs pa = {};
   pa.M = M;
   pa.scale = kept.scale;
@@ -284,8 +294,24 @@ mmf_status linear_backward(const mmf_tlinear* lins, int nlin, const mmf_act8& ke
     pa.g_scaled = dt == MMF_F32;
     pa.gb = w.gb;
   }
-  if (want_dxh || want_dw)
-    MMF_CUDA(timed("train_prep", s, [&] { return launch_train_prep(pa, s); }), "operands");
+  return pa;
+}
+
+// The backward of nlin layers on prepared operands. cmean: also the row means of
+// dx^ x^, with dx^ in one slice, for the GLU's down projection, whose norm's
+// gradient the next kernel applies.
+mmf_status linear_backward(const mmf_tlinear* lins, int nlin, const mmf_act8& kept, const void* x, const void* dy,
+                           const void* dres, mmf_dtype dt, int M, const mmf_linear_grads& g, const LinearWs& w,
+                           float* cmean, ColSumList& sums, cudaStream_t s) {
+  const int N = lins[0].N, K = lins[0].K;
+  const LinearPlan lp = linear_plan(nlin, N, M, dt);
+  const bool want_dxh = g.dx != nullptr || g.dgain != nullptr || cmean != nullptr;
+  bool want_dw = false;
+  void* dw[3] = {};
+  for (int i = 0; i < nlin; ++i) {
+    dw[i] = g.dw[i];
+    want_dw = want_dw || dw[i] != nullptr;
+  }
   Grad G;
   G.g = lp.copy ? w.gb : dy;
   G.ld = lp.cols;
@@ -294,31 +320,38 @@ mmf_status linear_backward(const mmf_tlinear* lins, int nlin, const mmf_act8& ke
   G.over_s = dt == MMF_F32;
   mmf_status r = MMF_OK;
   const float* gam[3] = {lins[0].gamma, lins[nlin > 1 ? 1 : 0].gamma, lins[nlin > 2 ? 2 : 0].gamma};
+  // the means come with the product where one launch of it leaves whole sums
+  const bool dots = cmean != nullptr && nlin == 1 && dt == MMF_BF16 && !w.pr.plan.together && w.pr.plan.splits[0] == 1;
   if (want_dxh || want_dw)
     r = run_products(w.pr, G, w.wb, gam, kept.scale, false, want_dxh ? w.dxh : nullptr, w.qb, nlin, N, lp.pitch,
-                     nullptr, want_dw ? dw : nullptr, w.part, dt, s);
+                     nullptr, want_dw ? dw : nullptr, w.part, dt, s, dots ? kept.q : nullptr, w.dots);
   if (r != MMF_OK) return r;
   if (want_dxh) {
     NormBackArgs n = norm_args(w.dxh, w.pr.plan.splits[0], M, K, kept, lins[0].gain, x);
-    if (cmean != nullptr) {
+    if (dots) {
+      const int slots = ceil_div(K, 128);
+      MMF_CUDA(timed("dot_join", s, [&] { return launch_dot_join(w.dots, slots, M, K, kept.scale, cmean, s); }),
+               "norm backward");
+    } else if (cmean != nullptr) {
       n.cmean = cmean;
       MMF_CUDA(timed("norm_stat", s, [&] { return launch_norm_back(n, true, dt, s); }), "norm backward");
       n.slices = 1;
     }
-    r = run_norm(n, dres, g.dx, g.dgain, w.colpart, dt, s);
+    r = run_norm(n, dres, g.dx, g.dgain, w.colpart, sums, dt, s);
     if (r != MMF_OK) return r;
   }
   bool want_db = false;
   for (int i = 0; i < nlin; ++i) want_db = want_db || g.dbias[i] != nullptr;
   if (want_db) {
-    ColSumArgs c = {};
+    ColSumArgs& c = sums.a[sums.n];
+    c = ColSumArgs{};
+    sums.kind[sums.n++] = ColSum::kGrad;
     c.src = dy;
     c.M = M;
     c.segs = nlin;
     c.N = c.pitch = N;
     for (int i = 0; i < nlin; ++i) c.out[i] = g.dbias[i];
-    c.part = w.colpart;
-    MMF_CUDA(timed("colsum", s, [&] { return launch_colsum(c, ColSum::kGrad, dt, s); }), "bias gradient");
+    c.part = w.colpart + w.gain_floats;
   }
   return MMF_OK;
 }
@@ -341,8 +374,8 @@ mmf_status zero_grads(const mmf_linear_grads& g, int n, int N, int K, mmf_dtype 
 
 }  // namespace
 
-extern "C" size_t mmf_bitlinear_train_ws_size(int32_t nlin, int32_t N, int32_t K) {
-  if (nlin < 1 || nlin > 3 || N < 0 || K < 0) return 0;
+extern "C" size_t mmf_bitlinear_train_ws_size(int32_t nlin, int32_t N, int32_t K, int32_t M) {
+  if (nlin < 1 || nlin > 3 || N < 0 || K < 0 || M < kUnpackMinTokens) return 0;
   return round_up((size_t)nlin * N * K, 256) + 1024;
 }
 
@@ -355,10 +388,11 @@ extern "C" mmf_status mmf_bitlinear_train(const mmf_tlinear* lins, int32_t nlin,
   if (r != MMF_OK) return r;
   if (!(eps > 0.0f)) return fail(MMF_ERR_INVALID_ARG, "%s: eps must be > 0", what);
   if (M == 0) return MMF_OK;
-  if ((r = check_ptrs(what, {x, y, ws}, {})) != MMF_OK || (r = check_kept(kept, what)) != MMF_OK) return r;
+  if ((r = check_ptrs(what, {x, y}, {ws})) != MMF_OK || (r = check_kept(kept, what)) != MMF_OK) return r;
   const int N = lins[0].N, K = lins[0].K;
-  if (ws_bytes < mmf_bitlinear_train_ws_size(nlin, N, K))
-    return fail(MMF_ERR_WORKSPACE, "%s: ws_bytes=%zu < %zu", what, ws_bytes, mmf_bitlinear_train_ws_size(nlin, N, K));
+  const size_t need = mmf_bitlinear_train_ws_size(nlin, N, K, M);
+  if (ws_bytes < need || (need > 0 && ws == nullptr))
+    return fail(MMF_ERR_WORKSPACE, "%s: ws_bytes=%zu < %zu", what, ws_bytes, need);
   cudaStream_t s = as_stream(stream);
   if ((r = quant_keep(x, dtype, M, K, lins[0].gain, eps, *kept, s)) != MMF_OK) return r;
   const mmf_tlinear* segs[3] = {&lins[0], &lins[nlin > 1 ? 1 : 0], &lins[nlin > 2 ? 2 : 0]};
@@ -376,7 +410,8 @@ extern "C" mmf_status mmf_bitlinear_train(const mmf_tlinear* lins, int32_t nlin,
       pa.wu[i] = a.wu[i] == nullptr ? u : nullptr;
       if (a.wu[i] == nullptr) a.wu[i] = u;
     }
-    MMF_CUDA(timed("train_prep", s, [&] { return launch_train_prep(pa, s); }), "one-byte codes");
+    const PrepArgs* sets[1] = {&pa};
+    MMF_CUDA(timed("train_prep", s, [&] { return launch_train_prep(sets, 1, s); }), "one-byte codes");
   }
   MMF_CUDA(run_gemm(a, Epi::kStore, dtype, s, "train"), "contraction");
   return MMF_OK;
@@ -402,11 +437,18 @@ extern "C" mmf_status mmf_bitlinear_backward(const mmf_tlinear* lins, int32_t nl
   cudaStream_t s = as_stream(stream);
   if (M == 0) return zero_grads(*grads, nlin, N, K, dtype, s);
   if ((r = check_ptrs(what, {dy, ws}, {x, dres})) != MMF_OK || (r = check_kept(kept, what)) != MMF_OK) return r;
-  const size_t need = mmf_bitlinear_backward_ws_size(nlin, N, K, M, dtype);
-  if (ws_bytes < need) return fail(MMF_ERR_WORKSPACE, "%s: ws_bytes=%zu < %zu", what, ws_bytes, need);
   Carver c(ws);
   const LinearWs w = carve_linear(c, nlin, N, K, M, dtype);
-  return linear_backward(lins, nlin, *kept, x, dy, dres, dtype, M, *grads, w, nullptr, s);
+  if (ws_bytes < c.off + 256) return fail(MMF_ERR_WORKSPACE, "%s: ws_bytes=%zu < %zu", what, ws_bytes, c.off + 256);
+  bool want_dw = false;
+  for (int i = 0; i < nlin; ++i) want_dw = want_dw || grads->dw[i] != nullptr;
+  const bool want_dxh = grads->dx != nullptr || grads->dgain != nullptr;
+  const PrepArgs pa = linear_prep(lins, nlin, *kept, dy, dtype, M, want_dxh, want_dw, w);
+  ColSumList sums;
+  sums.n = 0;
+  r = run_prep(&pa, nullptr, s);
+  if (r == MMF_OK) r = linear_backward(lins, nlin, *kept, x, dy, dres, dtype, M, *grads, w, nullptr, sums, s);
+  return r == MMF_OK ? run_sums(sums, dtype, s) : r;
 }
 
 // ------------------------------------------------------------------ GLU
@@ -469,14 +511,12 @@ struct GluWs {
   uint8_t *wu_gate, *wu_up;
   void *wb, *qb, *dz;
   float *cmean, *dxh, *part, *colpart;
+  size_t gain_floats;
 };
-// The down projection's scratch and the gate | up one live at different times,
-// except the down projection's dx^ (read by the recompute) - they are carved
-// one behind the other all the same.
 GluWs carve_glu(Carver& c, int M, int d, int I, mmf_dtype dt) {
   const int Ip = pad(I, 32), rows = plane_rows_of(M, dt);
   GluWs w;
-  w.down = carve_linear(c, 1, d, I, M, dt);
+  w.down = carve_linear(c, 1, d, I, M, dt, true);
   w.wu_gate = c.take<uint8_t>((size_t)I * d);
   w.wu_up = c.take<uint8_t>((size_t)I * d);
   w.wb = c.take<char>((size_t)2 * Ip * d * 2);
@@ -486,7 +526,8 @@ GluWs carve_glu(Carver& c, int M, int d, int I, mmf_dtype dt) {
   w.pr = products(M, d, 1, 2 * Ip, 2 * Ip, dt);
   w.dxh = c.take<float>(dxh_floats(w.pr));
   w.part = c.take<float>(dw_floats(w.pr));
-  w.colpart = c.take<float>(std::max(colsum_ws_floats(M, d), colsum_ws_floats(M, 2 * Ip)));
+  w.gain_floats = colsum_ws_floats(M, d);
+  w.colpart = c.take<float>(w.gain_floats + colsum_ws_floats(M, 2 * Ip));
   return w;
 }
 
@@ -524,21 +565,18 @@ extern "C" mmf_status mmf_glu_backward(const mmf_tlinear* gate, const mmf_tlinea
   if ((r = check_ptrs(what, {dy, ws}, {x, dres})) != MMF_OK || (r = check_kept(kept_x, what)) != MMF_OK ||
       (r = check_kept(kept_p, what)) != MMF_OK)
     return r;
-  const size_t need = mmf_glu_backward_ws_size(M, d, I, dtype);
-  if (ws_bytes < need) return fail(MMF_ERR_WORKSPACE, "%s: ws_bytes=%zu < %zu", what, ws_bytes, need);
   Carver c(ws);
   const GluWs w = carve_glu(c, M, d, I, dtype);
+  if (ws_bytes < c.off + 256) return fail(MMF_ERR_WORKSPACE, "%s: ws_bytes=%zu < %zu", what, ws_bytes, c.off + 256);
 
   const bool want_dxh = gx.dx != nullptr || gx.dgain != nullptr;
   const bool want_dw = gx.dw[0] != nullptr || gx.dw[1] != nullptr;
   const bool want_db = gx.dbias[0] != nullptr || gx.dbias[1] != nullptr;
   const bool inner = want_dxh || want_dw || want_db;   // anything behind the product
-  // 1. the down projection: dW, its gain's and bias's gradient, dx^ of p and its row means
-  r = linear_backward(down, 1, *kept_p, nullptr, dy, nullptr, dtype, M, gd, w.down, inner ? w.cmean : nullptr, s);
-  if (r != MMF_OK || !inner) return r;
-  // 2. u, v again; du, dv over the row's scale (and times gamma, so that gate and up add up in one product)
+  // 1. every operand
   const int Ip = pad(I, 32), rows = plane_rows_of(M, dtype), planes = planes_of(dtype);
   const mmf_tlinear* gu[2] = {gate, up};
+  const PrepArgs pd = linear_prep(down, 1, *kept_p, dy, dtype, M, inner || gd.dgain != nullptr, gd.dw[0] != nullptr, w.down);
   PrepArgs pa = {};
   pa.M = M;
   pa.scale = kept_x->scale;
@@ -557,7 +595,14 @@ extern "C" mmf_status mmf_glu_backward(const mmf_tlinear* gate, const mmf_tlinea
     pa.qK = d;
     pa.qb = w.qb;
   }
-  MMF_CUDA(timed("train_prep", s, [&] { return launch_train_prep(pa, s); }), "operands");
+  ColSumList sums;
+  sums.n = 0;
+  if ((r = run_prep(&pd, inner ? &pa : nullptr, s)) != MMF_OK) return r;
+  // 2. the down projection: dW, its gain's and bias's gradient, dx^ of p and its row means
+  r = linear_backward(down, 1, *kept_p, nullptr, dy, nullptr, dtype, M, gd, w.down, inner ? w.cmean : nullptr, sums, s);
+  if (r != MMF_OK) return r;
+  if (!inner) return run_sums(sums, dtype, s);
+  // 3. u, v again; du, dv over the row's scale (and times gamma, so that gate and up add up in one product)
   TGemmArgs a = gemm_args(gu, 2, kept_x->q, kept_x->scale, kept_x->qsum, M, w.dz, 2 * Ip, nullptr, nullptr);
   if (a.wu[0] == nullptr) a.wu[0] = w.wu_gate;
   if (a.wu[1] == nullptr) a.wu[1] = w.wu_up;
@@ -572,7 +617,7 @@ extern "C" mmf_status mmf_glu_backward(const mmf_tlinear* gate, const mmf_tlinea
   t.plane_cols = Ip;
   MMF_CUDA(timed("tgemm_tc:glu_back", s, [&] { return launch_tgemm_train(a, t, Epi::kGluBwd, dtype, status_word(), s); }),
            "gradient of the product");
-  // 3. gate and up
+  // 4. gate and up
   Grad G;
   G.g = w.dz;
   G.ld = 2 * Ip;
@@ -587,11 +632,13 @@ extern "C" mmf_status mmf_glu_backward(const mmf_tlinear* gate, const mmf_tlinea
   }
   if (want_dxh) {
     r = run_norm(norm_args(w.dxh, w.pr.plan.splits[0], M, d, *kept_x, gate->gain, x), dres, gx.dx, gx.dgain, w.colpart,
-                 dtype, s);
+                 sums, dtype, s);
     if (r != MMF_OK) return r;
   }
   if (want_db) {
-    ColSumArgs cs = {};
+    ColSumArgs& cs = sums.a[sums.n];
+    cs = ColSumArgs{};
+    sums.kind[sums.n++] = ColSum::kPlanes;
     cs.src = w.dz;
     cs.M = M;
     cs.segs = 2;
@@ -604,10 +651,9 @@ extern "C" mmf_status mmf_glu_backward(const mmf_tlinear* gate, const mmf_tlinea
       cs.inv_gamma[i] = gam[i];
       cs.out[i] = gx.dbias[i];
     }
-    cs.part = w.colpart;
-    MMF_CUDA(timed("colsum", s, [&] { return launch_colsum(cs, ColSum::kPlanes, dtype, s); }), "bias gradients");
+    cs.part = w.colpart + w.gain_floats;
   }
-  return MMF_OK;
+  return run_sums(sums, dtype, s);
 }
 
 // ------------------------------------------------------------------ LM head loss
@@ -644,6 +690,7 @@ struct HeadWs {
   uint8_t* wu;
   void *wb, *qb, *dz;
   float *dxh, *part, *colpart;
+  size_t gain_floats;
 };
 HeadWs carve_head(Carver& c, int M, int V, int K, mmf_dtype dt) {
   const int vp = std::min(piece_cols(M, V, dt), pad(V, 32));
@@ -658,7 +705,8 @@ HeadWs carve_head(Carver& c, int M, int V, int K, mmf_dtype dt) {
   tail.dx.R = tail.dw.I = last;
   w.dxh = c.take<float>(dxh_floats(w.pr));
   w.part = c.take<float>(std::max(dw_floats(w.pr), dw_floats(tail)));
-  w.colpart = c.take<float>(std::max(colsum_ws_floats(M, K), colsum_ws_floats(M, vp)));
+  w.gain_floats = colsum_ws_floats(M, K);
+  w.colpart = c.take<float>(w.gain_floats + colsum_ws_floats(M, vp));
   return w;
 }
 
@@ -695,12 +743,14 @@ extern "C" mmf_status mmf_head_loss(const mmf_tlinear* head, const void* x, mmf_
   Carver c(ws);
   const LossWs w = carve_loss(c, M, V, K);
   if ((r = quant_keep(x, dtype, M, K, head->gain, eps, *kept, s)) != MMF_OK) return r;
-  if (head->codes == nullptr)
+  // few tokens: the contraction expands the packed codes itself (rows of them on TMA's 16 bytes)
+  const bool packed = head->codes == nullptr && M < kUnpackMinTokens && K % 64 == 0;
+  if (head->codes == nullptr && !packed)
     MMF_CUDA(timed("unpack_codes", s, [&] { return launch_unpack_codes(head->packed, V, K, w.wu, s); }),
              "one-byte codes");
   const mmf_tlinear* seg[1] = {head};
   TGemmArgs a = gemm_args(seg, 1, kept->q, kept->scale, kept->qsum, M, nullptr, 0, nullptr, nullptr);
-  for (auto& u : a.wu) u = head->codes != nullptr ? head->codes : w.wu;
+  for (auto& u : a.wu) u = packed ? nullptr : head->codes != nullptr ? head->codes : w.wu;
   TrainEpi t = {};
   t.labels = labels;
   t.vocab = V;
@@ -749,10 +799,9 @@ extern "C" mmf_status mmf_head_loss_backward(const mmf_tlinear* head, const mmf_
   if ((r = check_ptrs(what, {labels, lse, ws}, {x, dloss})) != MMF_OK || (r = check_kept(kept, what)) != MMF_OK)
     return r;
   if (reduction == MMF_REDUCE_MEAN && count == nullptr) return fail(MMF_ERR_INVALID_ARG, "%s: null count", what);
-  const size_t need = mmf_head_loss_backward_ws_size(M, V, K, dtype);
-  if (ws_bytes < need) return fail(MMF_ERR_WORKSPACE, "%s: ws_bytes=%zu < %zu", what, ws_bytes, need);
   Carver c(ws);
   const HeadWs w = carve_head(c, M, V, K, dtype);
+  if (ws_bytes < c.off + 256) return fail(MMF_ERR_WORKSPACE, "%s: ws_bytes=%zu < %zu", what, ws_bytes, c.off + 256);
   const int vp = std::min(piece_cols(M, V, dtype), pad(V, 32)), rows = plane_rows_of(M, dtype);
   const bool want_dxh = grads->dx != nullptr || grads->dgain != nullptr, want_dw = grads->dw[0] != nullptr;
   const bool want_db = grads->dbias[0] != nullptr;
@@ -772,7 +821,9 @@ extern "C" mmf_status mmf_head_loss_backward(const mmf_tlinear* head, const mmf_
     pa.qK = K;
     pa.qb = w.qb;
   }
-  MMF_CUDA(timed("train_prep", s, [&] { return launch_train_prep(pa, s); }), "operands");
+  ColSumList sums;
+  sums.n = 0;
+  if ((r = run_prep(&pa, nullptr, s)) != MMF_OK) return r;
   const uint8_t* wu = head->codes != nullptr ? head->codes : w.wu;
   const mmf_tlinear* seg[1] = {head};
   for (int v0 = 0; v0 < V; v0 += vp) {
@@ -811,7 +862,9 @@ extern "C" mmf_status mmf_head_loss_backward(const mmf_tlinear* head, const mmf_
       if (r != MMF_OK) return r;
     }
     if (want_db) {
-      ColSumArgs cs = {};
+      ColSumArgs& cs = sums.a[sums.n];
+      cs = ColSumArgs{};
+      sums.kind[sums.n++] = ColSum::kPlanes;
       cs.src = w.dz;
       cs.M = M;
       cs.segs = 1;
@@ -821,11 +874,14 @@ extern "C" mmf_status mmf_head_loss_backward(const mmf_tlinear* head, const mmf_
       cs.plane_rows = rows;
       cs.scale = kept->scale;
       cs.out[0] = static_cast<char*>(grads->dbias[0]) + (size_t)v0 * elem_bytes(dtype);
-      cs.part = w.colpart;
-      MMF_CUDA(timed("colsum", s, [&] { return launch_colsum(cs, ColSum::kPlanes, dtype, s); }), "bias gradient");
+      cs.part = w.colpart + w.gain_floats;
+      if (v0 + vp < V && (r = run_sums(sums, dtype, s)) != MMF_OK) return r;   // the next piece takes its place
     }
   }
-  if (!want_dxh) return MMF_OK;
-  return run_norm(norm_args(w.dxh, w.pr.plan.splits[0], M, K, *kept, head->gain, x), nullptr, grads->dx, grads->dgain, w.colpart, dtype,
-                  s);
+  if (want_dxh) {
+    r = run_norm(norm_args(w.dxh, w.pr.plan.splits[0], M, K, *kept, head->gain, x), nullptr, grads->dx, grads->dgain,
+                 w.colpart, sums, dtype, s);
+    if (r != MMF_OK) return r;
+  }
+  return run_sums(sums, dtype, s);
 }

@@ -48,10 +48,10 @@ class Act8:
         self._m, self._k = q.shape
 
     @classmethod
-    def _new(cls, m: int, k: int, device: torch.device) -> "Act8":
+    def _new(cls, m: int, k: int, device: torch.device, extra: int = 0) -> "Act8":
         me = cls.__new__(cls)
         me._parts, me._m, me._k = None, m, k
-        me._buf = torch.empty(_pad16(m * k) + 3 * _pad16(4 * m), dtype=torch.int8, device=device)
+        me._buf = torch.empty(_pad16(m * k) + 3 * _pad16(4 * m) + extra, dtype=torch.int8, device=device)
         return me
 
     def _tensors(self):
@@ -80,12 +80,29 @@ class Act8:
         return L.Act8(*[t.data_ptr() for t in self._parts])
 
 
-class HeadKept(NamedTuple):
-    """What head_loss keeps: the codes of its input, lse [M], the number of counted tokens [1], its input's dtype."""
-    act: Act8
-    lse: torch.Tensor
-    count: torch.Tensor
-    dtype: torch.dtype
+class HeadKept:
+    """What head_loss keeps: act (Act8 of its input), lse [M] and count [1] (the counted tokens, at least 1;
+    not written for reduction "none"), and its input's dtype."""
+
+    __slots__ = ("act", "dtype", "_tail")
+
+    def __init__(self, m: int, k: int, dtype: torch.dtype, device: torch.device):
+        self.act = Act8._new(m, k, device, _pad16(4 * m) + 16)
+        self.dtype = dtype
+        self._tail = _pad16(m * k) + 3 * _pad16(4 * m)   # lse, then count, behind the codes
+
+    def _ptrs(self):
+        p = self.act._buf.data_ptr() + self._tail
+        return p, p + _pad16(4 * self.act._m)
+
+    @property
+    def lse(self) -> torch.Tensor:
+        return self.act._buf[self._tail: self._tail + 4 * self.act._m].view(torch.float32)
+
+    @property
+    def count(self) -> torch.Tensor:
+        at = self._tail + _pad16(4 * self.act._m)
+        return self.act._buf[at: at + 4].view(torch.float32)
 
 
 class LinearGrads(NamedTuple):
@@ -174,6 +191,8 @@ def _like(t: Optional[torch.Tensor], numel: int, dtype: torch.dtype, what: str) 
 
 def _scratch(nbytes: int, device: torch.device, ws: Optional[torch.Tensor]):
     """(address, bytes, tensor) of the caller's workspace, or of a new one."""
+    if nbytes == 0:
+        return None, 0, None
     if ws is None:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         return ws.data_ptr(), nbytes, ws
@@ -200,7 +219,7 @@ def bitlinear_train(lins: Union[TLinear, Sequence[TLinear]], x: torch.Tensor, ep
     y = torch.empty(x.shape[:-1] + ((N,) if isinstance(lins, TLinear) else (n, N)), dtype=dt, device=dev)
     kept = Act8._new(m, K, dev)
     lib = L.load()
-    wp, wn, _keep = _scratch(lib.mmf_bitlinear_train_ws_size(n, N, K), dev, ws)
+    wp, wn, _keep = _scratch(lib.mmf_bitlinear_train_ws_size(n, N, K, m), dev, ws)
     with _on(idx):
         L.check(lib.mmf_bitlinear_train(_c_layers(ls), n, x.data_ptr(), code, m, y.data_ptr(), eps,
                                         _byref(kept._c(m, K, idx)), wp, wn, _stream(idx)), "mmf_bitlinear_train")
@@ -317,14 +336,14 @@ def head_loss(head: TLinear, x: torch.Tensor, labels: torch.Tensor, ignore_index
     red = _head_args(labels, m, reduction)
     code = _code(x.dtype)
     loss = torch.empty(labels.shape if red == 0 else (), dtype=torch.float32, device=dev)
-    kept = HeadKept(Act8._new(m, K, dev), torch.empty(m, dtype=torch.float32, device=dev),
-                    torch.empty(1, dtype=torch.float32, device=dev), x.dtype)
+    kept = HeadKept(m, K, x.dtype, dev)
+    lse, count = kept._ptrs()
     lib = L.load()
     wp, wn, _keep = _scratch(lib.mmf_head_loss_ws_size(m, N, K), dev, ws)
     with _on(idx):
         L.check(lib.mmf_head_loss(_byref(head.c()), x.data_ptr(), code, m, labels.data_ptr(), ignore_index, red, eps,
-                                  loss.data_ptr(), _byref(kept.act._c(m, K, idx)), kept.lse.data_ptr(),
-                                  kept.count.data_ptr(), wp, wn, _stream(idx)), "mmf_head_loss")
+                                  loss.data_ptr(), _byref(kept.act._c(m, K, idx)), lse, count, wp, wn, _stream(idx)),
+                "mmf_head_loss")
     return loss, kept
 
 
@@ -335,25 +354,23 @@ def head_loss_backward(head: TLinear, kept: HeadKept, labels: torch.Tensor, dlos
     of the forward's input (mmf_head_loss_backward); labels, ignore_index and reduction as there, x as in
     bitlinear_backward."""
     idx, dev, dt = labels.get_device(), labels.device, kept.dtype
-    _check(idx, labels, dloss, x, kept.lse, kept.count)
+    _check(idx, labels, dloss, x)
     _on_device((head,), idx)
     m, N, K = labels.numel(), head.N, head.K
     red = _head_args(labels, m, reduction)
     code = _code(dt)
     if dloss is not None and (dloss.dtype != torch.float32 or dloss.numel() != (m if red == 0 else 1)):
         raise ValueError("dloss must be float32, one value (one per token for reduction 'none')")
-    if kept.lse.numel() != m:
-        raise ValueError("kept must come from head_loss on the same tokens")
     _like(x, m * K, dt, "x")
     dx = torch.empty(labels.shape + (K,), dtype=dt, device=dev)
     dw = torch.empty((N, K), dtype=dt, device=dev)
     dgain = None if head.gain is None else torch.empty(K, dtype=dt, device=dev)
     dbias = None if head.bias is None else torch.empty(N, dtype=dt, device=dev)
     cg = L.LinearGrads(dx.data_ptr(), _P3(dw.data_ptr()), _p(dgain), _P3(_p(dbias)))
+    lse, count = kept._ptrs()
     lib = L.load()
     wp, wn, _keep = _scratch(lib.mmf_head_loss_backward_ws_size(m, N, K, code), dev, ws)
     with _on(idx):
         L.check(lib.mmf_head_loss_backward(_byref(head.c()), _byref(kept.act._c(m, K, idx)), _p(x), labels.data_ptr(),
-                                           kept.lse.data_ptr(), kept.count.data_ptr(), _p(dloss), ignore_index, red,
-                                           code, m, _byref(cg), wp, wn, _stream(idx)), "mmf_head_loss_backward")
+                                           lse, count, _p(dloss), ignore_index, red, code, m, _byref(cg), wp, wn, _stream(idx)), "mmf_head_loss_backward")
     return LinearGrads(dx, [dw], dgain, [dbias])
