@@ -31,10 +31,18 @@
 // kernel that reads the result to add up in order (no atomics, same result
 // each run).
 //
+// Even shares: tiles rarely fill the last round (160 tiles on 74 pairs are 2.16
+// rounds of work in 3 rounds of time). With `even` the whole rounds go as
+// before and the tiles left over are cut so that every group gets the same
+// share of their reduction, in order: a group ends one tile and begins the
+// next. Parts of tiles go to fp32 slots (two per group), which a second kernel
+// adds in order of the reduction. 4096 x 2560 x 13824, gradient of the input:
+// 225 -> 185 us.
+//
 // One launch can run both products of a backward, dx's tiles before dw's: small
 // ones share the SMs, one start-up and one launch.
 //
-// Chained products: the reduction is cut in units (8 k-steps of one segment; 4 for fp32
+// Chained products: the reduction is cut in units (32 k-steps of one segment; 4 for fp32
 // planes) whose sums leave tensor memory one by one and are added in registers,
 // each times its segment's gamma. For several layers of one input that is the
 // sum over layers in one launch; for fp32 it bounds the error: the tensor
@@ -52,7 +60,7 @@ constexpr int A_BYTES = BM * BK * 2, BOX_BYTES = 64 * 64 * 2;
 constexpr int kEpiWarps = 8, kEpiWarp0 = 2;
 constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kChainF32 = 4, kChainBf16 = 8;   // k-steps per unit
+constexpr int kChainF32 = 4, kChainBf16 = 32;   // k-steps per unit
 
 template <int CTAS>
 struct __align__(1024) Smem {
@@ -194,7 +202,7 @@ __device__ __noinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volati
 
 // What the kernel reads of a product (BGemmArgs without its operands).
 struct ProbArgs {
-  int a_plane, planes, I, J, R, splits, slice_rows, seg_pitch;
+  int a_plane, planes, I, J, R, splits, slice_rows, seg_pitch, seg_rows;
   bool out_f32, accumulate;
   const void* out[3];
   const float *gamma[3], *inv_gamma[3], *row_scale;
@@ -209,13 +217,20 @@ struct Prob {
 };
 struct KArgs {
   Prob pr[2];               // dx, dw
-  int tiles0, tiles;        // dx's tiles; all tiles
+  int tiles0, tiles;        // dx's tiles; all tiles that go whole
+  int shared;               // even shares (one product): tiles after those, cut among all groups
   int* status;
   long long wait_cycles;
 };
 struct Maps {
   CUtensorMap a[2], b[2], o[4];   // outputs: dx, then dw's segments
+  CUtensorMap slots;              // even shares: fp32 [2 groups][tile rows][256]
 };
+
+// Group c's share of `total` units in `groups` equal parts.
+__host__ __device__ __forceinline__ long long share_begin(long long total, int groups, int c) {
+  return total * c / groups;
+}
 
 // KIND 0: nothing chained; 1: dx chained (several layers); 2: both (fp32 planes).
 // MODE 0: dx alone, 1: dw alone, 2: both.
@@ -273,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   struct Place {
     bool dw, chain;
     int sp, it, jt, lo, hi;
+    int slot;   // part of a tile: where its sums go (-1: a whole tile)
   };
   auto place = [&](int tile) {
     Place t;
@@ -285,7 +301,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     t.lo = (int)((long long)q.units * t.sp / q.g.splits);
     t.hi = (int)((long long)q.units * (t.sp + 1) / q.g.splits);
     t.chain = KIND == 2 || (KIND == 1 && !t.dw);
+    t.slot = -1;
     return t;
+  };
+  // This group's work in order: whole tiles, then its share of the others.
+  struct Walk {
+    int tile;
+    long long u, end;
+  };
+  auto begin = [&]() {
+    Walk w;
+    w.tile = first;
+    w.u = w.end = 0;
+    if (MODE < 2 && p.shared > 0) {
+      const long long total = (long long)p.shared * p.pr[MODE == 1].units;
+      w.u = share_begin(total, stride, first);
+      w.end = share_begin(total, stride, first + 1);
+    }
+    return w;
+  };
+  auto next = [&](Walk& w, Place& t) {
+    if (w.tile < p.tiles) {
+      t = place(w.tile);
+      w.tile += stride;
+      return true;
+    }
+    if (MODE == 2 || w.u >= w.end) return false;
+    const int units = p.pr[MODE == 1].units, k = (int)(w.u / units);
+    t = place(p.tiles + k);   // splits is 1: sp = 0
+    t.lo = (int)(w.u - (long long)k * units);
+    t.hi = (int)min((long long)units, t.lo + (w.end - w.u));
+    t.slot = t.lo == 0 && t.hi == units ? -1 : 2 * first + (t.lo == 0 ? 1 : 0);
+    w.u += t.hi - t.lo;
+    return true;
   };
   // MMA columns of a tile: a multiple of 16, for a pair of 32 (each CTA holds half
   // of B), of 128 where B comes in blocks
@@ -304,8 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ph = 1, n = 0;
       bool ok = true;
       const uint32_t bar0 = CTAS == 2 ? leader_addr(&sm.full[0]) : smem_u32(&sm.full[0]);
-      for (int tile = first; tile < p.tiles && ok; tile += stride) {
-        const Place t = place(tile);
+      Place t;
+      for (Walk w = begin(); ok && next(w, t);) {
         const Prob& q = p.pr[t.dw];
         const CUtensorMap *ma = &maps.a[t.dw], *mb = &maps.b[t.dw];
         const int half = cols_of(q, t.jt) / CTAS;
@@ -367,8 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0;
       uint32_t ph = 0, na = 0;   // ring phase; accumulators begun
       bool ok = true;
-      for (int tile = first; tile < p.tiles && ok; tile += stride) {
-        const Place t = place(tile);
+      Place t;
+      for (Walk w = begin(); ok && next(w, t);) {
         const Prob& q = p.pr[t.dw];
         const uint32_t idesc = idesc_bf16(BM * CTAS, cols_of(q, t.jt), t.dw, true);
         // 16 reduction steps: 2 row groups (MN-major) or 32 bytes (K-major)
@@ -446,8 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++na;
     };
-    for (int tile = first; tile < p.tiles; tile += stride) {
-      const Place t = place(tile);
+    Place t;
+    for (Walk walk = begin(); next(walk, t);) {
       const Prob& q = p.pr[t.dw];
       const int i0 = (t.it * CTAS + rank) * BM + quarter * 32;   // this warp's 32 rows of the result
       const int i = i0 + lane;
@@ -467,7 +515,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (q.g.row_scale != nullptr && i < q.g.I) sc *= q.g.row_scale[i];
       }
       const CUtensorMap* mo = &maps.o[t.dw ? 1 + (rows_ok ? seg : 0) : 0];
-      const bool f32 = MODE == 0 ? true : q.g.out_f32;
+      const bool part = MODE < 2 && t.slot >= 0;
+      const bool f32 = MODE == 0 || part ? true : q.g.out_f32;
+      const bool add = q.g.accumulate && !part;
+      if (part) {   // rows of a slot, scaled as the result would be
+        mo = &maps.slots;
+        y = (t.slot * CTAS + rank) * BM + quarter * 32;
+      }
+      const int jo = part ? t.jt * BN : 0;   // a slot's columns count from the tile's
       const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
       const int jg = t.jt * BN + group * 128;                    // this warp's first column
 
@@ -491,8 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (f32 && q.g.accumulate) tma_add_2d(mo, buf, j0, y);
-          else tma_store_2d(mo, buf, j0, y);
+          if (f32 && add) tma_add_2d(mo, buf, j0 - jo, y);
+          else tma_store_2d(mo, buf, j0 - jo, y);
         }
         last_bf16 = !f32;
         ++nst;
@@ -528,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 4; ++c)
           if (rows_ok && jg + 32 * c < q.g.J) put(acc[c], jg + 32 * c);
       } else if (KIND < 2) {
-        const bool dots = MODE == 0 && KIND == 0 && q.g.dot_q != nullptr;
+        const bool dots = MODE == 0 && KIND == 0 && q.g.dot_q != nullptr && !part;
         uint4 codes[8];   // this row's codes under the tile's columns, fetched ahead of the accumulator
         if (dots) {
 #pragma unroll
@@ -592,6 +647,86 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Even shares: adds up the parts of each tile that was cut, in order of the
+// reduction, into the result. A block has 4 rows x 256 columns, a thread 4
+// columns. With codes it also leaves the rows' partial dots that whole tiles
+// left in the epilogue.
+struct ShareArgs {
+  ProbArgs g;
+  int i_tiles, j_tiles, units, tile0, tiles, groups, tile_rows;
+  const float* slots;
+};
+
+template <typename OUT>
+__global__ void __launch_bounds__(256) share_join_kernel(const __grid_constant__ ShareArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const long long total = (long long)a.tiles * a.units, t0 = (long long)blockIdx.x * a.units, t1 = t0 + a.units;
+  // the groups whose shares meet this tile
+  int c0 = (int)(t0 * a.groups / total);
+  while (share_begin(total, a.groups, c0 + 1) <= t0) ++c0;
+  if (share_begin(total, a.groups, c0) <= t0 && share_begin(total, a.groups, c0 + 1) >= t1) return;   // whole
+  const int tile = a.tile0 + blockIdx.x, jt = tile % a.j_tiles, it = tile / a.j_tiles;
+  const int row = threadIdx.x / 64 + 4 * blockIdx.y, i = it * a.tile_rows + row;
+  if (i >= a.g.I) return;
+  void* out = nullptr;
+  size_t at = 0;
+  if (a.g.seg_pitch > 0) {
+    const int seg = i / a.g.seg_pitch, n = i - seg * a.g.seg_pitch;
+    if (seg >= 3 || n >= a.g.seg_rows) return;
+    out = const_cast<void*>(a.g.out[seg]);
+    at = (size_t)n * a.g.J;
+  } else {
+    out = const_cast<void*>(a.g.out[0]);
+    at = (size_t)i * a.g.J;
+  }
+  if (out == nullptr) return;
+  const int jl = threadIdx.x % 64 * 4, j = jt * BN + jl;   // J is a multiple of 16
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float dot = 0.0f;
+  if (j < a.g.J) {
+    for (int c = c0; c < a.groups; ++c) {
+      const long long lo = share_begin(total, a.groups, c);
+      if (lo >= t1) break;
+      if (share_begin(total, a.groups, c + 1) <= max(lo, t0)) continue;   // an empty share
+      const int slot = 2 * c + (lo <= t0 ? 1 : 0);   // began the tile, or went on with it
+      const float4 w = *reinterpret_cast<const float4*>(a.slots + ((size_t)slot * a.tile_rows + row) * BN + jl);
+      v[0] += w.x;
+      v[1] += w.y;
+      v[2] += w.z;
+      v[3] += w.w;
+    }
+    if (a.g.dot_q != nullptr) {
+      const int w = *reinterpret_cast<const int*>(a.g.dot_q + at + j);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dot = fmaf(v[e], (float)((w << (24 - 8 * e)) >> 24), dot);
+    }
+    OUT* o = static_cast<OUT*>(out) + at + j;
+    if constexpr (sizeof(OUT) == 4) {
+      if (a.g.accumulate) {
+        const float4 w = *reinterpret_cast<const float4*>(o);
+        v[0] += w.x;
+        v[1] += w.y;
+        v[2] += w.z;
+        v[3] += w.w;
+      }
+      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]), y = __floats2bfloat162_rn(v[2], v[3]);
+      uint2 u;
+      u.x = *reinterpret_cast<uint32_t*>(&x);
+      u.y = *reinterpret_cast<uint32_t*>(&y);
+      *reinterpret_cast<uint2*>(o) = u;
+    }
+  }
+  if (a.g.dot_q != nullptr) {   // a warp has 128 columns of one row
+    const int h = threadIdx.x % 64 / 32;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (threadIdx.x % 32 == 0 && jt * BN + 128 * h < a.g.J) a.g.dot_part[(size_t)(2 * jt + h) * a.g.I + i] = dot;
+  }
+}
+
 template <int KIND, int CTAS, int MODE>
 cudaError_t launch_form(const Maps& m, const KArgs& p, cudaStream_t stream) {
   auto kern = bgemm_tc_kernel<KIND, CTAS, MODE>;
@@ -600,7 +735,7 @@ cudaError_t launch_form(const Maps& m, const KArgs& p, cudaStream_t stream) {
   static SmemOptIn opt;
   const cudaError_t e = opt.set(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const int groups = std::min(p.tiles, num_sms() / CTAS);
+  const int groups = p.shared > 0 ? num_sms() / CTAS : std::min(p.tiles, num_sms() / CTAS);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(groups * CTAS);
   cfg.blockDim = dim3(kThreads);
@@ -691,7 +826,7 @@ BGemmPlan bgemm_plan(const BGemmShape& dx, const BGemmShape& dw) {
     }
   }
   if (best_t < 1e30) return best;
-  best.together = false;
+  best = {};
   const BGemmShape* sh[2] = {&dx, &dw};
   for (int i = 0; i < 2; ++i) {
     best_t = 1e30;
@@ -705,12 +840,29 @@ BGemmPlan bgemm_plan(const BGemmShape& dx, const BGemmShape& dw) {
           best_t = t;
           best.pair[i] = pair != 0;
           best.splits[i] = s;
+          best.even[i] = false;
         }
+      }
+      // even shares of the last round: their parts are written and read once more, and
+      // groups at different places of the reduction share fewer operands in L2
+      // (1024 x 2816 x 16384, 44 tiles: 94 us, in 3 splits 88 us)
+      const long long left = n % m.groups;
+      const double parts_us = 12.0 + (double)(m.groups + left) * (pair ? 2 : 1) * BM * BN * 8 / 4e6;
+      const double t = (double)(n / m.groups) * m.tile_time(*sh[i], 1) +
+                       (m.tile_time(*sh[i], 1) - m.tile_us) * left / m.groups + 2 * m.tile_us + parts_us;
+      if (left > 0 && t < best_t && left * bgemm_units(*sh[i]) >= 8 * m.groups) {
+        best_t = t;
+        best.pair[i] = pair != 0;
+        best.splits[i] = 1;
+        best.even[i] = true;
       }
     }
   }
   return best;
 }
+
+// Two slots per group: the same size for pairs and for single SMs.
+size_t bgemm_slot_floats() { return (size_t)2 * num_sms() * BM * BN; }
 
 int bgemm_slice_rows(int I) { return ceil_div(I, 32) * 32; }
 
@@ -760,6 +912,7 @@ cudaError_t launch_bgemm_tc(const BGemmArgs* dx, const BGemmArgs* dw, bool pair,
     q.g.out_f32 = g.out_f32;
     q.g.accumulate = g.accumulate;
     q.g.seg_pitch = g.seg_pitch;
+    q.g.seg_rows = g.seg_rows;
     for (int i = 0; i < 3; ++i) {
       q.g.out[i] = g.out[i];
       q.g.gamma[i] = g.gamma[i];
@@ -784,19 +937,39 @@ cudaError_t launch_bgemm_tc(const BGemmArgs* dx, const BGemmArgs* dw, bool pair,
   p.status = status;
   p.wait_cycles = wait_limit_cycles();
   const int kind = chain[1] ? 2 : chain[0] ? (args[0]->sh.planes > 1 ? 2 : 1) : 0;
+  const int groups = num_sms() / (pair ? 2 : 1), one = tiles[0] > 0 ? 0 : 1;
+  const float* slots = args[one] != nullptr ? args[one]->slots : nullptr;
+  if (slots != nullptr && (tiles[0] == 0 || tiles[1] == 0) && args[one]->splits == 1) {
+    p.shared = p.tiles % groups;
+    p.tiles -= p.shared;
+    if (p.shared > 0 && !make_tma_2d(&m.slots, slots, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, BN,
+                                     (uint64_t)2 * groups * BM * (pair ? 2 : 1), 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
   const int mode = tiles[1] == 0 ? 0 : tiles[0] == 0 ? 1 : 2;
-  if (pair) {
-    switch (kind) {
-      case 0: return launch_mode<0, 2>(mode, m, p, stream);
-      case 1: return launch_mode<1, 2>(mode, m, p, stream);
-      default: return launch_mode<2, 2>(mode, m, p, stream);
-    }
-  }
-  switch (kind) {
-    case 0: return launch_mode<0, 1>(mode, m, p, stream);
-    case 1: return launch_mode<1, 1>(mode, m, p, stream);
-    default: return launch_mode<2, 1>(mode, m, p, stream);
-  }
+  cudaError_t e;
+  if (pair)
+    e = kind == 0 ? launch_mode<0, 2>(mode, m, p, stream)
+                  : kind == 1 ? launch_mode<1, 2>(mode, m, p, stream) : launch_mode<2, 2>(mode, m, p, stream);
+  else
+    e = kind == 0 ? launch_mode<0, 1>(mode, m, p, stream)
+                  : kind == 1 ? launch_mode<1, 1>(mode, m, p, stream) : launch_mode<2, 1>(mode, m, p, stream);
+  if (e != cudaSuccess || p.shared == 0) return e;
+  const Prob& q = p.pr[one];
+  ShareArgs a;
+  a.g = q.g;
+  if (one == 0) a.g.seg_pitch = 0;
+  a.i_tiles = q.i_tiles;
+  a.j_tiles = q.j_tiles;
+  a.units = q.units;
+  a.tile0 = p.tiles;
+  a.tiles = p.shared;
+  a.groups = groups;
+  a.tile_rows = BM * (pair ? 2 : 1);
+  a.slots = slots;
+  const dim3 grid(p.shared, a.tile_rows / 4), block(256);
+  return q.g.out_f32 ? launch_pdl(share_join_kernel<float>, grid, block, 0, stream, a)
+                     : launch_pdl(share_join_kernel<bf16>, grid, block, 0, stream, a);
 }
 
 }  // namespace mmf

@@ -186,6 +186,7 @@ struct BGemmArgs {
   const float* gamma[3];    // dx: device scalars or null
   const float* row_scale;   // dx: [I] or null
   const float* inv_gamma[3];  // dw, splits 1: device scalars or null
+  float* slots;             // even shares of the last round: bgemm_slot_floats() of scratch, or null; splits 1
   const int8_t* dot_q;      // dx of one segment and plane, splits 1: codes [I, J], or null; then
   float* dot_part;          //   dot_part[2 jt + h][i] = sum over columns 256 jt + 128 h .. of D[i, j] dot_q[i, j]
 };
@@ -193,10 +194,12 @@ struct BGemmPlan {
   bool together;            // one launch for both
   bool pair[2];             // tiles of two SMs: dx, dw
   int splits[2];
+  bool even[2];             // the last round's tiles in even shares (BGemmArgs::slots)
 };
 BGemmPlan bgemm_plan(const BGemmShape& dx, const BGemmShape& dw);
 int bgemm_units(const BGemmShape& s);   // the most splits there can be
 int bgemm_slice_rows(int I);
+size_t bgemm_slot_floats();
 // Either product, or both in one launch (null: left out).
 cudaError_t launch_bgemm_tc(const BGemmArgs* dx, const BGemmArgs* dw, bool pair, int* status, cudaStream_t stream);
 

@@ -396,23 +396,41 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
     bool alive = true;
     uint32_t res_pending = 0;                     // RB: this tile's residual boxes not yet waited on
     // GLU backward: this warp's box of dx^ (map_res) and of p's codes (map_b2) for
-    // 16-column chunk cc (0, 1) of its 32 columns of a tile.
-    auto load_chunk = [&](int tile, int cc) {
-      const int n0 = tile % p.n_tiles * HALF + 32 * group + 16 * cc, y = tile / p.n_tiles * BM + quarter * 32;
-      mbar_arrive_expect_tx(&sm.res_full[ew][0], 2048 + 512);
-      tma_load_2d(sm.gx[ew], &map_res, n0, y, &sm.res_full[ew][0]);
-      tma_load_2d(sm.gq[ew], &map_b2, n0, y, &sm.res_full[ew][0]);
+    // the next of its 16-column chunks, walked ahead of the accumulators (pt:
+    // tile, pm and pn: its row and column tile, pc: chunk 0 or 1 of 32 columns).
+    const bool glu_back = EPI == Epi::kGluBwd;
+    int pt = glu_back ? (int)blockIdx.x : 0, pm = 0, pn = 0, pc = 0;
+    uint32_t nload = 0;                           // chunks begun by this warp
+    const int step_m = glu_back ? (int)gridDim.x / p.n_tiles : 0, step_n = glu_back ? (int)gridDim.x % p.n_tiles : 0;
+    auto next_tile = [&]() {   // the next tile in which this warp has columns
+      do {
+        pt += gridDim.x;
+        pm += step_m;
+        pn += step_n;
+        if (pn >= p.n_tiles) {
+          pn -= p.n_tiles;
+          ++pm;
+        }
+      } while (pt < n_tiles_total && pn * HALF + 32 * group >= p.t.plane_cols);
     };
-    // The first tile from `tile` on in which this warp has columns.
-    auto next_tile = [&](int tile) {
-      while (tile < n_tiles_total && tile % p.n_tiles * HALF + 32 * group >= p.t.plane_cols) tile += gridDim.x;
-      return tile;
+    auto load_chunk = [&]() {
+      if (pt >= n_tiles_total) return;
+      if (lane == 0) {
+        const int n0 = pn * HALF + 32 * group + 16 * pc, y = pm * BM + quarter * 32;
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(&sm.res_full[ew][0], 2048 + 512);
+        tma_load_2d(sm.gx[ew], &map_res, n0, y, &sm.res_full[ew][0]);
+        tma_load_2d(sm.gq[ew], &map_b2, n0, y, &sm.res_full[ew][0]);
+      }
+      ++nload;
+      pc ^= 1;
+      if (pc == 0) next_tile();
     };
-    uint32_t nload = 0;
     if constexpr (EPI == Epi::kGluBwd) {
-      const int t0 = next_tile(blockIdx.x);
-      if (lane == 0 && t0 < n_tiles_total) load_chunk(t0, 0);
-      nload = t0 < n_tiles_total;                 // chunks begun by this warp
+      pm = pt / p.n_tiles;
+      pn = pt % p.n_tiles;
+      if (pn * HALF + 32 * group >= p.t.plane_cols) next_tile();
+      load_chunk();
     }
     for (int tile = blockIdx.x; tile < n_tiles_total && alive; tile += gridDim.x, ++tl) {
       const int mt = tile / p.n_tiles, nt = tile % p.n_tiles;
@@ -570,25 +588,25 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
 #pragma unroll
             for (int b = 0; b < 4; ++b) {              // 2^23 + byte, less 2^23 + 128
               const float qf = __uint_as_float(__byte_perm(u4, 0x4B000000u, 0x7650 + b)) - 8388736.0f;
-              if (p.t.gain_p == nullptr) {
-                dp[4 * e + b] = fmaf(kq, qf, k1 * d[b]);
-              } else {                                 // n = xt / gain
+              dp[4 * e + b] = fmaf(kq, qf, k1 * d[b]);
+            }
+          }
+          if (p.t.gain_p != nullptr) {                 // n = xt / gain
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 d4 = *reinterpret_cast<const float4*>(sm.gx[ew] + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4));
+              const float* d = &d4.x;
+              const uint32_t u4 = qw[e] ^ 0x80808080u;
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                const float qf = __uint_as_float(__byte_perm(u4, 0x4B000000u, 0x7650 + b)) - 8388736.0f;
                 const float gn = n0 + 4 * e + b < p.g.N ? __ldg(p.t.gain_p + n0 + 4 * e + b) : 1.0f;
                 dp[4 * e + b] = k1 * gn * d[b] + (gn != 0.0f ? kq * qf / gn : 0.0f);
               }
             }
           }
           __syncwarp();
-          {   // this warp's next chunk into the buffers just read
-            const int tn = cc == 0 ? tile : next_tile(tile + gridDim.x);
-            if (tn < n_tiles_total) {
-              ++nload;
-              if (lane == 0) {
-                fence_proxy_async_smem();
-                load_chunk(tn, cc ^ 1);
-              }
-            }
-          }
+          load_chunk();   // this warp's next chunk into the buffers just read
           tmem_wait(ru);
           tmem_wait(rv);
           float du[16], dv[16];

@@ -99,8 +99,11 @@ Products products(int M, int K, int nseg, int cols, int dw_cols, mmf_dtype dt) {
   return p;
 }
 size_t dxh_floats(const Products& p) { return (size_t)p.plan.splits[0] * bgemm_slice_rows(p.dx.I) * p.dx.J; }
-size_t dw_floats(const Products& p) {
-  return p.plan.splits[1] > 1 ? (size_t)p.plan.splits[1] * bgemm_slice_rows(p.dw.I) * p.dw.J : 0;
+// Scratch of either product: dW's slices, or the slots of even shares (the
+// products follow one another, so they share it).
+size_t part_floats(const Products& p) {
+  const size_t slices = p.plan.splits[1] > 1 ? (size_t)p.plan.splits[1] * bgemm_slice_rows(p.dw.I) * p.dw.J : 0;
+  return std::max(slices, p.plan.even[0] || p.plan.even[1] ? bgemm_slot_floats() : 0);
 }
 
 // dx^ (+)= sum over segments of gamma[g] G_g W_g into dxh (null: not wanted);
@@ -127,6 +130,8 @@ mmf_status run_products(const Products& pr, const Grad& G, const void* wb, const
   x.accumulate = accumulate;
   for (int i = 0; gamma != nullptr && i < pr.dx.nseg; ++i) x.gamma[i] = gamma[i];
   x.row_scale = G.over_s ? scale : nullptr;
+  x.slots = pr.plan.even[0] ? part : nullptr;
+  w.slots = pr.plan.even[1] ? part : nullptr;
   x.dot_q = dot_q;
   x.dot_part = dot_part;
   w.splits = pr.plan.splits[1];
@@ -254,7 +259,7 @@ LinearWs carve_linear(Carver& c, int nlin, int N, int K, int M, mmf_dtype dt, bo
   w.gb = c.take<char>(p.copy ? (size_t)p.planes * p.rows * p.cols * 2 : 0);
   w.pr = products(M, K, nlin, p.pitch, nlin == 1 ? N : p.cols, dt);
   w.dxh = c.take<float>(dxh_floats(w.pr));
-  w.part = c.take<float>(dw_floats(w.pr));
+  w.part = c.take<float>(part_floats(w.pr));
   w.gain_floats = colsum_ws_floats(M, K);
   w.colpart = c.take<float>(w.gain_floats + colsum_ws_floats(M, nlin * N));
   w.dots = c.take<float>(dots ? (size_t)2 * ceil_div(K, 256) * M : 0);
@@ -483,15 +488,22 @@ extern "C" mmf_status mmf_glu_train(const mmf_tlinear* gate, const mmf_tlinear* 
   TGemmArgs a = gemm_args(gu, 2, kept_x->q, kept_x->scale, kept_x->qsum, M, p, I, nullptr, nullptr);
   TGemmArgs b = gemm_args(dn, 1, kept_p->q, kept_p->scale, kept_p->qsum, M, y, d, residual, nullptr);
   if (M >= kUnpackMinTokens) {
+    PrepArgs pa = {}, pd = {};   // gate and up; down
+    pa.dy_dt = pd.dy_dt = dtype;
+    pa.nseg = 2;
+    pa.N = pa.w_pitch = pd.K = I;
+    pa.K = pd.N = pd.w_pitch = d;
+    pd.nseg = 1;
     const mmf_tlinear* l[3] = {gate, up, down};
     const uint8_t* wu[3];
     for (int i = 0; i < 3; ++i) {
       uint8_t* u = c.take<uint8_t>((size_t)d * I);
       wu[i] = l[i]->codes != nullptr ? l[i]->codes : u;
-      if (l[i]->codes == nullptr)
-        MMF_CUDA(timed("unpack_codes", s, [&] { return launch_unpack_codes(l[i]->packed, l[i]->N, l[i]->K, u, s); }),
-                 "one-byte codes");
+      PrepArgs& p = i < 2 ? pa : pd;
+      p.w[i < 2 ? i : 0] = l[i]->packed;
+      p.wu[i < 2 ? i : 0] = l[i]->codes == nullptr ? u : nullptr;
     }
+    if ((r = run_prep(&pa, &pd, s)) != MMF_OK) return r;
     a.wu[0] = wu[0];
     a.wu[1] = wu[1];
     b.wu[0] = wu[2];
@@ -525,7 +537,7 @@ GluWs carve_glu(Carver& c, int M, int d, int I, mmf_dtype dt) {
   w.cmean = c.take<float>(M);
   w.pr = products(M, d, 1, 2 * Ip, 2 * Ip, dt);
   w.dxh = c.take<float>(dxh_floats(w.pr));
-  w.part = c.take<float>(dw_floats(w.pr));
+  w.part = c.take<float>(part_floats(w.pr));
   w.gain_floats = colsum_ws_floats(M, d);
   w.colpart = c.take<float>(w.gain_floats + colsum_ws_floats(M, 2 * Ip));
   return w;
@@ -704,7 +716,7 @@ HeadWs carve_head(Carver& c, int M, int V, int K, mmf_dtype dt) {
   Products tail = w.pr;   // the last piece keeps the plan
   tail.dx.R = tail.dw.I = last;
   w.dxh = c.take<float>(dxh_floats(w.pr));
-  w.part = c.take<float>(std::max(dw_floats(w.pr), dw_floats(tail)));
+  w.part = c.take<float>(std::max(part_floats(w.pr), part_floats(tail)));
   w.gain_floats = colsum_ws_floats(M, K);
   w.colpart = c.take<float>(w.gain_floats + colsum_ws_floats(M, vp));
   return w;
