@@ -809,7 +809,8 @@ BGemmPlan bgemm_plan(const BGemmShape& dx, const BGemmShape& dw) {
   for (int pair = 0; pair < 2; ++pair) {
     const Model m(pair != 0);
     const long long n0 = m.tiles(dx), n1 = m.tiles(dw);
-    if (n0 + n1 > m.groups) continue;
+    // one round either way: single SMs start quicker and split the rows finer
+    if (n0 + n1 > m.groups || best_t < 1e30) continue;
     for (int s0 : kTry) {
       if (n0 * s0 + n1 > m.groups || !may_split(dx, s0)) break;
       for (int s1 : kTry) {

@@ -89,11 +89,12 @@ enum class Epi : int {
   kLse = 4,       // per token and 128 columns: max and sum of exp of the logits; the label's logit
   kDz = 5,        // gradient of the loss by the logits, over the token's scale, as bf16 planes
   kGluBwd = 6,    // 2 segments gate,up: gradients of u and v, over the token's scale, as bf16 planes
+  kStoreAny = 7,  // kStore of one segment into rows of any pitch
 };
 
-// What the training epilogues read and write besides TGemmArgs. "Planes": one
-// bf16 plane for bf16 runs, three (g0 + g1 + g2, 24 bits) for fp32 runs, each
-// plane_rows rows tall.
+// What the training epilogues read and write besides TGemmArgs. Planes: a
+// gradient as the sum of 1 to 3 bf16 planes (8, 16, 24 bits), each plane_rows
+// rows tall.
 struct TrainEpi {
   const int32_t* labels;    // kLse, kDz: [M]
   int col0, vocab;          // kLse, kDz: vocabulary index of column 0; vocabulary size
@@ -108,7 +109,7 @@ struct TrainEpi {
   const int8_t* qp;         // kGluBwd: codes [M, N] of the down projection's input, their scales, 1 / rms,
   const float *sp, *rp;     //   the row means of dxh x^, and the down projection's gain or null
   const float *cp, *gain_p;
-  int plane_rows, plane_cols;   // columns written per segment (N padded, zeros past N)
+  int planes, plane_rows, plane_cols;   // columns written per segment (N padded, zeros past N)
 };
 
 // Weight scale as it is folded into a stored gradient and divided out again: 1
@@ -158,10 +159,12 @@ bool tgemm_mma_fused_quant_supported(int M, int K, int esize);
 // tcgen05 (TMEM) contraction for prefill-sized token counts. Needs K % 64 == 0
 // and N % 128 == 0; `status` is the device status word for bounded-wait timeouts.
 bool tgemm_tc_supported(const TGemmArgs& a, Epi epi);
+// The same kernel on one-byte codes (a.wu) with any N and K a multiple of 16: kStore and kGlu where rows of the
+// output start on 16 bytes, kStoreAny elsewhere.
+bool tgemm_tc_any_supported(const TGemmArgs& a, Epi epi, mmf_dtype dt);
 cudaError_t launch_tgemm_tc(const TGemmArgs& a, Epi epi, mmf_dtype dt, int* status, cudaStream_t stream);
 // The training epilogues kLse, kDz, kGluBwd (a.wu set; out: bf16 planes, ldo columns).
-cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, mmf_dtype dt, int* status,
-                               cudaStream_t stream);
+cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, int* status, cudaStream_t stream);
 
 // bf16 training products (bgemm_tc.cu), D fp32 accumulated:
 //   dx: D[i, j] = row_scale[i] sum_g gamma[g] sum_r A[i, g R + r] B[g R + r, j]

@@ -33,6 +33,7 @@
 // and all roles leave their loops; nothing traps.
 #include "kernels.cuh"
 #include <cstddef>
+#include <type_traits>
 
 #include "umma.cuh"
 
@@ -105,6 +106,12 @@ struct TcArgs {
 
 __host__ __device__ constexpr bool is_train(Epi e) { return e == Epi::kLse || e == Epi::kDz || e == Epi::kGluBwd; }
 __host__ __device__ constexpr bool is_glu(Epi e) { return e == Epi::kGlu || e == Epi::kGluBwd; }
+// Training epilogues: T says how many bf16 planes they write.
+struct TwoPlanes {};
+template <typename T>
+constexpr int planes_in() {
+  return std::is_same<T, TwoPlanes>::value ? 2 : sizeof(T) == 2 ? 1 : 3;
+}
 // Bytes of one staged output element: the training epilogues stage bf16 planes.
 template <Epi EPI, typename T>
 constexpr int out_bytes() {
@@ -202,7 +209,7 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
   static_assert(!RB || (EPI == Epi::kStore && OB == 2), "residual prefetch: kStore with 2-byte outputs");
   using Smem = SmemLayout<OB, UNP, RB, EPI == Epi::kGluBwd>;
   constexpr int NS = Smem::NS;
-  constexpr int kPlanes = sizeof(T) == 2 ? 1 : 3;   // training epilogues
+  constexpr int kPlanes = planes_in<T>();   // training epilogues
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -473,14 +480,35 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
           for (int j = 0; j < 32; ++j) {
             float uu = (float)((int)ru[j] - qs) * sc_u;
             float vv = (float)((int)rv[j] - qs) * sc_v;
-            if (p.g.bias[0] != nullptr) uu += p.g.bias[0][n0 + j];
-            if (p.g.bias[1] != nullptr) vv += p.g.bias[1][n0 + j];
+            if (p.g.bias[0] != nullptr && n0 + j < p.g.N) uu += p.g.bias[0][n0 + j];
+            if (p.g.bias[1] != nullptr && n0 + j < p.g.N) vv += p.g.bias[1][n0 + j];
             out[j] = silu_fast(uu) * vv;
           }
           uint8_t* buf;
           claim(buf);
           stage_row(buf, lane, out, (T*)nullptr);
           release(n0, y0, buf);
+        }
+      } else if constexpr (EPI == Epi::kStoreAny) {
+        // rows of any pitch: a 32 x 32 box goes through shared memory, then out row by row
+        const float sc = *p.g.gamma[0] * inv_s;
+        const float* bias = p.g.bias[0];
+        for (int c = 0; c < HALF / 32; ++c) {
+          const int n0 = nt * BN + group * HALF + 32 * c;
+          if (n0 >= p.g.N) break;
+          uint32_t r[32];
+          tmem_ld32(tbase + group * HALF + 32 * c, r);
+          float* box = reinterpret_cast<float*>(sm.stage[ew][0]);   // both buffers: 32 x 32 fp32, column j of row r at j ^ r
+#pragma unroll
+          for (int j = 0; j < 32; ++j) box[lane * 32 + (j ^ lane)] = (float)((int)r[j] - qs) * sc;
+          __syncwarp();
+          const int n = n0 + lane;
+          const float b = bias != nullptr && n < p.g.N ? __ldg(bias + n) : 0.0f;
+          const int rows = min(32, p.g.M - y0);
+          if (n < p.g.N)
+            for (int i = 0; i < rows; ++i)
+              static_cast<T*>(p.g.out)[(size_t)(y0 + i) * p.g.ldo + n] = from_f32<T>(box[i * 32 + (lane ^ i)] + b);
+          __syncwarp();
         }
       } else if constexpr (EPI == Epi::kLse) {
         // Online softmax statistics of this token's 128 logits, in log2 units
@@ -658,7 +686,7 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               float v = (float)((int)r[j] - qs) * sc;
-              if (bias != nullptr) v += bias[n0 + j];
+              if (bias != nullptr && n0 + j < p.g.N) v += bias[n0 + j];
               out[j] = v;
             }
             const bool ok = mbar_wait(&sm.res_full[ew][c], nres & 1, abort_flag, p.status, p.wait_cycles);
@@ -691,7 +719,7 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
                 float v = (float)((int)r[j] - qs) * sc;
-                if (bias != nullptr) v += bias[n0 + j];
+                if (bias != nullptr && n0 + j < p.g.N) v += bias[n0 + j];
                 out[j] = v;
               }
               if (has_res) {
@@ -776,6 +804,16 @@ cudaError_t launch_typed(const CUtensorMap& ma, const CUtensorMap (&mb)[3], cons
 
 }  // namespace
 
+bool tgemm_tc_any_supported(const TGemmArgs& a, Epi epi, mmf_dtype dt) {
+  if (!tma_available() || a.K % 16 != 0) return false;
+  for (int i = 0; i < a.nseg; ++i)
+    if (a.wu[i] == nullptr) return false;
+  if (epi == Epi::kStoreAny) return a.nseg == 1 && a.residual == nullptr;
+  const int per16 = dt == MMF_BF16 ? 8 : 4;   // TMA rows start on 16 bytes
+  if (epi == Epi::kGlu) return a.nseg == 2 && a.N % per16 == 0;
+  return epi == Epi::kStore && a.nseg == 1 && a.N % per16 == 0;
+}
+
 bool tgemm_tc_supported(const TGemmArgs& a, Epi epi) {
   if (epi != Epi::kStore && epi != Epi::kAcc && epi != Epi::kGlu) return false;
   if (a.K % 64 != 0 || a.N % HALF != 0) return false;   // 16-byte TMA row strides, whole 128-row halves
@@ -786,7 +824,7 @@ bool tgemm_tc_supported(const TGemmArgs& a, Epi epi) {
 
 cudaError_t launch_tgemm_tc(const TGemmArgs& a, Epi epi, mmf_dtype dt, int* status, cudaStream_t stream) {
   if (a.M == 0) return cudaSuccess;
-  if (!tgemm_tc_supported(a, epi)) return cudaErrorNotSupported;
+  if (!tgemm_tc_supported(a, epi) && !tgemm_tc_any_supported(a, epi, dt)) return cudaErrorNotSupported;
   CUtensorMap ma, mb[3];
   if (!make_tma_2d(&ma, a.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.M, BK, BM,
                 CU_TENSOR_MAP_SWIZZLE_128B))
@@ -826,13 +864,15 @@ cudaError_t launch_tgemm_tc(const TGemmArgs& a, Epi epi, mmf_dtype dt, int* stat
     case Epi::kStore: return MMF_TC_LAUNCH(Epi::kStore);
     case Epi::kAcc: return MMF_TC_LAUNCH(Epi::kAcc);
     case Epi::kGlu: return MMF_TC_LAUNCH(Epi::kGlu);
+    case Epi::kStoreAny:   // ma stands in for the output map, which this epilogue does not use
+      return b ? launch_mapped<Epi::kStoreAny, bf16, true>(ma, mb, ma, ma, p, stream)
+               : launch_mapped<Epi::kStoreAny, float, true>(ma, mb, ma, ma, p, stream);
     default: return cudaErrorNotSupported;
   }
 #undef MMF_TC_LAUNCH
 }
 
-cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, mmf_dtype dt, int* status,
-                               cudaStream_t stream) {
+cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, int* status, cudaStream_t stream) {
   if (a.M == 0) return cudaSuccess;
   CUtensorMap ma, mb[3], mo;
   if (!make_tma_2d(&ma, a.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.M, BK, BM,
@@ -848,10 +888,9 @@ cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, m
                                          (uint64_t)a.N, BK, is_glu(epi) ? HALF : BN, CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok) return cudaErrorInvalidValue;
   }
-  const int planes = dt == MMF_BF16 ? 1 : 3;
   mo = ma;   // kLse stores no tile
   if (epi != Epi::kLse &&
-      !make_tma_2d(&mo, a.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)a.ldo, (uint64_t)planes * t.plane_rows,
+      !make_tma_2d(&mo, a.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)a.ldo, (uint64_t)t.planes * t.plane_rows,
                    epi == Epi::kGluBwd ? 16 : kEpiChunk, 32,
                    epi == Epi::kGluBwd ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
@@ -872,19 +911,19 @@ cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, m
   p.skip_it = (uint32_t)test_hook("MMF_TC_SKIP_KSTEP");
   p.m_tiles = ceil_div(a.M, BM);
   p.n_tiles = is_glu(epi) ? ceil_div(a.N, HALF) : ceil_div(a.N, BN);
-  const bool b = dt == MMF_BF16;
+#define MMF_TRAIN_LAUNCH(E)                                                             \
+  (t.planes == 1 ? launch_mapped<E, bf16, true>(ma, mb, mo, mr, p, stream)              \
+                 : t.planes == 2 ? launch_mapped<E, TwoPlanes, true>(ma, mb, mo, mr, p, stream) \
+                                 : launch_mapped<E, float, true>(ma, mb, mo, mr, p, stream))
   switch (epi) {
     case Epi::kLse:
       return packed ? launch_mapped<Epi::kLse, bf16, false>(ma, mb, mo, mr, p, stream)
                     : launch_mapped<Epi::kLse, bf16, true>(ma, mb, mo, mr, p, stream);
-    case Epi::kDz:
-      return b ? launch_mapped<Epi::kDz, bf16, true>(ma, mb, mo, mr, p, stream)
-               : launch_mapped<Epi::kDz, float, true>(ma, mb, mo, mr, p, stream);
-    case Epi::kGluBwd:
-      return b ? launch_mapped<Epi::kGluBwd, bf16, true>(ma, mb, mo, mr, p, stream)
-               : launch_mapped<Epi::kGluBwd, float, true>(ma, mb, mo, mr, p, stream);
+    case Epi::kDz: return MMF_TRAIN_LAUNCH(Epi::kDz);
+    case Epi::kGluBwd: return MMF_TRAIN_LAUNCH(Epi::kGluBwd);
     default: return cudaErrorNotSupported;
   }
+#undef MMF_TRAIN_LAUNCH
 }
 
 }  // namespace mmf

@@ -311,39 +311,101 @@ __global__ void __launch_bounds__(kThreads) dot_join_kernel(const float* __restr
 }
 
 // ---------------------------------------------------------------- column sums
-constexpr int kColsPerBlock = 64, kColLanes = kColsPerBlock / 4, kRowLanes = kThreads / kColLanes;
+constexpr int kColsPerBlock = 32, kColLanes = kColsPerBlock / 4, kRowLanes = kThreads / kColLanes;
+constexpr int kColBatch = 4;   // rows a thread has in flight
 
-// 4 columns c.. of row t; vec: rows start on 4-element boundaries and c + 4 <= cols.
-template <ColSum KIND, typename T>
-__device__ __forceinline__ void col_terms(const ColSumArgs& a, int t, int c, int cols, bool vec, float (&v)[4]) {
-  if constexpr (KIND == ColSum::kGain) {
-    const NormBackArgs& b = a.nb;
-    float xh[4], n[4], g[4];
-    const size_t at = (size_t)t * b.K + c;   // K is a multiple of 16
-    slices4(b, at, v);
-    norm4<T>(b, at, c, 1.0f / b.scale[t], b.rinv[t], xh, n, g);
+// Sums of 4 columns c.. over rows t0, t0 + kRowLanes, .. < t1. Each form issues
+// the loads of a batch of rows before it uses the first, with no branch among
+// them (a short sum's time is that latency: 16 us of 22 us before).
+template <typename T>
+__device__ __forceinline__ void sum_grad(const ColSumArgs& a, int t0, int t1, int c, int cols, float (&sum)[4]) {
+  const T* src = static_cast<const T*>(a.src) + c;
+  if (cols % 4 == 0) {   // rows start on 4-element boundaries
+    for (int t = t0; t < t1; t += kRowLanes * kColBatch) {
+      float v[kColBatch][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] *= n[i];
-  } else if constexpr (KIND == ColSum::kPlanes) {   // pitch is a multiple of 32
-    const float s = a.scale[t];
-    v[0] = v[1] = v[2] = v[3] = 0.0f;
-    for (int p = a.planes - 1; p >= 0; --p) {
-      float w[4];
-      ld4(static_cast<const bf16*>(a.src) + ((size_t)p * a.plane_rows + t) * cols + c, w);
+      for (int u = 0; u < kColBatch; ++u) ld4(src + (size_t)min(t + u * kRowLanes, t1 - 1) * cols, v[u]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += w[i];
+      for (int u = 0; u < kColBatch; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] += t + u * kRowLanes < t1 ? v[u][i] : 0.0f;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] *= s;
   } else {
-    const T* src = static_cast<const T*>(a.src) + (size_t)t * cols + c;
-    if (vec) {
-      ld4(src, v);
-    } else {
+    for (int t = t0; t < t1; t += kRowLanes * kColBatch) {
+      float v[kColBatch][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = c + i < cols ? to_f32(src[i]) : 0.0f;
+      for (int u = 0; u < kColBatch; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[u][i] = to_f32(src[(size_t)min(t + u * kRowLanes, t1 - 1) * cols + (c + i < cols ? i : 0)]);
+#pragma unroll
+      for (int u = 0; u < kColBatch; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] += t + u * kRowLanes < t1 ? v[u][i] : 0.0f;
     }
   }
+}
+
+template <int PLANES>
+__device__ __forceinline__ void sum_planes(const ColSumArgs& a, int t0, int t1, int c, int cols, float (&sum)[4]) {
+  const bf16* src = static_cast<const bf16*>(a.src) + c;   // the pitch is a multiple of 32
+  for (int t = t0; t < t1; t += kRowLanes * kColBatch) {
+    float v[kColBatch][PLANES][4], s[kColBatch];
+#pragma unroll
+    for (int u = 0; u < kColBatch; ++u) {
+      const int r = min(t + u * kRowLanes, t1 - 1);
+      s[u] = a.scale[r];
+#pragma unroll
+      for (int p = 0; p < PLANES; ++p) ld4(src + ((size_t)p * a.plane_rows + r) * cols, v[u][p]);
+    }
+#pragma unroll
+    for (int u = 0; u < kColBatch; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float g = v[u][PLANES - 1][i];
+#pragma unroll
+        for (int p = PLANES - 2; p >= 0; --p) g += v[u][p][i];
+        sum[i] += t + u * kRowLanes < t1 ? g * s[u] : 0.0f;
+      }
+  }
+}
+
+// sum over rows (and slices) of dx^ n; X: n from the kept input, else from the codes.
+template <typename T, bool X>
+__device__ __forceinline__ void sum_gain(const NormBackArgs& b, int t0, int t1, int c, float (&sum)[4]) {
+  float g[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+  if (!X && b.gain != nullptr) ld4(b.gain + c, g);
+  float total[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int sl = 0; sl < b.slices; ++sl) {
+    const float* dxh = b.dxh + (size_t)sl * b.slice_rows * b.K + c;
+    for (int t = t0; t < t1; t += kRowLanes * kColBatch) {
+      float v[kColBatch][4], x[kColBatch][4], f[kColBatch];
+      int w[kColBatch];
+#pragma unroll
+      for (int u = 0; u < kColBatch; ++u) {
+        const int r = min(t + u * kRowLanes, t1 - 1);
+        ld4(dxh + (size_t)r * b.K, v[u]);
+        if constexpr (X) {
+          ld4(static_cast<const T*>(b.x) + (size_t)r * b.K + c, x[u]);
+          f[u] = b.rinv[r];
+        } else {
+          w[u] = *reinterpret_cast<const int*>(b.q + (size_t)r * b.K + c);
+          f[u] = b.scale[r];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kColBatch; ++u) {
+        const float k = t + u * kRowLanes < t1 ? (X ? f[u] : 1.0f / f[u]) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float n = X ? x[u][i] : (float)((w[u] << (24 - 8 * i)) >> 24);
+          total[i] = k != 0.0f ? fmaf(v[u][i], n * k, total[i]) : total[i];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum[i] += X ? total[i] : (g[i] != 0.0f ? total[i] / g[i] : 0.0f);
 }
 
 template <typename T>
@@ -364,20 +426,8 @@ struct ColSumTasks {
   int n;
 };
 
-template <ColSum KIND, typename T>
-__device__ __forceinline__ void col_range(const ColSumArgs& a, int t0, int t1, int c, int cols, float (&sum)[4]) {
-  const bool vec = cols % 4 == 0;
-#pragma unroll 4
-  for (int t = t0; t < t1; t += kRowLanes) {
-    float v[4];
-    col_terms<KIND, T>(a, t, c, cols, vec, v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum[i] += v[i];
-  }
-}
-
-// All of a call's column sums in one launch. A block has 64 columns and a range
-// of rows of one task; a thread sums every 16th row of 4 columns, the 16 are
+// All of a call's column sums in one launch. A block has 32 columns and a range
+// of rows of one task; a thread sums every 32nd row of 4 columns, the 32 are
 // added in order. One range writes the result, several write partial sums.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) colsum_kernel(const __grid_constant__ ColSumTasks l) {
@@ -392,10 +442,16 @@ __global__ void __launch_bounds__(kThreads) colsum_kernel(const __grid_constant_
   const int t0 = part * k.rows_per, t1 = min(k.a.M, t0 + k.rows_per);
   float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c < k.cols) {
-    switch (k.kind) {
-      case ColSum::kGrad: col_range<ColSum::kGrad, T>(k.a, t0 + rl, t1, c, k.cols, sum); break;
-      case ColSum::kPlanes: col_range<ColSum::kPlanes, T>(k.a, t0 + rl, t1, c, k.cols, sum); break;
-      case ColSum::kGain: col_range<ColSum::kGain, T>(k.a, t0 + rl, t1, c, k.cols, sum); break;
+    if (k.kind == ColSum::kGrad) {
+      sum_grad<T>(k.a, t0 + rl, t1, c, k.cols, sum);
+    } else if (k.kind == ColSum::kPlanes) {
+      if (k.a.planes == 1) sum_planes<1>(k.a, t0 + rl, t1, c, k.cols, sum);
+      else if (k.a.planes == 2) sum_planes<2>(k.a, t0 + rl, t1, c, k.cols, sum);
+      else sum_planes<3>(k.a, t0 + rl, t1, c, k.cols, sum);
+    } else if (k.a.nb.x != nullptr) {
+      sum_gain<T, true>(k.a.nb, t0 + rl, t1, c, sum);
+    } else {
+      sum_gain<T, false>(k.a.nb, t0 + rl, t1, c, sum);
     }
   }
 #pragma unroll
@@ -422,11 +478,11 @@ __global__ void __launch_bounds__(kThreads) colsum_join_kernel(const __grid_cons
   col_store<T>(k.a, c, v);
 }
 
-// Row ranges: at least 256 rows each (16 per thread; below that one launch is
+// Row ranges: at least 512 rows each (16 per thread; below that one launch is
 // quicker than two), about two blocks per SM in all.
 int colsum_parts(int M, int cols) {
   const int want = std::max(1, 2 * 148 / ceil_div(cols, kColsPerBlock));
-  return std::max(1, std::min(want, ceil_div(M, 256)));
+  return std::max(1, std::min(want, ceil_div(M, 512)));
 }
 
 // ---------------------------------------------------------------- joining slices of dW
@@ -461,7 +517,7 @@ __global__ void __launch_bounds__(kThreads) dw_join_kernel(const DwJoinArgs a) {
 
 // ---------------------------------------------------------------- the loss
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kJoinRows = 32, kJoinGroups = kThreads / kJoinRows;
+constexpr int kJoinRows = 32, kJoinGroups = 8;
 
 __device__ __forceinline__ bool counted_label(const LossArgs& a, int l) {
   return l != a.ignore_index && l >= 0 && l < a.vocab;
@@ -471,8 +527,8 @@ __device__ __forceinline__ bool counted_label(const LossArgs& a, int l) {
 // g, g + 8, ... (slot-major, so a warp reads 32 neighbouring rows), the eight
 // are folded in order. loss_t = (lse - z_label), both in log2 units until here.
 // Returns this thread's row's loss (0 but for g = 0).
-__device__ __forceinline__ float loss_rows(const LossArgs& a, int m, int r, int g, float2 (*red)[kJoinRows],
-                                           int* status) {
+template <int ROWS>
+__device__ __forceinline__ float loss_rows(const LossArgs& a, int m, int r, int g, float2 (*red)[ROWS], int* status) {
   float mx = -INFINITY, sum = 0.0f;
   auto fold = [&](float2 o) {
     const float nm = fmaxf(mx, o.x);
@@ -514,25 +570,37 @@ __global__ void __launch_bounds__(kThreads) loss_rows_kernel(const LossArgs a, i
   loss_rows(a, blockIdx.x * kJoinRows + r, r, threadIdx.x / kJoinRows, red, status);
 }
 
-// Few tokens: rows and reduction in one block.
-__global__ void __launch_bounds__(kThreads) loss_small_kernel(const LossArgs a, int* status) {
-  __shared__ float2 red[kJoinGroups][kJoinRows];
+// Few tokens: rows, 128 at a time, and reduction in one block.
+constexpr int kSmallRows = 128;
+__global__ void __launch_bounds__(1024) loss_small_kernel(const LossArgs a, int* status) {
+  __shared__ float2 red[kJoinGroups][kSmallRows];
+  __shared__ double sums[kSmallRows / 32];
+  __shared__ int counts[kSmallRows / 32];
   pdl_trigger();
   pdl_wait();
-  const int r = threadIdx.x % kJoinRows, g = threadIdx.x / kJoinRows;
+  const int r = threadIdx.x % kSmallRows, g = threadIdx.x / kSmallRows;
   double s = 0.0;
   int n = 0;
-  for (int m0 = 0; m0 < a.M; m0 += kJoinRows) {
+  for (int m0 = 0; m0 < a.M; m0 += kSmallRows) {
     s += (double)loss_rows(a, m0 + r, r, g, red, status);
     n += g == 0 && m0 + r < a.M && counted_label(a, a.labels[m0 + r]);
   }
-  if (g == 0) {   // one warp holds all of it
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      s += __shfl_xor_sync(0xffffffffu, s, o);
-      n += __shfl_xor_sync(0xffffffffu, n, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+  }
+  if (g == 0 && r % 32 == 0) {
+    sums[r / 32] = s;
+    counts[r / 32] = n;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kSmallRows / 32; ++w) {
+      s += sums[w];
+      n += counts[w];
     }
-    if (r == 0) loss_out(a, s, n);
+    loss_out(a, s, n);
   }
 }
 
@@ -671,8 +739,8 @@ cudaError_t launch_dw_join(const DwJoinArgs& a, mmf_dtype dt, cudaStream_t strea
 }
 
 cudaError_t launch_loss_join(const LossArgs& a, int* status, cudaStream_t stream) {
-  if (a.M <= 8 * kJoinRows && a.reduction != MMF_REDUCE_NONE)
-    return launch_pdl(loss_small_kernel, dim3(1), dim3(kThreads), 0, stream, a, status);
+  if (a.M <= 4 * kSmallRows && a.reduction != MMF_REDUCE_NONE)
+    return launch_pdl(loss_small_kernel, dim3(1), dim3(1024), 0, stream, a, status);
   cudaError_t e = launch_pdl(loss_rows_kernel, dim3(ceil_div(a.M, kJoinRows)), dim3(kThreads), 0, stream, a, status);
   if (e != cudaSuccess || a.reduction == MMF_REDUCE_NONE) return e;
   return launch_pdl(loss_reduce_kernel, dim3(1), dim3(1024), 0, stream, a);

@@ -9,8 +9,15 @@ namespace {
 constexpr size_t kPieceBytes = size_t(256) << 20;   // gradient of the logits held at once
 
 int pad(int v, int to) { return (v + to - 1) / to * to; }
-int planes_of(mmf_dtype dt) { return dt == MMF_BF16 ? 1 : 3; }
-int plane_rows_of(int M, mmf_dtype dt) { return dt == MMF_BF16 ? M : pad(M, 128); }
+
+// bf16 planes of a gradient [M, cols] that meets K columns: three for fp32
+// (24 bits); one for bf16, but two (16 bits) for products up to 1 GFLOP, which
+// launches bound: there the exactness costs nothing, and the few values of a
+// short gradient then carry one rounding, their own.
+int planes_of(mmf_dtype dt, int M, int K, int cols) {
+  return dt == MMF_F32 ? 3 : 2.0 * M * K * cols <= 1e9 ? 2 : 1;
+}
+int plane_rows_of(int M, int planes) { return planes == 1 ? M : pad(M, 128); }
 
 mmf_status check_kept(const mmf_act8* k, const char* what) {
   if (k == nullptr) return fail(MMF_ERR_INVALID_ARG, "%s: null kept activations", what);
@@ -76,6 +83,33 @@ mmf_status quant_keep(const void* x, mmf_dtype dt, int M, int K, const float* ga
 // below, that launch costs more than it saves.
 constexpr int kUnpackMinTokens = 1024;
 
+// Shapes that run_gemm leaves to the decode-sized kernel (widths that are not
+// whole tiles) take the tcgen05 kernel's general form, on one-byte codes, once
+// the product is worth its launches: from 2^28 multiplications (1003 x 1040 x
+// 777: 22 us on the decode-sized kernel).
+bool wants_general(int M, int N, int K, bool plain_tc) {
+  return !plain_tc && M >= 128 && (double)M * N * K >= (double)(1 << 28);
+}
+
+// y [M, nseg, N] of a training forward on one-byte codes by the general form, one launch per layer.
+mmf_status run_general(TGemmArgs a, mmf_dtype dt, cudaStream_t s) {
+  const int nseg = a.nseg;
+  const TGemmArgs all = a;
+  a.nseg = 1;
+  for (int i = 0; i < nseg; ++i) {
+    a.wu[0] = all.wu[i];
+    a.w[0] = all.w[i];
+    a.gamma[0] = all.gamma[i];
+    a.bias[0] = all.bias[i];
+    a.out = static_cast<char*>(all.out) + (size_t)i * a.N * elem_bytes(dt);
+    const bool whole = nseg == 1 && tgemm_tc_any_supported(a, Epi::kStore, dt);
+    MMF_CUDA(timed("tgemm_tc:train", s,
+                   [&] { return launch_tgemm_tc(a, whole ? Epi::kStore : Epi::kStoreAny, dt, status_word(), s); }),
+             "contraction");
+  }
+  return MMF_OK;
+}
+
 // ---------------------------------------------------------------- the two products of a backward
 
 // An operand gradient G [M, cols], as bf16 planes: dy itself, or prepared ones.
@@ -91,10 +125,10 @@ struct Products {
   BGemmShape dx, dw;
   BGemmPlan plan;
 };
-Products products(int M, int K, int nseg, int cols, int dw_cols, mmf_dtype dt) {
+Products products(int M, int K, int nseg, int cols, int dw_cols, int planes) {
   Products p;
-  p.dx = {M, K, cols, planes_of(dt), nseg};
-  p.dw = {dw_cols, K, M, planes_of(dt), 1};
+  p.dx = {M, K, cols, planes, nseg};
+  p.dw = {dw_cols, K, M, planes, 1};
   p.plan = bgemm_plan(p.dx, p.dw);
   return p;
 }
@@ -229,19 +263,19 @@ mmf_status run_prep(const PrepArgs* a, const PrepArgs* b, cudaStream_t s) {
 
 // A caller's gradient [M, nlin, N] is the operand as it lies when its rows and
 // layers start on TMA's 16 bytes (several layers: on whole 64-step blocks of
-// the reduction); fp32 ones, and the others, are written to padded bf16 planes
-// first.
+// the reduction); the others, and those of several planes, are written to padded
+// bf16 planes first.
 struct LinearPlan {
   bool copy;
   int pitch, cols, planes, rows;
 };
-LinearPlan linear_plan(int nlin, int N, int M, mmf_dtype dt) {
+LinearPlan linear_plan(int nlin, int N, int K, int M, mmf_dtype dt) {
   LinearPlan p;
-  p.copy = dt == MMF_F32 || N % 8 != 0 || (nlin > 1 && N % 64 != 0);
+  p.planes = planes_of(dt, M, K, nlin * N);
+  p.copy = p.planes > 1 || N % 8 != 0 || (nlin > 1 && N % 64 != 0);
   p.pitch = !p.copy ? N : pad(N, nlin > 1 ? 64 : 8);
   p.cols = nlin * p.pitch;
-  p.planes = planes_of(dt);
-  p.rows = plane_rows_of(M, dt);
+  p.rows = plane_rows_of(M, p.planes);
   return p;
 }
 
@@ -252,12 +286,12 @@ struct LinearWs {
   size_t gain_floats;   // the gain's share of colpart; the biases' follow
 };
 LinearWs carve_linear(Carver& c, int nlin, int N, int K, int M, mmf_dtype dt, bool dots = false) {
-  const LinearPlan p = linear_plan(nlin, N, M, dt);
+  const LinearPlan p = linear_plan(nlin, N, K, M, dt);
   LinearWs w;
   w.wb = c.take<char>((size_t)p.cols * K * 2);
   w.qb = c.take<char>((size_t)M * K * 2);
   w.gb = c.take<char>(p.copy ? (size_t)p.planes * p.rows * p.cols * 2 : 0);
-  w.pr = products(M, K, nlin, p.pitch, nlin == 1 ? N : p.cols, dt);
+  w.pr = products(M, K, nlin, p.pitch, nlin == 1 ? N : p.cols, p.planes);
   w.dxh = c.take<float>(dxh_floats(w.pr));
   w.part = c.take<float>(part_floats(w.pr));
   w.gain_floats = colsum_ws_floats(M, K);
@@ -270,7 +304,7 @@ LinearWs carve_linear(Carver& c, int nlin, int N, int K, int M, mmf_dtype dt, bo
 PrepArgs linear_prep(const mmf_tlinear* lins, int nlin, const mmf_act8& kept, const void* dy, mmf_dtype dt, int M,
                      bool want_dxh, bool want_dw, const LinearWs& w) {
   const int N = lins[0].N, K = lins[0].K;
-  const LinearPlan lp = linear_plan(nlin, N, M, dt);
+  const LinearPlan lp = linear_plan(nlin, N, K, M, dt);
   PrepArgs pa = {};
   pa.M = M;
   pa.scale = kept.scale;
@@ -286,7 +320,7 @@ PrepArgs linear_prep(const mmf_tlinear* lins, int nlin, const mmf_act8& kept, co
   if (want_dw) {
     pa.q = kept.q;
     pa.qK = K;
-    pa.q_scaled = dt == MMF_BF16;   // fp32: the gradient's planes carry 1 / s instead
+    pa.q_scaled = lp.planes == 1;   // several planes carry 1 / s themselves
     pa.qb = w.qb;
   }
   if (lp.copy && (want_dxh || want_dw)) {
@@ -296,7 +330,7 @@ PrepArgs linear_prep(const mmf_tlinear* lins, int nlin, const mmf_act8& kept, co
     pa.g_pitch = lp.pitch;
     pa.g_planes = lp.planes;
     pa.g_rows = lp.rows;
-    pa.g_scaled = dt == MMF_F32;
+    pa.g_scaled = lp.planes > 1;
     pa.gb = w.gb;
   }
   return pa;
@@ -309,7 +343,7 @@ mmf_status linear_backward(const mmf_tlinear* lins, int nlin, const mmf_act8& ke
                            const void* dres, mmf_dtype dt, int M, const mmf_linear_grads& g, const LinearWs& w,
                            float* cmean, ColSumList& sums, cudaStream_t s) {
   const int N = lins[0].N, K = lins[0].K;
-  const LinearPlan lp = linear_plan(nlin, N, M, dt);
+  const LinearPlan lp = linear_plan(nlin, N, K, M, dt);
   const bool want_dxh = g.dx != nullptr || g.dgain != nullptr || cmean != nullptr;
   bool want_dw = false;
   void* dw[3] = {};
@@ -322,11 +356,11 @@ mmf_status linear_backward(const mmf_tlinear* lins, int nlin, const mmf_act8& ke
   G.ld = lp.cols;
   G.plane_rows = lp.rows;
   G.planes = lp.planes;
-  G.over_s = dt == MMF_F32;
+  G.over_s = lp.planes > 1;
   mmf_status r = MMF_OK;
   const float* gam[3] = {lins[0].gamma, lins[nlin > 1 ? 1 : 0].gamma, lins[nlin > 2 ? 2 : 0].gamma};
   // the means come with the product where one launch of it leaves whole sums
-  const bool dots = cmean != nullptr && nlin == 1 && dt == MMF_BF16 && !w.pr.plan.together && w.pr.plan.splits[0] == 1;
+  const bool dots = cmean != nullptr && nlin == 1 && lp.planes == 1 && !w.pr.plan.together && w.pr.plan.splits[0] == 1;
   if (want_dxh || want_dw)
     r = run_products(w.pr, G, w.wb, gam, kept.scale, false, want_dxh ? w.dxh : nullptr, w.qb, nlin, N, lp.pitch,
                      nullptr, want_dw ? dw : nullptr, w.part, dt, s, dots ? kept.q : nullptr, w.dots);
@@ -380,7 +414,8 @@ mmf_status zero_grads(const mmf_linear_grads& g, int n, int N, int K, mmf_dtype 
 }  // namespace
 
 extern "C" size_t mmf_bitlinear_train_ws_size(int32_t nlin, int32_t N, int32_t K, int32_t M) {
-  if (nlin < 1 || nlin > 3 || N < 0 || K < 0 || M < kUnpackMinTokens) return 0;
+  if (nlin < 1 || nlin > 3 || N < 0 || K < 0 || M < 128) return 0;
+  if (M < kUnpackMinTokens && !wants_general(M, N * nlin, K, N % 128 == 0 && K % 64 == 0)) return 0;
   return round_up((size_t)nlin * N * K, 256) + 1024;
 }
 
@@ -402,7 +437,8 @@ extern "C" mmf_status mmf_bitlinear_train(const mmf_tlinear* lins, int32_t nlin,
   if ((r = quant_keep(x, dtype, M, K, lins[0].gain, eps, *kept, s)) != MMF_OK) return r;
   const mmf_tlinear* segs[3] = {&lins[0], &lins[nlin > 1 ? 1 : 0], &lins[nlin > 2 ? 2 : 0]};
   TGemmArgs a = gemm_args(segs, nlin, kept->q, kept->scale, kept->qsum, M, y, nlin * N, nullptr, nullptr);
-  if (M >= kUnpackMinTokens && tgemm_tc_supported(a, Epi::kStore)) {
+  const bool plain = tgemm_tc_supported(a, Epi::kStore), general = wants_general(M, N * nlin, K, plain);
+  if ((M >= kUnpackMinTokens && plain) || general) {
     Carver c(ws);
     PrepArgs pa = {};
     pa.dy_dt = dtype;
@@ -418,6 +454,7 @@ extern "C" mmf_status mmf_bitlinear_train(const mmf_tlinear* lins, int32_t nlin,
     const PrepArgs* sets[1] = {&pa};
     MMF_CUDA(timed("train_prep", s, [&] { return launch_train_prep(sets, 1, s); }), "one-byte codes");
   }
+  if (general) return run_general(a, dtype, s);
   MMF_CUDA(run_gemm(a, Epi::kStore, dtype, s, "train"), "contraction");
   return MMF_OK;
 }
@@ -487,7 +524,9 @@ extern "C" mmf_status mmf_glu_train(const mmf_tlinear* gate, const mmf_tlinear* 
   const mmf_tlinear* dn[1] = {down};
   TGemmArgs a = gemm_args(gu, 2, kept_x->q, kept_x->scale, kept_x->qsum, M, p, I, nullptr, nullptr);
   TGemmArgs b = gemm_args(dn, 1, kept_p->q, kept_p->scale, kept_p->qsum, M, y, d, residual, nullptr);
-  if (M >= kUnpackMinTokens) {
+  const bool plain_gu = tgemm_tc_supported(a, Epi::kGlu), plain_dn = tgemm_tc_supported(b, Epi::kStore);
+  const bool gen_gu = wants_general(M, 2 * I, d, plain_gu), gen_dn = wants_general(M, d, I, plain_dn);
+  if (M >= kUnpackMinTokens || gen_gu || gen_dn) {
     PrepArgs pa = {}, pd = {};   // gate and up; down
     pa.dy_dt = pd.dy_dt = dtype;
     pa.nseg = 2;
@@ -509,9 +548,18 @@ extern "C" mmf_status mmf_glu_train(const mmf_tlinear* gate, const mmf_tlinear* 
     b.wu[0] = wu[2];
   }
   if ((r = quant_keep(x, dtype, M, d, gate->gain, eps, *kept_x, s)) != MMF_OK) return r;
-  MMF_CUDA(run_gemm(a, Epi::kGlu, dtype, s, "gate_up"), "contraction");
+  // d and I are multiples of 16, so rows of p and y start on 16 bytes
+  if (gen_gu)
+    MMF_CUDA(timed("tgemm_tc:gate_up", s, [&] { return launch_tgemm_tc(a, Epi::kGlu, dtype, status_word(), s); }),
+             "contraction");
+  else
+    MMF_CUDA(run_gemm(a, Epi::kGlu, dtype, s, "gate_up"), "contraction");
   if ((r = quant_keep(p, dtype, M, I, down->gain, eps, *kept_p, s)) != MMF_OK) return r;
-  MMF_CUDA(run_gemm(b, Epi::kStore, dtype, s, "down"), "contraction");
+  if (gen_dn)
+    MMF_CUDA(timed("tgemm_tc:down", s, [&] { return launch_tgemm_tc(b, Epi::kStore, dtype, status_word(), s); }),
+             "contraction");
+  else
+    MMF_CUDA(run_gemm(b, Epi::kStore, dtype, s, "down"), "contraction");
   return MMF_OK;
 }
 
@@ -526,16 +574,16 @@ struct GluWs {
   size_t gain_floats;
 };
 GluWs carve_glu(Carver& c, int M, int d, int I, mmf_dtype dt) {
-  const int Ip = pad(I, 32), rows = plane_rows_of(M, dt);
+  const int Ip = pad(I, 32), planes = planes_of(dt, M, d, 2 * I), rows = plane_rows_of(M, planes);
   GluWs w;
   w.down = carve_linear(c, 1, d, I, M, dt, true);
   w.wu_gate = c.take<uint8_t>((size_t)I * d);
   w.wu_up = c.take<uint8_t>((size_t)I * d);
   w.wb = c.take<char>((size_t)2 * Ip * d * 2);
   w.qb = c.take<char>((size_t)M * d * 2);
-  w.dz = c.take<char>((size_t)planes_of(dt) * rows * 2 * Ip * 2);
+  w.dz = c.take<char>((size_t)planes * rows * 2 * Ip * 2);
   w.cmean = c.take<float>(M);
-  w.pr = products(M, d, 1, 2 * Ip, 2 * Ip, dt);
+  w.pr = products(M, d, 1, 2 * Ip, 2 * Ip, planes);
   w.dxh = c.take<float>(dxh_floats(w.pr));
   w.part = c.take<float>(part_floats(w.pr));
   w.gain_floats = colsum_ws_floats(M, d);
@@ -586,7 +634,7 @@ extern "C" mmf_status mmf_glu_backward(const mmf_tlinear* gate, const mmf_tlinea
   const bool want_db = gx.dbias[0] != nullptr || gx.dbias[1] != nullptr;
   const bool inner = want_dxh || want_dw || want_db;   // anything behind the product
   // 1. every operand
-  const int Ip = pad(I, 32), rows = plane_rows_of(M, dtype), planes = planes_of(dtype);
+  const int Ip = pad(I, 32), planes = planes_of(dtype, M, d, 2 * I), rows = plane_rows_of(M, planes);
   const mmf_tlinear* gu[2] = {gate, up};
   const PrepArgs pd = linear_prep(down, 1, *kept_p, dy, dtype, M, inner || gd.dgain != nullptr, gd.dw[0] != nullptr, w.down);
   PrepArgs pa = {};
@@ -625,9 +673,10 @@ extern "C" mmf_status mmf_glu_backward(const mmf_tlinear* gate, const mmf_tlinea
   t.rp = kept_p->rinv;
   t.cp = w.cmean;
   t.gain_p = down->gain;
+  t.planes = planes;
   t.plane_rows = rows;
   t.plane_cols = Ip;
-  MMF_CUDA(timed("tgemm_tc:glu_back", s, [&] { return launch_tgemm_train(a, t, Epi::kGluBwd, dtype, status_word(), s); }),
+  MMF_CUDA(timed("tgemm_tc:glu_back", s, [&] { return launch_tgemm_train(a, t, Epi::kGluBwd, status_word(), s); }),
            "gradient of the product");
   // 4. gate and up
   Grad G;
@@ -690,8 +739,8 @@ LossWs carve_loss(Carver& c, int M, int V, int K) {
 
 // Equal pieces of the vocabulary, whole 256-column tiles, of at most
 // kPieceBytes of gradient (but no fewer than 1024 columns).
-int piece_cols(int M, int V, mmf_dtype dt) {
-  const size_t col = (size_t)planes_of(dt) * plane_rows_of(M, dt) * 2;
+int piece_cols(int M, int V, int planes) {
+  const size_t col = (size_t)planes * plane_rows_of(M, planes) * 2;
   const int most = (int)std::max<size_t>(1024, std::min<size_t>(kPieceBytes / std::max<size_t>(col, 1) / 256 * 256, 1u << 28));
   const int pieces = ceil_div(V, most);
   return pad(ceil_div(V, pieces), 256);
@@ -705,14 +754,15 @@ struct HeadWs {
   size_t gain_floats;
 };
 HeadWs carve_head(Carver& c, int M, int V, int K, mmf_dtype dt) {
-  const int vp = std::min(piece_cols(M, V, dt), pad(V, 32));
+  const int planes = planes_of(dt, M, K, V);
+  const int vp = std::min(piece_cols(M, V, planes), pad(V, 32));
   HeadWs w;
   w.wu = c.take<uint8_t>((size_t)V * K);
   w.wb = c.take<char>((size_t)V * K * 2);
   w.qb = c.take<char>((size_t)M * K * 2);
-  w.dz = c.take<char>((size_t)planes_of(dt) * plane_rows_of(M, dt) * vp * 2);
+  w.dz = c.take<char>((size_t)planes * plane_rows_of(M, planes) * vp * 2);
   const int n = std::min(vp, V), last = V - (ceil_div(V, vp) - 1) * vp;
-  w.pr = products(M, K, 1, n, n, dt);
+  w.pr = products(M, K, 1, n, n, planes);
   Products tail = w.pr;   // the last piece keeps the plan
   tail.dx.R = tail.dw.I = last;
   w.dxh = c.take<float>(dxh_floats(w.pr));
@@ -768,7 +818,7 @@ extern "C" mmf_status mmf_head_loss(const mmf_tlinear* head, const void* x, mmf_
   t.vocab = V;
   t.part = w.part;
   t.zlabel = w.zlabel;
-  MMF_CUDA(timed("tgemm_tc:lse", s, [&] { return launch_tgemm_train(a, t, Epi::kLse, dtype, status_word(), s); }),
+  MMF_CUDA(timed("tgemm_tc:lse", s, [&] { return launch_tgemm_train(a, t, Epi::kLse, status_word(), s); }),
            "logits");
   LossArgs l = {};
   l.part = w.part;
@@ -814,7 +864,8 @@ extern "C" mmf_status mmf_head_loss_backward(const mmf_tlinear* head, const mmf_
   Carver c(ws);
   const HeadWs w = carve_head(c, M, V, K, dtype);
   if (ws_bytes < c.off + 256) return fail(MMF_ERR_WORKSPACE, "%s: ws_bytes=%zu < %zu", what, ws_bytes, c.off + 256);
-  const int vp = std::min(piece_cols(M, V, dtype), pad(V, 32)), rows = plane_rows_of(M, dtype);
+  const int planes = planes_of(dtype, M, K, V), rows = plane_rows_of(M, planes);
+  const int vp = std::min(piece_cols(M, V, planes), pad(V, 32));
   const bool want_dxh = grads->dx != nullptr || grads->dgain != nullptr, want_dw = grads->dw[0] != nullptr;
   const bool want_db = grads->dbias[0] != nullptr;
   if (!want_dxh && !want_dw && !want_db) return MMF_OK;
@@ -854,15 +905,16 @@ extern "C" mmf_status mmf_head_loss_backward(const mmf_tlinear* head, const mmf_
     t.count = reduction == MMF_REDUCE_MEAN ? count : nullptr;
     t.per_token = reduction == MMF_REDUCE_NONE;
     t.ignore_index = ignore_index;
+    t.planes = planes;
     t.plane_rows = rows;
     t.plane_cols = pad(n, 32);
-    MMF_CUDA(timed("tgemm_tc:dz", s, [&] { return launch_tgemm_train(a, t, Epi::kDz, dtype, status_word(), s); }),
+    MMF_CUDA(timed("tgemm_tc:dz", s, [&] { return launch_tgemm_train(a, t, Epi::kDz, status_word(), s); }),
              "gradient of the logits");
     Grad G;
     G.g = w.dz;
     G.ld = vp;
     G.plane_rows = rows;
-    G.planes = planes_of(dtype);
+    G.planes = planes;
     G.over_s = true;
     if (want_dxh || want_dw) {
       Products pr = w.pr;

@@ -15,7 +15,6 @@ of the input's device.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import NamedTuple, Optional, Sequence, Union
 
@@ -48,10 +47,10 @@ class Act8:
         self._m, self._k = q.shape
 
     @classmethod
-    def _new(cls, m: int, k: int, device: torch.device, extra: int = 0) -> "Act8":
+    def _new(cls, m: int, k: int, like: torch.Tensor, extra: int = 0) -> "Act8":
         me = cls.__new__(cls)
         me._parts, me._m, me._k = None, m, k
-        me._buf = torch.empty(_pad16(m * k) + 3 * _pad16(4 * m) + extra, dtype=torch.int8, device=device)
+        me._buf = like.new_empty(_pad16(m * k) + 3 * _pad16(4 * m) + extra, dtype=torch.int8)
         return me
 
     def _tensors(self):
@@ -86,9 +85,9 @@ class HeadKept:
 
     __slots__ = ("act", "dtype", "_tail")
 
-    def __init__(self, m: int, k: int, dtype: torch.dtype, device: torch.device):
-        self.act = Act8._new(m, k, device, _pad16(4 * m) + 16)
-        self.dtype = dtype
+    def __init__(self, m: int, k: int, x: torch.Tensor):
+        self.act = Act8._new(m, k, x, _pad16(4 * m) + 16)
+        self.dtype = x.dtype
         self._tail = _pad16(m * k) + 3 * _pad16(4 * m)   # lse, then count, behind the codes
 
     def _ptrs(self):
@@ -126,13 +125,16 @@ def _pad16(n: int) -> int:
     return (n + 15) // 16 * 16
 
 
-def _on(index: int):
-    """Run on device `index`, whichever one is current."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == index else torch.cuda.device(index)
-
-
-def _stream(index: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(index)
+def _call(index: int, name: str, *args) -> None:
+    """Library call `name` on the current stream of device `index`, whichever device is current."""
+    fn = getattr(L.load(), name)
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        L.check(status, name)
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -189,14 +191,14 @@ def _like(t: Optional[torch.Tensor], numel: int, dtype: torch.dtype, what: str) 
         raise ValueError(f"{what} must have the shape and dtype of the input")
 
 
-def _scratch(nbytes: int, device: torch.device, ws: Optional[torch.Tensor]):
-    """(address, bytes, tensor) of the caller's workspace, or of a new one."""
+def _scratch(nbytes: int, like: torch.Tensor, ws: Optional[torch.Tensor]):
+    """(address, bytes, tensor) of the caller's workspace, or of a new one on like's device."""
     if nbytes == 0:
         return None, 0, None
     if ws is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws = like.new_empty(nbytes, dtype=torch.uint8)
         return ws.data_ptr(), nbytes, ws
-    _check(device.index, ws)
+    _check(like.get_device(), ws)
     have = ws.numel() * ws.element_size()
     if have < nbytes:
         raise ValueError(f"workspace too small: {have} < {nbytes}")
@@ -210,19 +212,18 @@ def bitlinear_train(lins: Union[TLinear, Sequence[TLinear]], x: torch.Tensor, ep
     """Training forward of 1 to 3 layers of one shape and gain on x [..., K] (mmf_bitlinear_train).
 
     Returns (y, kept): y [..., N] for a layer, [..., n, N] for a sequence of n; kept: Act8."""
-    idx, dev, dt = x.get_device(), x.device, x.dtype
+    idx, dt = x.get_device(), x.dtype
     _check(idx, x)
     ls = _layers(lins, idx)
     n, N, K = len(ls), ls[0].N, ls[0].K
     m = _rows(x, K, "x")
     code = _code(dt)
-    y = torch.empty(x.shape[:-1] + ((N,) if isinstance(lins, TLinear) else (n, N)), dtype=dt, device=dev)
-    kept = Act8._new(m, K, dev)
+    y = x.new_empty(x.shape[:-1] + ((N,) if isinstance(lins, TLinear) else (n, N)))
+    kept = Act8._new(m, K, x)
     lib = L.load()
-    wp, wn, _keep = _scratch(lib.mmf_bitlinear_train_ws_size(n, N, K, m), dev, ws)
-    with _on(idx):
-        L.check(lib.mmf_bitlinear_train(_c_layers(ls), n, x.data_ptr(), code, m, y.data_ptr(), eps,
-                                        _byref(kept._c(m, K, idx)), wp, wn, _stream(idx)), "mmf_bitlinear_train")
+    wp, wn, _keep = _scratch(lib.mmf_bitlinear_train_ws_size(n, N, K, m), x, ws)
+    _call(idx, "mmf_bitlinear_train", _c_layers(ls), n, x.data_ptr(), code, m, y.data_ptr(), eps,
+          _byref(kept._c(m, K, idx)), wp, wn)
     return y, kept
 
 
@@ -233,7 +234,7 @@ def bitlinear_backward(lins: Union[TLinear, Sequence[TLinear]], kept: Act8, dy: 
 
     x: the forward's input, for layers whose gain comes near 0 (otherwise read from the codes);
     dres: added to dx, e.g. the gradient that reaches x along a residual."""
-    idx, dev, dt = dy.get_device(), dy.device, dy.dtype
+    idx, dt = dy.get_device(), dy.dtype
     _check(idx, dy, x, dres)
     ls = _layers(lins, idx)
     n, N, K = len(ls), ls[0].N, ls[0].K
@@ -246,17 +247,16 @@ def bitlinear_backward(lins: Union[TLinear, Sequence[TLinear]], kept: Act8, dy: 
     code = _code(dt)
     _like(x, m * K, dt, "x")
     _like(dres, m * K, dt, "dres")
-    dx = torch.empty(dy.shape[:-1 if one else -2] + (K,), dtype=dt, device=dev)
-    dw = [torch.empty((N, K), dtype=dt, device=dev) for _ in ls]
-    dgain = None if ls[0].gain is None else torch.empty(K, dtype=dt, device=dev)
-    dbias = [None if lin.bias is None else torch.empty(N, dtype=dt, device=dev) for lin in ls]
+    new = dy.new_empty
+    dx = new(dy.shape[:-1 if one else -2] + (K,))
+    dw = [new((N, K)) for _ in ls]
+    dgain = None if ls[0].gain is None else new((K,))
+    dbias = [None if lin.bias is None else new((N,)) for lin in ls]
     cg = L.LinearGrads(dx.data_ptr(), _P3(*[t.data_ptr() for t in dw]), _p(dgain), _P3(*[_p(t) for t in dbias]))
     lib = L.load()
-    wp, wn, _keep = _scratch(lib.mmf_bitlinear_backward_ws_size(n, N, K, m, code), dev, ws)
-    with _on(idx):
-        L.check(lib.mmf_bitlinear_backward(_c_layers(ls), n, _byref(kept._c(m, K, idx)), _p(x), dy.data_ptr(),
-                                           _p(dres), code, m, _byref(cg), wp, wn, _stream(idx)),
-                "mmf_bitlinear_backward")
+    wp, wn, _keep = _scratch(lib.mmf_bitlinear_backward_ws_size(n, N, K, m, code), dy, ws)
+    _call(idx, "mmf_bitlinear_backward", _c_layers(ls), n, _byref(kept._c(m, K, idx)), _p(x), dy.data_ptr(),
+          _p(dres), code, m, _byref(cg), wp, wn)
     return LinearGrads(dx, dw, dgain, dbias)
 
 
@@ -265,21 +265,20 @@ def bitlinear_backward(lins: Union[TLinear, Sequence[TLinear]], kept: Act8, dy: 
 def glu_train(gate: TLinear, up: TLinear, down: TLinear, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
               eps: float = DEFAULT_EPS, ws: Optional[torch.Tensor] = None):
     """glu() that keeps the codes of x and of the product: (y, (kept_x, kept_p)) (mmf_glu_train)."""
-    idx, dev, dt = x.get_device(), x.device, x.dtype
+    idx, dt = x.get_device(), x.dtype
     _check(idx, x, residual)
     _on_device((gate, up, down), idx)
     d, inner = gate.K, gate.N
     m = _rows(x, d, "x")
     code = _code(dt)
     _like(residual, m * d, dt, "residual")
-    y = torch.empty_like(x)
-    kx, kp = Act8._new(m, d, dev), Act8._new(m, inner, dev)
+    y = x.new_empty(x.shape)
+    kx, kp = Act8._new(m, d, x), Act8._new(m, inner, x)
     lib = L.load()
-    wp, wn, _keep = _scratch(lib.mmf_glu_train_ws_size(m, d, inner, code), dev, ws)
-    with _on(idx):
-        L.check(lib.mmf_glu_train(_byref(gate.c()), _byref(up.c()), _byref(down.c()), x.data_ptr(), _p(residual),
-                                  y.data_ptr(), m, code, eps, _byref(kx._c(m, d, idx)), _byref(kp._c(m, inner, idx)),
-                                  wp, wn, _stream(idx)), "mmf_glu_train")
+    wp, wn, _keep = _scratch(lib.mmf_glu_train_ws_size(m, d, inner, code), x, ws)
+    _call(idx, "mmf_glu_train", _byref(gate.c()), _byref(up.c()), _byref(down.c()), x.data_ptr(), _p(residual),
+          y.data_ptr(), m, code, eps, _byref(kx._c(m, d, idx)), _byref(kp._c(m, inner, idx)),
+          wp, wn)
     return y, (kx, kp)
 
 
@@ -288,7 +287,7 @@ def glu_backward(gate: TLinear, up: TLinear, down: TLinear, kept, dy: torch.Tens
     """Gradients of glu_train for dy [..., d] (mmf_glu_backward); kept, x, dres as in bitlinear_backward.
 
     With residual=x in the forward, pass dres=dy."""
-    idx, dev, dt = dy.get_device(), dy.device, dy.dtype
+    idx, dt = dy.get_device(), dy.dtype
     _check(idx, dy, x, dres)
     ls = (gate, up, down)
     _on_device(ls, idx)
@@ -298,17 +297,17 @@ def glu_backward(gate: TLinear, up: TLinear, down: TLinear, kept, dy: torch.Tens
     _like(x, m * d, dt, "x")
     _like(dres, m * d, dt, "dres")
     kx, kp = kept
-    dx = torch.empty_like(dy)
-    dw = [torch.empty((lin.N, lin.K), dtype=dt, device=dev) for lin in ls]
-    dgain = [None if lin.gain is None else torch.empty(lin.K, dtype=dt, device=dev) for lin in (gate, down)]
-    dbias = [None if lin.bias is None else torch.empty(lin.N, dtype=dt, device=dev) for lin in ls]
+    new = dy.new_empty
+    dx = new(dy.shape)
+    dw = [new((lin.N, lin.K)) for lin in ls]
+    dgain = [None if lin.gain is None else new((lin.K,)) for lin in (gate, down)]
+    dbias = [None if lin.bias is None else new((lin.N,)) for lin in ls]
     cg = L.GluGrads(dx.data_ptr(), *[t.data_ptr() for t in dw], *[_p(t) for t in dgain], *[_p(t) for t in dbias])
     lib = L.load()
-    wp, wn, _keep = _scratch(lib.mmf_glu_backward_ws_size(m, d, inner, code), dev, ws)
-    with _on(idx):
-        L.check(lib.mmf_glu_backward(_byref(gate.c()), _byref(up.c()), _byref(down.c()), _byref(kx._c(m, d, idx)),
-                                     _byref(kp._c(m, inner, idx)), _p(x), dy.data_ptr(), _p(dres), code, m, _byref(cg),
-                                     wp, wn, _stream(idx)), "mmf_glu_backward")
+    wp, wn, _keep = _scratch(lib.mmf_glu_backward_ws_size(m, d, inner, code), dy, ws)
+    _call(idx, "mmf_glu_backward", _byref(gate.c()), _byref(up.c()), _byref(down.c()), _byref(kx._c(m, d, idx)),
+          _byref(kp._c(m, inner, idx)), _p(x), dy.data_ptr(), _p(dres), code, m, _byref(cg),
+          wp, wn)
     return GluGrads(dx, dw, dgain, dbias)
 
 
@@ -328,22 +327,20 @@ def head_loss(head: TLinear, x: torch.Tensor, labels: torch.Tensor, ignore_index
     """Softmax cross entropy of the logits head(x) against int32 labels, without storing the logits
     (mmf_head_loss): (loss, kept). loss is a float32 scalar ("mean" over the counted tokens, "sum") or the
     per-token losses in labels' shape ("none"); kept: HeadKept for head_loss_backward."""
-    idx, dev = x.get_device(), x.device
+    idx = x.get_device()
     _check(idx, x, labels)
     _on_device((head,), idx)
     N, K = head.N, head.K
     m = _rows(x, K, "x")
     red = _head_args(labels, m, reduction)
     code = _code(x.dtype)
-    loss = torch.empty(labels.shape if red == 0 else (), dtype=torch.float32, device=dev)
-    kept = HeadKept(m, K, x.dtype, dev)
+    loss = x.new_empty(labels.shape if red == 0 else (), dtype=torch.float32)
+    kept = HeadKept(m, K, x)
     lse, count = kept._ptrs()
     lib = L.load()
-    wp, wn, _keep = _scratch(lib.mmf_head_loss_ws_size(m, N, K), dev, ws)
-    with _on(idx):
-        L.check(lib.mmf_head_loss(_byref(head.c()), x.data_ptr(), code, m, labels.data_ptr(), ignore_index, red, eps,
-                                  loss.data_ptr(), _byref(kept.act._c(m, K, idx)), lse, count, wp, wn, _stream(idx)),
-                "mmf_head_loss")
+    wp, wn, _keep = _scratch(lib.mmf_head_loss_ws_size(m, N, K), x, ws)
+    _call(idx, "mmf_head_loss", _byref(head.c()), x.data_ptr(), code, m, labels.data_ptr(), ignore_index, red, eps,
+          loss.data_ptr(), _byref(kept.act._c(m, K, idx)), lse, count, wp, wn)
     return loss, kept
 
 
@@ -353,7 +350,7 @@ def head_loss_backward(head: TLinear, kept: HeadKept, labels: torch.Tensor, dlos
     """Gradients of head_loss for dloss (float32: one value, or one per token for "none"; None: 1), in the dtype
     of the forward's input (mmf_head_loss_backward); labels, ignore_index and reduction as there, x as in
     bitlinear_backward."""
-    idx, dev, dt = labels.get_device(), labels.device, kept.dtype
+    idx, dt = labels.get_device(), kept.dtype
     _check(idx, labels, dloss, x)
     _on_device((head,), idx)
     m, N, K = labels.numel(), head.N, head.K
@@ -362,15 +359,14 @@ def head_loss_backward(head: TLinear, kept: HeadKept, labels: torch.Tensor, dlos
     if dloss is not None and (dloss.dtype != torch.float32 or dloss.numel() != (m if red == 0 else 1)):
         raise ValueError("dloss must be float32, one value (one per token for reduction 'none')")
     _like(x, m * K, dt, "x")
-    dx = torch.empty(labels.shape + (K,), dtype=dt, device=dev)
-    dw = torch.empty((N, K), dtype=dt, device=dev)
-    dgain = None if head.gain is None else torch.empty(K, dtype=dt, device=dev)
-    dbias = None if head.bias is None else torch.empty(N, dtype=dt, device=dev)
+    dx = labels.new_empty(labels.shape + (K,), dtype=dt)
+    dw = dx.new_empty((N, K))
+    dgain = None if head.gain is None else dx.new_empty((K,))
+    dbias = None if head.bias is None else dx.new_empty((N,))
     cg = L.LinearGrads(dx.data_ptr(), _P3(dw.data_ptr()), _p(dgain), _P3(_p(dbias)))
     lse, count = kept._ptrs()
     lib = L.load()
-    wp, wn, _keep = _scratch(lib.mmf_head_loss_backward_ws_size(m, N, K, code), dev, ws)
-    with _on(idx):
-        L.check(lib.mmf_head_loss_backward(_byref(head.c()), _byref(kept.act._c(m, K, idx)), _p(x), labels.data_ptr(),
-                                           lse, count, _p(dloss), ignore_index, red, code, m, _byref(cg), wp, wn, _stream(idx)), "mmf_head_loss_backward")
+    wp, wn, _keep = _scratch(lib.mmf_head_loss_backward_ws_size(m, N, K, code), labels, ws)
+    _call(idx, "mmf_head_loss_backward", _byref(head.c()), _byref(kept.act._c(m, K, idx)), _p(x), labels.data_ptr(),
+          lse, count, _p(dloss), ignore_index, red, code, m, _byref(cg), wp, wn)
     return LinearGrads(dx, [dw], dgain, [dbias])

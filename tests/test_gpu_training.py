@@ -89,7 +89,8 @@ def through(l, kept):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("m,k,n,layers", [(1, 256, 256, 1), (5, 16, 3, 1), (130, 272, 777, 1), (257, 1024, 129, 2),
                                           (64, 512, 96, 3), (300, 80, 100, 3), (1537, 640, 320, 1),
-                                          (2049, 256, 512, 3)])
+                                          (2049, 256, 512, 3), (1003, 1040, 777, 1), (700, 1008, 501, 3),
+                                          (3000, 720, 712, 2)])
 @pytest.mark.parametrize("gain,bias,keep_x", [(False, False, False), (True, True, False), (True, False, True)])
 def test_bitlinear_train_and_backward(m, k, n, layers, dtype, gain, bias, keep_x):
     g, ls, x = make(m + k + n, m, k, n, dtype, gain, bias, layers)
@@ -191,7 +192,8 @@ def glu64(gate, up, down, kept, dy, x=None):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("m,d,inner", [(1, 256, 768), (7, 16, 16), (130, 272, 400), (513, 128, 1040), (1100, 320, 208)])
+@pytest.mark.parametrize("m,d,inner", [(1, 256, 768), (7, 16, 16), (130, 272, 400), (513, 128, 1040), (1100, 320, 208),
+                                       (1500, 272, 1200)])
 @pytest.mark.parametrize("gain,bias,keep_x", [(False, False, False), (True, True, False), (True, False, True)])
 def test_glu_train_and_backward(m, d, inner, dtype, gain, bias, keep_x):
     g = torch.Generator(device="cuda")
