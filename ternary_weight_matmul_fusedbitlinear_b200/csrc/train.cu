@@ -148,38 +148,47 @@ __device__ __forceinline__ void norm4(const NormBackArgs& a, size_t at, int k, f
   }
 }
 
-// Rows of one slice, read through the codes, without a gain (most calls): every
-// load of the row is issued before the first is used, with no branch between
-// them (a loop over slices there made them wait for one another: 112 us for
-// 16384 x 2816, 6 us a load), and kept in registers. WPR warps per row of at
-// most WPR * 128 * NV columns.
-template <typename T, int WPR, int NV, bool STAT, bool RES>
-__global__ void __launch_bounds__(kThreads) norm_back_plain_kernel(const NormBackArgs a) {
-  __shared__ float red[kThreads / 32];
+// Rows of one slice (most calls): every load of the row is issued before the
+// first is used, with no branch between them (a loop over slices there made them
+// wait for one another: 112 us for 16384 x 2816), and kept in registers. WPR
+// warps per row of at most WPR * 128 * NV columns; 16 columns a thread keep four
+// blocks on an SM, whose phases overlap (56 us, 5.8 TB/s; 32 columns: 76 us).
+// N: 0 no gain, the norm read through the codes; 1 with a gain; 2 from x.
+template <int WPR>
+constexpr int row_threads() { return WPR > 8 ? 32 * WPR : kThreads; }
+
+template <typename T, int WPR, int NV, bool STAT, bool RES, int N>
+__global__ void __launch_bounds__(row_threads<WPR>()) norm_back_plain_kernel(const NormBackArgs a) {
+  constexpr int kWarps = row_threads<WPR>() / 32, kRows = kWarps / WPR, kLanes = 32 * WPR;
+  __shared__ float red[kWarps];
   pdl_trigger();
   pdl_wait();
-  constexpr int kRows = kThreads / 32 / WPR, kLanes = 32 * WPR;
   const int lane = threadIdx.x % kLanes, warp = threadIdx.x >> 5;
   const int row = min(blockIdx.x * kRows + (int)threadIdx.x / kLanes, a.M - 1);   // a tail repeats the last row
   const size_t base = (size_t)row * a.K;
-  float v[NV][4], d[RES ? NV : 1][4];
+  float v[NV][4], d[RES ? NV : 1][4], x[N == 2 ? NV : 1][4];
   int w[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int k = (i * kLanes + lane) * 4;
     const size_t at = base + (k < a.K ? k : 0);
     ld4(a.dxh + at, v[i]);
-    w[i] = *reinterpret_cast<const int*>(a.q + at);
+    if constexpr (N == 2) ld4(static_cast<const T*>(a.x) + at, x[i]);
+    else w[i] = *reinterpret_cast<const int*>(a.q + at);
     if constexpr (RES) ld4(static_cast<const T*>(a.dres) + at, d[i]);
   }
   const float inv_s = 1.0f / a.scale[row], rinv = a.rinv[row];
+  // N < 2: x^ = q / s, mean over q; N = 2: n = x rinv, x^ = n gain, mean over x gain
   float dot = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    float part = 0.0f;
+    const int k = (i * kLanes + lane) * 4;
+    float part = 0.0f, g[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+    if (N == 2 && a.gain != nullptr) ld4(a.gain + (k < a.K ? k : 0), g);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) part = fmaf(v[i][j], (float)((w[i] << (24 - 8 * j)) >> 24), part);
-    dot += (i * kLanes + lane) * 4 < a.K ? part : 0.0f;
+    for (int j = 0; j < 4; ++j)
+      part = fmaf(v[i][j], N == 2 ? x[i][j] * g[j] : (float)((w[i] << (24 - 8 * j)) >> 24), part);
+    dot += k < a.K ? part : 0.0f;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
@@ -189,18 +198,21 @@ __global__ void __launch_bounds__(kThreads) norm_back_plain_kernel(const NormBac
     dot = 0.0f;
     for (int i = 0; i < WPR; ++i) dot += red[warp / WPR * WPR + i];
   }
-  const float c = dot * inv_s / (float)a.K;
+  const float unit = N == 2 ? rinv : inv_s, c = dot * unit / (float)a.K;
   if constexpr (STAT) {
     if (lane == 0) a.cmean[row] = c;
   } else {
-    const float ci = c * inv_s;
+    const float ci = c * unit;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int k = (i * kLanes + lane) * 4;
-      float o[4];
+      float o[4], g[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+      if (N == 1 || (N == 2 && a.gain != nullptr)) ld4(a.gain + (k < a.K ? k : 0), g);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        o[j] = rinv * fmaf(-ci, (float)((w[i] << (24 - 8 * j)) >> 24), v[i][j]);
+        float n = N == 2 ? x[i][j] : (float)((w[i] << (24 - 8 * j)) >> 24);
+        if (N == 1) n = g[j] != 0.0f ? n / g[j] : 0.0f;   // a column whose gain is 0 left nothing in the codes
+        o[j] = rinv * fmaf(-ci, n, N == 0 ? v[i][j] : g[j] * v[i][j]);
         if constexpr (RES) o[j] += d[i][j];
       }
       if (k < a.K) st4(static_cast<T*>(a.dx) + base + k, o);
@@ -208,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) norm_back_plain_kernel(const NormBac
   }
 }
 
-// Any other row: slices, gain, x. WPR warps per row, WPR * 128 * NV columns at
+// Any other row (slices, or very long). WPR warps per row, WPR * 128 * NV columns at
 // most; the row's dx^ stays in registers between the mean and the result (its
 // codes are read again from L1). NV = 0: rows of any length, read twice.
 template <typename T, int WPR, int NV, bool STAT>
@@ -662,27 +674,32 @@ cudaError_t launch_train_prep(const PrepArgs* const* sets, int n, cudaStream_t s
                         : launch_pdl(train_prep_kernel<float>, grid, dim3(kThreads), 0, stream, list);
 }
 
+template <typename T, int WPR, int NV, bool STAT, int N>
+static cudaError_t plain_rows_n(const NormBackArgs& a, cudaStream_t stream) {
+  constexpr int kBlock = row_threads<WPR>();
+  const dim3 grid(ceil_div(a.M, kBlock / 32 / WPR)), block(kBlock);
+  if (!STAT && a.dres != nullptr)
+    return launch_pdl(norm_back_plain_kernel<T, WPR, NV, false, true, N>, grid, block, 0, stream, a);
+  return launch_pdl(norm_back_plain_kernel<T, WPR, NV, STAT, false, N>, grid, block, 0, stream, a);
+}
 template <typename T, int WPR, int NV, bool STAT>
 static cudaError_t plain_rows(const NormBackArgs& a, cudaStream_t stream) {
-  const dim3 grid(ceil_div(a.M, 8 / WPR)), block(kThreads);
-  if (!STAT && a.dres != nullptr)
-    return launch_pdl(norm_back_plain_kernel<T, WPR, NV, false, true>, grid, block, 0, stream, a);
-  return launch_pdl(norm_back_plain_kernel<T, WPR, NV, STAT, false>, grid, block, 0, stream, a);
+  if (STAT || (a.gain == nullptr && a.x == nullptr)) return plain_rows_n<T, WPR, NV, STAT, 0>(a, stream);
+  return a.x != nullptr ? plain_rows_n<T, WPR, NV, false, 2>(a, stream) : plain_rows_n<T, WPR, NV, false, 1>(a, stream);
 }
 
 template <typename T, bool STAT>
 static cudaError_t norm_back_typed(const NormBackArgs& a, cudaStream_t stream) {
-  const dim3 block(kThreads);
-  if (a.slices == 1 && a.gain == nullptr && a.x == nullptr && a.K <= 8 * 1024) {
-    // as few warps per row as hold it at 32 columns a thread; 8 when rows are few
+  if (a.slices == 1 && a.K <= 8 * 1024) {   // as few warps per row as hold it at 16 columns a thread; 8 when rows are few
     const bool few = a.M < num_sms() * 8;
-    if (!few && a.K <= 1024) return plain_rows<T, 1, 8, STAT>(a, stream);
-    if (!few && a.K <= 2 * 1024) return plain_rows<T, 2, 8, STAT>(a, stream);
-    if (!few && a.K <= 4 * 1024) return plain_rows<T, 4, 8, STAT>(a, stream);
+    if (!few && a.K <= 512) return plain_rows<T, 1, 4, STAT>(a, stream);
+    if (!few && a.K <= 1024) return plain_rows<T, 2, 4, STAT>(a, stream);
+    if (!few && a.K <= 2 * 1024) return plain_rows<T, 4, 4, STAT>(a, stream);
     if (a.K <= 2 * 1024) return plain_rows<T, 8, 2, STAT>(a, stream);
-    return plain_rows<T, 8, 8, STAT>(a, stream);
+    if (a.K <= 4 * 1024) return plain_rows<T, 8, 4, STAT>(a, stream);
+    return plain_rows<T, 16, 4, STAT>(a, stream);
   }
-  const dim3 grid(a.M);
+  const dim3 grid(a.M), block(kThreads);
   if (a.K <= 2 * 1024) return launch_pdl(norm_back_kernel<T, 8, 2, STAT>, grid, block, 0, stream, a);
   if (a.K <= 8 * 1024) return launch_pdl(norm_back_kernel<T, 8, 8, STAT>, grid, block, 0, stream, a);
   return launch_pdl(norm_back_kernel<T, 8, 0, STAT>, grid, block, 0, stream, a);

@@ -90,7 +90,8 @@ def through(l, kept):
 @pytest.mark.parametrize("m,k,n,layers", [(1, 256, 256, 1), (5, 16, 3, 1), (130, 272, 777, 1), (257, 1024, 129, 2),
                                           (64, 512, 96, 3), (300, 80, 100, 3), (1537, 640, 320, 1),
                                           (2049, 256, 512, 3), (1003, 1040, 777, 1), (700, 1008, 501, 3),
-                                          (3000, 720, 712, 2)])
+                                          (3000, 720, 712, 2), (1300, 2064, 64, 1), (1300, 6912, 48, 1),
+                                          (40, 9216, 32, 1), (1250, 400, 80, 1)])
 @pytest.mark.parametrize("gain,bias,keep_x", [(False, False, False), (True, True, False), (True, False, True)])
 def test_bitlinear_train_and_backward(m, k, n, layers, dtype, gain, bias, keep_x):
     g, ls, x = make(m + k + n, m, k, n, dtype, gain, bias, layers)
