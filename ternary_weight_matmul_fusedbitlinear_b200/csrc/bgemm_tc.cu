@@ -295,11 +295,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     t.dw = MODE == 2 ? tile >= p.tiles0 : MODE == 1;
     const Prob& q = p.pr[t.dw];
     const int id = MODE == 2 && t.dw ? tile - p.tiles0 : tile;
-    t.jt = id % q.j_tiles;
-    t.it = id / q.j_tiles % q.i_tiles;
-    t.sp = id / (q.j_tiles * q.i_tiles);
-    t.lo = (int)((long long)q.units * t.sp / q.g.splits);
-    t.hi = (int)((long long)q.units * (t.sp + 1) / q.g.splits);
+    // one division in the usual case: between tiles the MMA thread's own
+    // arithmetic is time the tensor cores lose
+    const unsigned row = (unsigned)id / (unsigned)q.j_tiles;
+    t.jt = id - (int)row * q.j_tiles;
+    t.it = (int)row;
+    t.sp = 0;
+    t.lo = 0;
+    t.hi = q.units;
+    if (q.g.splits > 1) {
+      t.sp = (int)(row / (unsigned)q.i_tiles);
+      t.it = (int)row - t.sp * q.i_tiles;
+      t.lo = (int)((long long)q.units * t.sp / q.g.splits);
+      t.hi = (int)((long long)q.units * (t.sp + 1) / q.g.splits);
+    }
     t.chain = KIND == 2 || (KIND == 1 && !t.dw);
     t.slot = -1;
     return t;
