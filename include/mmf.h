@@ -294,7 +294,13 @@ mmf_status mmf_glu(const mmf_tlinear* gate, const mmf_tlinear* up, const mmf_tli
 /* Training: BitLinear and GLU with activations kept in 8 bits                */
 /* ------------------------------------------------------------------------- */
 
-/* What a layer's forward keeps of its input x [M, K] for the backward: the
+/* For every call of this and the next section: outputs must not overlap inputs
+ * (but dres may be the dx it is added to); the first call on a device makes the
+ * status word that mmf_check reads, so make it outside stream capture; labels,
+ * losses, lse, count and dloss need the alignment of their type only. Results
+ * depend on the inputs and sizes alone, not on the run.
+ *
+ * What a layer's forward keeps of its input x [M, K] for the backward: the
  * int8 codes that the forward contraction reads anyway, 1 byte per element and
  * 16 per row (a bf16 copy of x would be 2 bytes per element, of x^ 2 more).
  * All device memory owned by the caller, 16-byte aligned.

@@ -32,6 +32,7 @@
 // kernel records an error in the status word, raises a CTA-wide abort flag,
 // and all roles leave their loops; nothing traps.
 #include "kernels.cuh"
+#include <cfloat>
 #include <cstddef>
 #include <type_traits>
 
@@ -156,9 +157,14 @@ __device__ __forceinline__ void logits32(const uint32_t (&r)[32], int qs, float 
                                          int n0, int N, float (&z)[32]) {
   scaled(r, qs, sc2, magic, z);
   if (bias != nullptr) {
+    // a finite bias gives a finite logit, also where log2(e) would take it past
+    // the type (a mask of the type's lowest value)
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (n0 + j < N) z[j] = fmaf(__ldg(bias + n0 + j), kLog2e, z[j]);
+      if (n0 + j < N) {
+        const float b = __ldg(bias + n0 + j), t = fmaf(b, kLog2e, z[j]);
+        z[j] = fabsf(b) < INFINITY ? fminf(fmaxf(t, -FLT_MAX), FLT_MAX) : t;
+      }
   }
   if (n0 + 32 > N) {
 #pragma unroll

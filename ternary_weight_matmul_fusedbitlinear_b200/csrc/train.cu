@@ -557,11 +557,11 @@ __device__ __forceinline__ float loss_rows(const LossArgs& a, int m, int r, int 
   float loss = 0.0f;
   if (g == 0 && m < a.M) {
     for (int i = 1; i < kJoinGroups; ++i) fold(red[i][r]);
-    const float lse2 = mx + log2f(sum);
+    const float ls = log2f(sum);
     const int l = a.labels[m];
-    if (counted_label(a, l)) loss = (lse2 - a.zlabel[m]) * kLn2;
+    if (counted_label(a, l)) loss = ((mx - a.zlabel[m]) + ls) * kLn2;
     else if (l != a.ignore_index && status != nullptr) atomicExch(status, 9);   // reported by mmf_check
-    a.lse[m] = lse2 * kLn2;
+    a.lse[m] = (mx + ls) * kLn2;
     a.token[m] = loss;
   }
   __syncthreads();

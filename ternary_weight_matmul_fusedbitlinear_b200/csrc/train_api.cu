@@ -34,6 +34,11 @@ mmf_status check_common(const char* what, mmf_dtype dt, int M) {
   return MMF_OK;
 }
 
+mmf_status check_size(const char* what, long long n, int k) {
+  if (n > (1 << 28) || k > (1 << 20)) return fail(MMF_ERR_UNSUPPORTED_SHAPE, "%s: %lld x %d is too large", what, n, k);
+  return MMF_OK;
+}
+
 // Layers of one input: same shape, same gain.
 mmf_status check_lins(const mmf_tlinear* lins, int n, const char* what) {
   if (lins == nullptr || n < 1 || n > 3) return fail(MMF_ERR_INVALID_ARG, "%s: %d layers (1 to 3)", what, n);
@@ -45,9 +50,7 @@ mmf_status check_lins(const mmf_tlinear* lins, int n, const char* what) {
     if (lins[i].gain != lins[0].gain)
       return fail(MMF_ERR_UNSUPPORTED_SHAPE, "%s: layers of one input must share one gain", what);
   }
-  if ((long long)n * lins[0].N > (1 << 28) || lins[0].K > (1 << 20))
-    return fail(MMF_ERR_UNSUPPORTED_SHAPE, "%s: %d x %d is too large", what, lins[0].N, lins[0].K);
-  return MMF_OK;
+  return check_size(what, (long long)n * lins[0].N, lins[0].K);
 }
 
 mmf_status check_ptrs(const char* what, std::initializer_list<const void*> needed,
@@ -58,6 +61,17 @@ mmf_status check_ptrs(const char* what, std::initializer_list<const void*> neede
     if (!aligned16(p)) return fail(MMF_ERR_MISALIGNED, "%s: pointer not 16-byte aligned", what);
   for (const void* p : optional)
     if (p != nullptr && !aligned16(p)) return fail(MMF_ERR_MISALIGNED, "%s: pointer not 16-byte aligned", what);
+  return MMF_OK;
+}
+
+// Vectors of 4-byte values that are read one by one: labels, losses and their gradients.
+mmf_status check_words(const char* what, std::initializer_list<const void*> needed,
+                       std::initializer_list<const void*> optional) {
+  for (const void* p : needed)
+    if (p == nullptr) return fail(MMF_ERR_INVALID_ARG, "%s: null pointer", what);
+  for (auto list : {needed, optional})
+    for (const void* p : list)
+      if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return fail(MMF_ERR_MISALIGNED, "%s: pointer not 4-byte aligned", what);
   return MMF_OK;
 }
 
@@ -508,6 +522,7 @@ extern "C" mmf_status mmf_glu_train(const mmf_tlinear* gate, const mmf_tlinear* 
   if (!gate) return fail(MMF_ERR_INVALID_ARG, "%s: null gate", what);
   const int d = gate->K, I = gate->N;
   mmf_status r = check_glu(gate, up, down, d);
+  if (r == MMF_OK) r = check_size(what, 2LL * I, std::max(d, I));
   if (r == MMF_OK) r = check_common(what, dtype, M);
   if (r != MMF_OK) return r;
   if (!(eps > 0.0f)) return fail(MMF_ERR_INVALID_ARG, "%s: eps must be > 0", what);
@@ -608,6 +623,7 @@ extern "C" mmf_status mmf_glu_backward(const mmf_tlinear* gate, const mmf_tlinea
   if (!gate) return fail(MMF_ERR_INVALID_ARG, "%s: null gate", what);
   const int d = gate->K, I = gate->N;
   mmf_status r = check_glu(gate, up, down, d);
+  if (r == MMF_OK) r = check_size(what, 2LL * I, std::max(d, I));
   if (r == MMF_OK) r = check_common(what, dtype, M);
   if (r != MMF_OK) return r;
   if (grads == nullptr) return fail(MMF_ERR_INVALID_ARG, "%s: null gradients", what);
@@ -795,9 +811,10 @@ extern "C" mmf_status mmf_head_loss(const mmf_tlinear* head, const void* x, mmf_
   if (!(eps > 0.0f)) return fail(MMF_ERR_INVALID_ARG, "%s: eps must be > 0", what);
   const bool reduce = reduction != MMF_REDUCE_NONE;
   cudaStream_t s = as_stream(stream);
-  if (reduce && (r = check_ptrs(what, {loss, count}, {})) != MMF_OK) return r;
+  if (reduce && (r = check_words(what, {loss, count}, {})) != MMF_OK) return r;
   if (M == 0) return reduce ? zero(loss, sizeof(float), s) : MMF_OK;
-  if ((r = check_ptrs(what, {x, labels, loss, lse, ws}, {})) != MMF_OK || (r = check_kept(kept, what)) != MMF_OK)
+  if ((r = check_ptrs(what, {x, ws}, {})) != MMF_OK || (r = check_words(what, {labels, loss, lse}, {})) != MMF_OK ||
+      (r = check_kept(kept, what)) != MMF_OK)
     return r;
   const int V = head->N, K = head->K;
   const size_t need = mmf_head_loss_ws_size(M, V, K);
@@ -858,7 +875,8 @@ extern "C" mmf_status mmf_head_loss_backward(const mmf_tlinear* head, const mmf_
   const int V = head->N, K = head->K;
   cudaStream_t s = as_stream(stream);
   if (M == 0) return zero_grads(*grads, 1, V, K, dtype, s);
-  if ((r = check_ptrs(what, {labels, lse, ws}, {x, dloss})) != MMF_OK || (r = check_kept(kept, what)) != MMF_OK)
+  if ((r = check_ptrs(what, {ws}, {x})) != MMF_OK || (r = check_words(what, {labels, lse}, {dloss, count})) != MMF_OK ||
+      (r = check_kept(kept, what)) != MMF_OK)
     return r;
   if (reduction == MMF_REDUCE_MEAN && count == nullptr) return fail(MMF_ERR_INVALID_ARG, "%s: null count", what);
   Carver c(ws);

@@ -161,3 +161,45 @@ def test_scan_backward_validation(lib):
     assert lib.mmf_mlgru_scan_backward(p, 0, 2, 3, 12, p, p, None, p, p, q, None, 0, None) == 2          # d % 8 still
     assert lib.mmf_mlgru_scan_states(p, 0, 2, 3, 16, p, None, None, None) == 1                          # null hs
     assert lib.mmf_mlgru_scan_states(p, 0, 2, 3, 16, p, ctypes.c_void_p(4100), p, None) == 3            # misaligned o
+
+
+def test_training_validation(lib):
+    p = ctypes.c_void_p(4096)
+    k = L.Act8(4096, 4096, 4096, 4096)
+    kr = ctypes.byref(k)
+    one = (L.TLinear * 1)(_tl(64, 32))
+    g = L.LinearGrads()
+    gr = ctypes.byref(g)
+    train = lambda lins, n, x, dt, m, y, eps, kept, ws, wb: lib.mmf_bitlinear_train(lins, n, x, dt, m, y, eps, kept,
+                                                                                   ws, wb, None)
+    assert train(one, 0, p, 0, 4, p, 1e-6, kr, None, 0) == 1
+    assert train(one, 4, p, 0, 4, p, 1e-6, kr, None, 0) == 1
+    assert train(None, 1, p, 0, 4, p, 1e-6, kr, None, 0) == 1
+    assert train((L.TLinear * 1)(_tl(64, 24)), 1, p, 0, 4, p, 1e-6, kr, None, 0) == 2
+    assert train((L.TLinear * 2)(_tl(64, 32), _tl(32, 32)), 2, p, 0, 4, p, 1e-6, kr, None, 0) == 2
+    assert train((L.TLinear * 2)(_tl(64, 32), L.TLinear(16, 16, 32, None, 64, 32)), 2, p, 0, 4, p, 1e-6, kr, None, 0) == 2
+    assert b"share one gain" in lib.mmf_last_error()
+    # an empty batch does nothing, whatever the rest (on a machine without a driver it may say that it cannot work)
+    assert train(one, 1, None, 0, 0, None, 1e-6, None, None, 0) in (0, 5)
+    assert train(one, 1, p, 9, 4, p, 1e-6, kr, None, 0) == 1
+    assert train(one, 1, p, 0, -1, p, 1e-6, kr, None, 0) == 1
+    for fn, args in ((lib.mmf_bitlinear_backward, (one, 1, kr, None, p, None, 9, 4, gr, p, 0, None)),
+                     (lib.mmf_head_loss, (one, p, 9, 4, p, -100, 2, 1e-6, p, kr, p, p, p, 0, None)),
+                     (lib.mmf_head_loss_backward, (one, kr, None, p, p, p, None, -100, 2, 9, 4, gr, p, 0, None))):
+        assert fn(*args) == 1
+    gate, up, down = _tl(64, 32), _tl(64, 32), _tl(32, 64)
+    gg = L.GluGrads()
+    assert lib.mmf_glu_backward(ctypes.byref(gate), ctypes.byref(_tl(48, 32)), ctypes.byref(down), kr, kr, None, p, None,
+                                0, 4, ctypes.byref(gg), p, 0, None) == 2
+    assert lib.mmf_glu_train(None, ctypes.byref(up), ctypes.byref(down), p, None, p, 4, 0, 1e-6, kr, kr, p, 0, None) == 1
+
+
+def test_training_workspace_sizes(lib):
+    assert lib.mmf_bitlinear_train_ws_size(1, 256, 256, 4) == 0
+    assert lib.mmf_bitlinear_train_ws_size(3, 1024, 1024, 4096) >= 3 * 1024 * 1024
+    assert lib.mmf_bitlinear_backward_ws_size(1, 64, 64, 8, 1) < lib.mmf_bitlinear_backward_ws_size(1, 1024, 1024, 4096, 1)
+    assert lib.mmf_bitlinear_backward_ws_size(4, 64, 64, 8, 1) == 0
+    assert lib.mmf_glu_backward_ws_size(4096, 1024, 2816, 1) > 4096 * 2816 * 4
+    # the logits' gradient is held in pieces: far below M x V values
+    assert lib.mmf_head_loss_backward_ws_size(65536, 64000, 1024, 1) < 65536 * 64000
+    assert lib.mmf_head_loss_ws_size(65536, 32000, 1024) < 65536 * 32000

@@ -180,6 +180,31 @@ def test_gradient_of_the_input_against_differences():
     assert rel(dx, want) <= TOL["f32"]
 
 
+# Products of several rounds of tiles: pairs of SMs, splits, even shares of the last
+# round, layers summed in registers over more than one unit, widths that are not
+# multiples of 64, fp32 planes. 512 blocks of 16 terms at most for fp32: 2^-14.
+@pytest.mark.parametrize("m,k,n,layers,dtype", [
+    (4096, 2560, 13824, 1, "bf16"), (16384, 2816, 1024, 1, "bf16"), (16384, 272, 1024, 1, "bf16"),
+    (5000, 2000, 3001, 1, "bf16"), (3000, 1040, 2304, 3, "bf16"), (9000, 512, 2560, 2, "bf16"),
+    (4096, 2560, 4096, 1, "f32"), (2500, 1040, 1100, 2, "f32")])
+def test_large_products(m, k, n, layers, dtype):
+    g, ls, x = make(m + n, m, k, n, dtype, layers=layers)
+    lins = [l.lin for l in ls]
+    _, kept = mmf.bitlinear_train(lins, x)
+    dy = torch.randn(m, layers, n, generator=g, device="cuda").to(DT[dtype])
+    got = mmf.bitlinear_backward(lins, kept, dy)
+    dx, dws, _, _ = back64(ls, kept, [dy[:, i].double() for i in range(layers)])
+    tol = TOL["bf16"] if dtype == "bf16" else 2.0 ** -14
+    for a, b in zip([got.dx, *got.dw], [dx, *dws]):
+        assert torch.isfinite(a).all() and rel(a, b) <= tol
+    rows = torch.tensor([0, m // 2, m - 1], device="cuda")   # and row by row at the ends and in the middle
+    for r in rows:
+        assert rel(got.dx[r], dx[r]) <= 2 * tol
+    again = mmf.bitlinear_backward(lins, kept, dy)
+    assert torch.equal(got.dx, again.dx) and all(torch.equal(a, b) for a, b in zip(got.dw, again.dw))
+    mmf.check()
+
+
 # ---------------------------------------------------------------- GLU
 
 def glu64(gate, up, down, kept, dy, x=None):
@@ -222,6 +247,25 @@ def test_glu_train_and_backward(m, d, inner, dtype, gain, bias, keep_x):
     if gain:
         near(got.dgain[0], dgs[0], dtype, "dgain")
         near(got.dgain[1], dgs[1], dtype, "dgain down")
+    mmf.check()
+
+
+@pytest.mark.parametrize("m,d,inner", [(4096, 8192, 2560), (8192, 1024, 2816)])
+def test_large_glu(m, d, inner):
+    """The down projection's norm means from the product's own epilogue, whole tiles and shared ones."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m)
+    gate, up, down = Layer(g, inner, d), Layer(g, inner, d), Layer(g, d, inner)
+    x = torch.randn(m, d, generator=g, device="cuda").bfloat16()
+    y, kept = mmf.glu_train(gate.lin, up.lin, down.lin, x)
+    near(y, through(down, kept[1]), "bf16", "y")
+    dy = torch.randn(m, d, generator=g, device="cuda").bfloat16()
+    got = mmf.glu_backward(gate.lin, up.lin, down.lin, kept, dy)
+    dx, dws, _, _ = glu64(gate, up, down, kept, dy)
+    for a, b in zip([got.dx, *got.dw], [dx, *dws]):
+        near(a, b, "bf16", "gradient")
+    again = mmf.glu_backward(gate.lin, up.lin, down.lin, kept, dy)
+    assert torch.equal(got.dx, again.dx) and all(torch.equal(a, b) for a, b in zip(got.dw, again.dw))
     mmf.check()
 
 
@@ -286,6 +330,11 @@ def test_masked_vocabulary_entries_and_ignored_batches(dtype):
     near(got.dw[0], dws[0], dtype, "dw")
     near(got.dbias[0], dbias[0], dtype, "dbias")
     assert torch.count_nonzero(got.dw[0][7::11]) == 0
+    head.bias.fill_(torch.finfo(torch.float32).min)   # a mask that leaves nothing: every entry alike
+    loss, kept = mmf.head_loss(head.lin, x, labels)
+    got = mmf.head_loss_backward(head.lin, kept, labels)
+    assert abs(float(loss) - np.log(300.0)) <= 2.0 ** -16
+    assert torch.isfinite(got.dx).all() and torch.isfinite(got.dw[0]).all()
     labels.fill_(-100)
     for how in ("mean", "sum", "none"):
         loss, kept = mmf.head_loss(head.lin, x, labels, reduction=how)
@@ -309,9 +358,9 @@ def test_labels_outside_the_vocabulary_are_left_out_and_reported():
     mmf.check()
 
 
-def test_vocabulary_in_pieces():
+@pytest.mark.parametrize("m,k,V", [(8200, 64, 20011), (8192, 2048, 32000)])
+def test_vocabulary_in_pieces(m, k, V):
     """More gradient of the logits than is held at once: several pieces, the last one shorter and odd."""
-    m, k, V = 8200, 64, 20011
     g, (head,), x = make(8, m, k, V, "bf16", bias=True, std=0.2)
     labels = torch.randint(0, V, (m,), generator=g, device="cuda", dtype=torch.int32)
     loss, kept = mmf.head_loss(head.lin, x, labels)
@@ -322,6 +371,19 @@ def test_vocabulary_in_pieces():
     near(got.dx, dx, "bf16", "dx")
     near(got.dw[0], dws[0], "bf16", "dw")
     near(got.dbias[0], dbias[0], "bf16", "dbias")
+
+
+def test_labels_and_losses_at_any_word():
+    """Labels, per-token gradients and losses are plain vectors: a slice that starts anywhere will do."""
+    g, (head,), x = make(9, 33, 64, 70, "bf16", std=0.2)
+    labels = torch.randint(0, 70, (34,), generator=g, device="cuda", dtype=torch.int32)
+    dl = torch.rand(34, generator=g, device="cuda")
+    a, ka = mmf.head_loss(head.lin, x, labels[1:], reduction="none")
+    b, kb = mmf.head_loss(head.lin, x, labels[1:].clone(), reduction="none")
+    assert torch.equal(a, b)
+    ga = mmf.head_loss_backward(head.lin, ka, labels[1:], dl[1:], reduction="none")
+    gb = mmf.head_loss_backward(head.lin, kb, labels[1:].clone(), dl[1:].clone(), reduction="none")
+    assert torch.equal(ga.dx, gb.dx) and torch.equal(ga.dw[0], gb.dw[0])
 
 
 # ---------------------------------------------------------------- use
@@ -416,4 +478,68 @@ def test_training_step_captured_and_on_another_stream():
         l2, g2, _ = _step(p, ids2, lab2)
     side.synchronize()
     assert torch.equal(l2, loss) and all(torch.equal(g2[n], grads[n]) for n in grads)
+    mmf.check()
+
+
+@pytest.mark.parametrize("m", [40, 2500])
+def test_any_subset_of_the_gradients(m):
+    """Outputs left out through the C ABI change nothing about the others, nor what lies behind them."""
+    import ctypes
+    from ternary_weight_matmul_fusedbitlinear_b200 import _lib as L
+    lib = L.load()
+    g, ls, x = make(13, m, 256, 320, "bf16", True, True, layers=3)
+    lins = [l.lin for l in ls]
+    _, kept = mmf.bitlinear_train(lins, x)
+    dy = torch.randn(m, 3, 320, generator=g, device="cuda").bfloat16()
+    full = mmf.bitlinear_backward(lins, kept, dy)
+    want = [full.dx, *full.dw, full.dgain, *full.dbias]
+    cl = (L.TLinear * 3)(*[l.c() for l in lins])
+    ck = L.Act8(*[t.data_ptr() for t in (kept.q, kept.scale, kept.qsum, kept.rinv)])
+    nbytes = lib.mmf_bitlinear_backward_ws_size(3, 320, 256, m, L.MMF_BF16)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    for mask in (0b00000001, 0b00000010, 0b00000100, 0b00001010, 0b00010000, 0b01000001, 0b11110000, 0b10001000, 0):
+        outs = [torch.full((w.numel() + 64,), 7.0, dtype=w.dtype, device="cuda") for w in want]
+        p = [o.data_ptr() if mask >> i & 1 else None for i, o in enumerate(outs)]
+        cg = L.LinearGrads(p[0], (L.c_vp * 3)(*p[1:4]), p[4], (L.c_vp * 3)(*p[5:8]))
+        st = lib.mmf_bitlinear_backward(cl, 3, ctypes.byref(ck), None, dy.data_ptr(), None, L.MMF_BF16, m,
+                                        ctypes.byref(cg), ws.data_ptr(), nbytes,
+                                        torch.cuda.current_stream().cuda_stream)
+        L.check(st, "mmf_bitlinear_backward")
+        for i, (o, w) in enumerate(zip(outs, want)):
+            n = w.numel()
+            if mask >> i & 1:
+                assert torch.equal(o[:n], w.reshape(-1)), (mask, i)
+                assert bool((o[n:] == 7).all())
+            else:
+                assert bool((o == 7).all())
+    mmf.check()
+
+
+def test_refusals():
+    g, (l,), x = make(2, 8, 64, 48, "bf16", gain=True)
+    lin = l.lin
+    y, kept = mmf.bitlinear_train(lin, x)
+    other = mmf.quantize_weights(torch.randn(48, 80, device="cuda"))
+    for bad in (lambda: mmf.bitlinear_train(lin, x.cpu()), lambda: mmf.bitlinear_train(lin, x.half()),
+                lambda: mmf.bitlinear_train(lin, x[:, :32]), lambda: mmf.bitlinear_train(lin, x.t()),
+                lambda: mmf.bitlinear_train([lin] * 4, x), lambda: mmf.bitlinear_train([], x),
+                lambda: mmf.bitlinear_backward(lin, kept, y[:4]), lambda: mmf.bitlinear_backward([lin, lin], kept, y),
+                lambda: mmf.bitlinear_backward(lin, kept, y, x=x.float()),
+                lambda: mmf.bitlinear_backward(lin, kept, y, dres=x[:4]),
+                lambda: mmf.bitlinear_backward(lin, kept, y, ws=torch.empty(16, dtype=torch.uint8, device="cuda")),
+                lambda: mmf.Act8(kept.q.float(), kept.scale, kept.qsum, kept.rinv),
+                lambda: mmf.Act8(kept.q, kept.scale[:4], kept.qsum, kept.rinv),
+                lambda: mmf.head_loss(lin, x, torch.zeros(8, dtype=torch.int64, device="cuda")),
+                lambda: mmf.head_loss(lin, x, torch.zeros(7, dtype=torch.int32, device="cuda")),
+                lambda: mmf.head_loss(lin, x, torch.zeros(8, dtype=torch.int32, device="cuda"), reduction="max")):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(mmf.MMFError, match="share one gain"):
+        mmf.bitlinear_train([lin, mmf.TLinear(lin.packed, lin.gamma, 48, 64)], x)
+    with pytest.raises(mmf.MMFError, match="one shape"):
+        mmf.bitlinear_train([lin, other], x)
+    with pytest.raises(mmf.MMFError):
+        mmf.glu_train(lin, lin, lin, x)
+    with pytest.raises(mmf.MMFError, match="eps"):
+        mmf.bitlinear_train(lin, x, eps=0.0)
     mmf.check()
