@@ -638,7 +638,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         release_acc();
       }
     }
-    if (lane == 0) bulk_wait_all();
+    // the staging areas have been read; the stores themselves end with the kernel
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncwarp();
   }
 

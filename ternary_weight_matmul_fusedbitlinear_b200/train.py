@@ -169,11 +169,17 @@ def _layers(lins: Union[TLinear, Sequence[TLinear]], index: int) -> list:
 
 
 def _on_device(lins: Sequence[TLinear], index: int) -> None:
+    """Layers (checked when they were made) on device `index`, with float32 gains and biases."""
     for lin in lins:
-        _check(index, lin.packed, lin.gamma, lin.gain, lin.bias, lin.codes)
+        ok = lin.packed.get_device() == index and lin.gamma.get_device() == index and \
+            (lin.codes is None or lin.codes.get_device() == index)
         for t in (lin.gain, lin.bias):
-            if t is not None and t.dtype != torch.float32:
-                raise ValueError("gains and biases are float32")
+            if t is not None:
+                ok = ok and t.get_device() == index
+                if t.dtype != torch.float32:
+                    raise ValueError("gains and biases are float32")
+        if not ok:
+            raise ValueError("all tensors must be on one CUDA device")
 
 
 def _c_layers(lins: Sequence[TLinear]):
