@@ -524,11 +524,32 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
           const float sc2 = *p.g.gamma[0] * inv_s * kLog2e;
           const int lab = row_ok ? p.t.labels[m] - p.t.col0 : -1;
           float mx = -INFINITY, sum = 0.0f;
+          const bool plain = p.g.bias[0] == nullptr && p.g.K <= kMaxMagicK;
           for (int c = 0; c < HALF / 32; ++c) {
             const int n0 = c0 + 32 * c;
             if (n0 >= p.g.N) break;
             uint32_t r[32];
             tmem_ld32(tbase + group * HALF + 32 * c, r);
+            if (plain && n0 + 32 <= p.g.N) {   // no bias: the maximum of the accumulators is the logits' (sc2 >= 0)
+              float f[32], fm;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) f[j] = acc_magic(r[j], 0x4B400000 - qs);
+              fm = f[0];
+#pragma unroll
+              for (int j = 1; j < 32; ++j) fm = fmaxf(fm, f[j]);
+              if (lab >= n0 && lab < n0 + 32) {
+                float fl = f[0];
+#pragma unroll
+                for (int j = 1; j < 32; ++j) fl = (lab == n0 + j) ? f[j] : fl;
+                p.t.zlabel[m] = fl * sc2;
+              }
+              const float nm = fmaxf(mx, fm * sc2);
+              sum *= exp2_fast(mx - nm);       // mx = -inf at first: 0
+              mx = nm;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sum += exp2_fast(fmaf(f[j], sc2, -nm));
+              continue;
+            }
             float z[32];
             logits32(r, qs, sc2, p.g.K <= kMaxMagicK, p.g.bias[0], n0, p.g.N, z);
             float cm = z[0];
@@ -555,9 +576,10 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
         // and dW multiplies by the codes themselves).
         const int c0 = nt * BN + group * HALF;
         if (c0 < p.t.plane_cols) {
-          const float sc2 = *p.g.gamma[0] * inv_s * kLog2e;
+          // a token without weight: logits 0 against lse = +inf, so exp2 gives 0
+          // whatever its row holds
+          float sc2 = 0.0f, wt = 0.0f, lse2 = INFINITY;
           int lab = -1;
-          float wt = 0.0f, lse2 = 0.0f;
           if (row_ok) {
             const int l = p.t.labels[m];
             if (l != p.t.ignore_index && l >= 0 && l < p.t.vocab) {
@@ -566,19 +588,33 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
               if (p.t.count != nullptr) wt /= *p.t.count;
               wt *= inv_s;
               lse2 = p.t.lse[m] * kLog2e;
+              sc2 = *p.g.gamma[0] * inv_s * kLog2e;
             }
           }
+          const bool plain = p.g.bias[0] == nullptr && p.g.K <= kMaxMagicK;
           for (int c = 0; c < HALF / 32; ++c) {
             const int n0 = c0 + 32 * c;
             if (n0 >= p.t.plane_cols) break;
             uint32_t r[32];
             tmem_ld32(tbase + group * HALF + 32 * c, r);
             float z[32];
-            logits32(r, qs, sc2, p.g.K <= kMaxMagicK, p.g.bias[0], n0, p.g.N, z);
+            if (plain && n0 + 32 <= p.g.N) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float g = exp2_fast(z[j] - lse2) - (lab == n0 + j ? 1.0f : 0.0f);
-              z[j] = wt == 0.0f || n0 + j >= p.g.N ? 0.0f : g * wt;
+              for (int j = 0; j < 32; ++j) z[j] = exp2_fast(fmaf(acc_magic(r[j], 0x4B400000 - qs), sc2, -lse2)) * wt;
+            } else {
+              logits32(r, qs, sc2, p.g.K <= kMaxMagicK, p.g.bias[0], n0, p.g.N, z);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) z[j] = exp2_fast(z[j] - lse2) * wt;   // past N: exp2(-inf) = 0
+            }
+            if (lab >= n0 && lab < n0 + 32) {   // softmax - onehot, once per token: p - 1 before the weight
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (lab == n0 + j) {
+                  const float f = (float)((int)r[j] - qs);
+                  float zl = f * sc2;
+                  if (p.g.bias[0] != nullptr) zl = fmaf(__ldg(p.g.bias[0] + n0 + j), kLog2e, zl);
+                  z[j] = (exp2_fast(zl - lse2) - 1.0f) * wt;
+                }
             }
 #pragma unroll
             for (int pl = 0; pl < kPlanes; ++pl) {

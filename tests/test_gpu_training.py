@@ -344,6 +344,25 @@ def test_masked_vocabulary_entries_and_ignored_batches(dtype):
     mmf.check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_whatever_ignored_rows_hold(dtype, bias):
+    """Padded tokens may hold anything: the others' losses and gradients are those without them, bit for bit."""
+    g, (head,), x = make(12, 60, 64, 300, dtype, bias=bias, std=0.2)
+    labels = torch.randint(0, 300, (60,), generator=g, device="cuda", dtype=torch.int32)
+    labels[::3] = -100
+    junk = x.clone()
+    junk[0::9], junk[3::9], junk[6::9] = float("nan"), float("inf"), 0.0
+    (l0, k0), (l1, k1) = (mmf.head_loss(head.lin, v, labels) for v in (x, junk))
+    assert torch.isfinite(l0) and torch.equal(l0, l1)
+    g0, g1 = (mmf.head_loss_backward(head.lin, k, labels) for k in (k0, k1))
+    on = labels >= 0
+    assert torch.equal(g0.dx[on], g1.dx[on]) and torch.equal(g0.dw[0], g1.dw[0])
+    if bias:
+        assert torch.equal(g0.dbias[0], g1.dbias[0])
+    mmf.check()
+
+
 def test_labels_outside_the_vocabulary_are_left_out_and_reported():
     g, (head,), x = make(6, 9, 64, 100, "bf16", std=0.2)
     labels = torch.randint(0, 100, (9,), generator=g, device="cuda", dtype=torch.int32)
