@@ -482,13 +482,19 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
           tmem_ld32(tbase + HALF + 32 * c, rv);
           const int n0 = nt * HALF + 32 * c;
           float out[32];
+          if (p.g.bias[0] == nullptr && p.g.bias[1] == nullptr) {   // no test per element
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float uu = (float)((int)ru[j] - qs) * sc_u;
-            float vv = (float)((int)rv[j] - qs) * sc_v;
-            if (p.g.bias[0] != nullptr && n0 + j < p.g.N) uu += p.g.bias[0][n0 + j];
-            if (p.g.bias[1] != nullptr && n0 + j < p.g.N) vv += p.g.bias[1][n0 + j];
-            out[j] = silu_fast(uu) * vv;
+            for (int j = 0; j < 32; ++j)
+              out[j] = silu_fast((float)((int)ru[j] - qs) * sc_u) * ((float)((int)rv[j] - qs) * sc_v);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              float uu = (float)((int)ru[j] - qs) * sc_u;
+              float vv = (float)((int)rv[j] - qs) * sc_v;
+              if (p.g.bias[0] != nullptr && n0 + j < p.g.N) uu += p.g.bias[0][n0 + j];
+              if (p.g.bias[1] != nullptr && n0 + j < p.g.N) vv += p.g.bias[1][n0 + j];
+              out[j] = silu_fast(uu) * vv;
+            }
           }
           uint8_t* buf;
           claim(buf);
@@ -726,11 +732,11 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
             tmem_ld32(tbase + h * HALF + 32 * c, r);
             float out[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              float v = (float)((int)r[j] - qs) * sc;
-              if (bias != nullptr && n0 + j < p.g.N) v += bias[n0 + j];
-              out[j] = v;
-            }
+            for (int j = 0; j < 32; ++j) out[j] = (float)((int)r[j] - qs) * sc;
+            if (bias != nullptr)
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (n0 + j < p.g.N) out[j] += bias[n0 + j];
             const bool ok = mbar_wait(&sm.res_full[ew][c], nres & 1, abort_flag, p.status, p.wait_cycles);
             if (!__all_sync(0xffffffffu, ok)) { alive = false; break; }
             res_pending &= ~(1u << c);
@@ -759,11 +765,11 @@ __global__ void __launch_bounds__(threads_of(EPI), 1)
             } else {
               float out[32];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                float v = (float)((int)r[j] - qs) * sc;
-                if (bias != nullptr && n0 + j < p.g.N) v += bias[n0 + j];
-                out[j] = v;
-              }
+              for (int j = 0; j < 32; ++j) out[j] = (float)((int)r[j] - qs) * sc;
+              if (bias != nullptr)
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (n0 + j < p.g.N) out[j] += bias[n0 + j];
               if (has_res) {
                 const bool ok = mbar_wait(&sm.res_full[ew][0], nres & 1, abort_flag, p.status, p.wait_cycles);
                 ++nres;
