@@ -562,3 +562,49 @@ def test_refusals():
     with pytest.raises(mmf.MMFError, match="eps"):
         mmf.bitlinear_train(lin, x, eps=0.0)
     mmf.check()
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams share nothing but the layers."""
+    g, ls, x = make(41, 3000, 512, 768, "bf16", gain=True, bias=True)
+    lin = ls[0].lin
+    _, kept = mmf.bitlinear_train(lin, x)
+    dys = [torch.randn(3000, 768, generator=g, device="cuda").bfloat16() for _ in range(2)]
+    want = [mmf.bitlinear_backward(lin, kept, dy) for dy in dys]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(mmf.bitlinear_backward(lin, kept, dys[i]))
+    torch.cuda.synchronize()
+    for w, many in zip(want, got):
+        for a in many:
+            assert torch.equal(a.dx, w.dx) and torch.equal(a.dw[0], w.dw[0])
+            assert torch.equal(a.dgain, w.dgain) and torch.equal(a.dbias[0], w.dbias[0])
+    mmf.check()
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements: the last rows, and the sums over all of them, are right."""
+    m, k, n = 1_050_001, 2064, 24
+    g = torch.Generator(device="cuda")
+    g.manual_seed(51)
+    layer = Layer(g, n, k)
+    x = torch.empty(m, k, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    dy = torch.empty(m, n, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    y, kept = mmf.bitlinear_train(layer.lin, x)
+    del x
+    got = mmf.bitlinear_backward(layer.lin, kept, dy)
+    dw = torch.zeros(n, k, dtype=torch.float64, device="cuda")
+    for r in range(0, m, 150_000):
+        part = slice(r, min(m, r + 150_000))
+        dw += dy[part].double().t() @ (kept.q[part].double() / kept.scale[part].double()[:, None])
+    near(got.dw[0], dw, "bf16", "dw")
+    tail = slice(m - 300, m)
+    cut = mmf.Act8(*[t[tail].contiguous() for t in (kept.q, kept.scale, kept.qsum, kept.rinv)])
+    dx, _, _, _ = back64([layer], cut, [dy[tail].double()])
+    near(got.dx[tail], dx, "bf16", "dx")
+    near(y[tail], through(layer, cut), "bf16", "y")
+    mmf.check()
