@@ -11,82 +11,129 @@ namespace {
 constexpr int kThreads = 256;
 
 // ---------------------------------------------------------------- operands
-// A bf16 pair of ternary codes: stored field 0, 1, 2 -> -1, 0, 1.
-__device__ __forceinline__ uint32_t code_bf16(uint32_t c) { return c == 0u ? 0xBF80u : (c == 1u ? 0u : 0x3F80u); }
+// Codes of 8 consecutive weights, from one half of a packed word (column
+// 4i + b at bits 8b + 2i): 4 bytes of stored fields each, 0, 1, 2 for -1, 0, 1.
+__device__ __forceinline__ uint2 fields8(uint32_t word, uint32_t half) {
+  word >>= 4 * half;
+  return make_uint2(word & 0x03030303u, (word >> 2) & 0x03030303u);
+}
+// Four stored fields -> bf16: each selects its low and its high byte from two
+// tables of three bytes (BF80, 0000, 3F80).
+__device__ __forceinline__ uint2 fields_bf16(uint32_t f) {
+  const uint32_t sel = f | (f << 4) | 0x04040404u;
+  return make_uint2(__byte_perm(0x003F00BFu, 0x00800080u, sel), __byte_perm(0x003F00BFu, 0x00800080u, sel >> 16));
+}
+// Four int8 codes -> fp32: q + 128 in the low bits of 2^23, which one subtraction takes off again (exact).
+__device__ __forceinline__ void codes_f32(uint32_t w, float* f) {
+  w ^= 0x80808080u;
+  f[0] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540)) - 8388736.0f;
+  f[1] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7541)) - 8388736.0f;
+  f[2] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7542)) - 8388736.0f;
+  f[3] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7543)) - 8388736.0f;
+}
 
+// Work in pieces of 8 columns (one 16-byte store of bf16), a warp taking 64
+// pieces of codes at a time, two per lane and 32 apart, or 32 of a gradient:
+// every load and store of a warp is one contiguous run. All blocks are resident
+// at once. 2.7B GLU's operands, 270 MB: 58 us (16 columns per lane in two
+// stores with rows from 64-bit divisions: 68; 8 blocks of which 6 fit: 65).
+constexpr int kCodePieces = 64, kGradPieces = 32, kPrepBlocks = 6;
 struct PrepUnits {
   PrepArgs a;
-  size_t w_units, q_units, g_units;   // 16 weights; 16 codes; 8 gradient columns
-  int g_row_units;
+  size_t w_pieces, q_pieces, g_pieces;
+  int g_row_pieces;
+  __host__ __device__ size_t w_warps() const { return (w_pieces + kCodePieces - 1) / kCodePieces; }
+  __host__ __device__ size_t q_warps() const { return (q_pieces + kCodePieces - 1) / kCodePieces; }
+  __host__ __device__ size_t warps() const { return w_warps() + q_warps() + (g_pieces + kGradPieces - 1) / kGradPieces; }
 };
 struct PrepList {
   PrepUnits u[2];
 };
 
+template <typename I>
+__device__ __forceinline__ void prep_weights(const PrepArgs& a, I p, I end) {
+  const I ppr = (I)(a.K / 8);
+#pragma unroll
+  for (int h = 0; h < 2; ++h, p += 32) {
+    if (p >= end) break;
+    const int row = (int)(p / ppr), seg = (row >= a.w_pitch) + (row >= 2 * a.w_pitch), n = row - seg * a.w_pitch;
+    const size_t at = (size_t)n * ppr + (p - (I)row * ppr);                 // piece within the segment
+    const uint32_t word = n < a.N ? __ldg(a.w[seg] + at / 2) : 0x55555555u;   // all zero weights
+    const uint2 f = fields8(word, (uint32_t)(at & 1));
+    if (a.wb != nullptr) {
+      const uint2 lo = fields_bf16(f.x), hi = fields_bf16(f.y);
+      static_cast<uint4*>(a.wb)[p] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+    if (a.wu[seg] != nullptr && n < a.N) reinterpret_cast<uint2*>(a.wu[seg])[at] = f;
+  }
+}
+
+template <typename I>
+__device__ __forceinline__ void prep_codes(const PrepArgs& a, I p, I end) {
+  uint2 v[2] = {};
+  float sc[2] = {1.0f, 1.0f};
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (p + 32 * h < end) {
+      v[h] = reinterpret_cast<const uint2*>(a.q)[p + 32 * h];
+      if (a.q_scaled) sc[h] = 1.0f / __ldg(a.scale + (p + 32 * h) / (I)(a.qK / 8));
+    }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (p + 32 * h < end) {
+      float f[8];
+      codes_f32(v[h].x, f);
+      codes_f32(v[h].y, f + 4);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) f[c] *= sc[h];
+      store8(static_cast<bf16*>(a.qb) + (size_t)(p + 32 * h) * 8, f);
+    }
+}
+
+template <typename T, typename I>
+__device__ __forceinline__ void prep_gradient(const PrepArgs& a, I row_pieces, I p, I end) {
+  if (p >= end) return;
+  const int row = (int)(p / row_pieces), c0 = (int)(p - (I)row * row_pieces) * 8;
+  const int seg = c0 / a.g_pitch, n0 = c0 - seg * a.g_pitch;
+  const T* src = static_cast<const T*>(a.dy) + ((size_t)row * a.g_seg + seg) * a.g_N;
+  const float sc = a.g_scaled && row < a.M ? 1.0f / __ldg(a.scale + row) : 1.0f;
+  float v[8];
+  if (row < a.M && a.g_N % 8 == 0 && n0 < a.g_N) {
+    load8(src + n0, v);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] *= sc;
+  } else {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = row < a.M && n0 + c < a.g_N ? to_f32(src[n0 + c]) * sc : 0.0f;
+  }
+  const size_t ld = (size_t)a.g_seg * a.g_pitch;
+  for (int q = 0; q < a.g_planes; ++q) {
+    float o[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      o[c] = round_to<bf16>(v[c]);
+      v[c] -= o[c];
+    }
+    store8(static_cast<bf16*>(a.gb) + ((size_t)q * a.g_rows + row) * ld + c0, o);
+  }
+}
+
 // One launch for the operands of a backward: packed codes -> bf16 (and bytes),
-// int8 codes -> bf16, the gradient -> padded bf16 planes. Each unit is one
-// 16- or 32-byte store.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) train_prep_kernel(const __grid_constant__ PrepList list) {
+// int8 codes -> bf16, the gradient -> padded bf16 planes. I: the type of piece
+// indices, 32 bits wherever they fit (the rows come from divisions).
+template <typename T, typename I>
+__global__ void __launch_bounds__(kThreads, kPrepBlocks) train_prep_kernel(const __grid_constant__ PrepList list) {
   pdl_trigger();
   pdl_wait();
-  const size_t total0 = list.u[0].w_units + list.u[0].q_units + list.u[0].g_units;
-  const size_t total = total0 + list.u[1].w_units + list.u[1].q_units + list.u[1].g_units;
-  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (size_t)gridDim.x * kThreads) {
+  const I total0 = (I)list.u[0].warps(), total = total0 + (I)list.u[1].warps();
+  const I lane = threadIdx.x % 32;
+  for (I i = (I)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; i < total; i += (I)gridDim.x * (kThreads / 32)) {
     const PrepUnits& u = list.u[i >= total0];
-    const PrepArgs& a = u.a;
-    const size_t id = i >= total0 ? i - total0 : i;
-    if (id < u.w_units) {
-      const int wpr = a.K / 16;
-      const int row = (int)(id / wpr), j = (int)(id % wpr);
-      const int seg = row / a.w_pitch, n = row - seg * a.w_pitch;
-      const uint32_t word = n < a.N ? __ldg(a.w[seg] + (size_t)n * wpr + j) : 0x55555555u;   // all zero weights
-      if (a.wb != nullptr) {
-        uint32_t o[8];
-#pragma unroll
-        for (int c = 0; c < 16; c += 2) {   // column 4i + b at bits 8b + 2i
-          const int s0 = 8 * (c & 3) + 2 * (c >> 2), s1 = 8 * ((c + 1) & 3) + 2 * ((c + 1) >> 2);
-          o[c / 2] = code_bf16((word >> s0) & 3u) | (code_bf16((word >> s1) & 3u) << 16);
-        }
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.wb) + id * 32);
-        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-      }
-      if (a.wu[seg] != nullptr && n < a.N)
-        *reinterpret_cast<uint4*>(a.wu[seg] + ((size_t)n * wpr + j) * 16) =
-            make_uint4(word & 0x03030303u, (word >> 2) & 0x03030303u, (word >> 4) & 0x03030303u,
-                       (word >> 6) & 0x03030303u);
-    } else if (id < u.w_units + u.q_units) {
-      const size_t k = id - u.w_units;
-      const int4 v = *reinterpret_cast<const int4*>(a.q + k * 16);
-      const float sc = a.q_scaled ? 1.0f / __ldg(a.scale + k / (a.qK / 16)) : 1.0f;
-      const int* w = &v.x;
-      float f[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) f[c] = (float)((w[c >> 2] << (24 - 8 * (c & 3))) >> 24) * sc;
-      bf16* dst = static_cast<bf16*>(a.qb) + k * 16;
-      store8(dst, *reinterpret_cast<float(*)[8]>(&f[0]));
-      store8(dst + 8, *reinterpret_cast<float(*)[8]>(&f[8]));
-    } else {
-      const size_t k = id - u.w_units - u.q_units;
-      const int row = (int)(k / u.g_row_units), c0 = (int)(k % u.g_row_units) * 8;
-      const int seg = c0 / a.g_pitch, n0 = c0 - seg * a.g_pitch;
-      const T* src = static_cast<const T*>(a.dy) + ((size_t)row * a.g_seg + seg) * a.g_N;
-      const float sc = a.g_scaled && row < a.M ? 1.0f / __ldg(a.scale + row) : 1.0f;
-      float v[8];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] = row < a.M && n0 + c < a.g_N ? to_f32(src[n0 + c]) * sc : 0.0f;
-      const size_t ld = (size_t)a.g_seg * a.g_pitch;
-      for (int p = 0; p < a.g_planes; ++p) {
-        float o[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          o[c] = round_to<bf16>(v[c]);
-          v[c] -= o[c];
-        }
-        store8(static_cast<bf16*>(a.gb) + ((size_t)p * a.g_rows + row) * ld + c0, o);
-      }
-    }
+    const I id = i >= total0 ? i - total0 : i;
+    const I w = (I)u.w_warps(), q = w + (I)u.q_warps();
+    if (id < w) prep_weights<I>(u.a, id * kCodePieces + lane, (I)u.w_pieces);
+    else if (id < q) prep_codes<I>(u.a, (id - w) * kCodePieces + lane, (I)u.q_pieces);
+    else prep_gradient<T, I>(u.a, (I)u.g_row_pieces, (id - q) * kGradPieces + lane, (I)u.g_pieces);
   }
 }
 
@@ -309,16 +356,26 @@ __global__ void __launch_bounds__(kThreads) norm_back_kernel(const NormBackArgs 
 }
 
 // c = mean(dx^ x^) of each row from the partial sums of dx^ q that the product's
-// epilogue left, one per 128 columns.
+// epilogue left, one per 128 columns. 32 rows per block and 8 threads per row,
+// so that a row's partial sums are in flight together (4096 rows of 54: one
+// thread per row 15.8 us, this 9.7).
+constexpr int kDotRows = 32, kDotGroups = kThreads / kDotRows;
 __global__ void __launch_bounds__(kThreads) dot_join_kernel(const float* __restrict__ part, int slots, int M, int K,
                                                             const float* __restrict__ scale, float* __restrict__ cmean) {
+  __shared__ float red[kDotGroups][kDotRows];
   pdl_trigger();
   pdl_wait();
-  const int m = blockIdx.x * kThreads + threadIdx.x;
-  if (m >= M) return;
+  const int r = threadIdx.x % kDotRows, g = threadIdx.x / kDotRows, m = blockIdx.x * kDotRows + r;
   float s = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < slots; ++i) s += part[(size_t)i * M + m];
+  if (m < M) {
+#pragma unroll 8
+    for (int i = g; i < slots; i += kDotGroups) s += part[(size_t)i * M + m];
+  }
+  red[g][r] = s;
+  __syncthreads();
+  if (g != 0 || m >= M) return;
+#pragma unroll
+  for (int i = 1; i < kDotGroups; ++i) s += red[i][r];
   cmean[m] = s / scale[m] / (float)K;
 }
 
@@ -529,7 +586,7 @@ __global__ void __launch_bounds__(kThreads) dw_join_kernel(const DwJoinArgs a) {
 
 // ---------------------------------------------------------------- the loss
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kJoinRows = 32, kJoinGroups = 8;
+constexpr int kJoinRows = 32, kJoinGroups = 8, kJoinBatch = 8;
 
 __device__ __forceinline__ bool counted_label(const LossArgs& a, int l) {
   return l != a.ignore_index && l >= 0 && l < a.vocab;
@@ -542,21 +599,34 @@ __device__ __forceinline__ bool counted_label(const LossArgs& a, int l) {
 template <int ROWS>
 __device__ __forceinline__ float loss_rows(const LossArgs& a, int m, int r, int g, float2 (*red)[ROWS], int* status) {
   float mx = -INFINITY, sum = 0.0f;
-  auto fold = [&](float2 o) {
-    const float nm = fmaxf(mx, o.x);
-    if (nm != -INFINITY) sum = sum * exp2f(mx - nm) + o.y * exp2f(o.x - nm);
-    else sum += o.y;   // keeps a NaN
-    mx = nm;
-  };
   if (m < a.M) {
-#pragma unroll 4
-    for (int s = g; s < a.slots; s += kJoinGroups) fold(a.part[(size_t)s * a.M + m]);
+    for (int s0 = g; s0 < a.slots; s0 += kJoinGroups * kJoinBatch) {
+      float2 o[kJoinBatch];
+      float nm = mx;
+#pragma unroll
+      for (int i = 0; i < kJoinBatch; ++i) {
+        const int s = s0 + i * kJoinGroups;
+        o[i] = s < a.slots ? a.part[(size_t)s * a.M + m] : make_float2(-INFINITY, 0.0f);
+      }
+#pragma unroll
+      for (int i = 0; i < kJoinBatch; ++i) nm = fmaxf(nm, o[i].x);
+      const float base = nm != -INFINITY ? nm : 0.0f;   // nothing but -inf so far: the terms are 0, or NaN and stay so
+      sum *= exp2f(mx - base);
+#pragma unroll
+      for (int i = 0; i < kJoinBatch; ++i) sum += o[i].y * exp2f(o[i].x - base);
+      mx = nm;
+    }
   }
   red[g][r] = make_float2(mx, sum);
   __syncthreads();
   float loss = 0.0f;
   if (g == 0 && m < a.M) {
-    for (int i = 1; i < kJoinGroups; ++i) fold(red[i][r]);
+    for (int i = 1; i < kJoinGroups; ++i) {
+      const float2 o = red[i][r];
+      const float nm = fmaxf(mx, o.x), base = nm != -INFINITY ? nm : 0.0f;
+      sum = sum * exp2f(mx - base) + o.y * exp2f(o.x - base);
+      mx = nm;
+    }
     const float ls = log2f(sum);
     const int l = a.labels[m];
     if (counted_label(a, l)) loss = ((mx - a.zlabel[m]) + ls) * kLn2;
@@ -656,22 +726,25 @@ int blocks_for(size_t units, int per_sm) {
 
 cudaError_t launch_train_prep(const PrepArgs* const* sets, int n, cudaStream_t stream) {
   PrepList list = {};
-  size_t total = 0;
+  size_t total = 0, most = 0;
   mmf_dtype dt = MMF_BF16;
   for (int i = 0; i < n; ++i) {
     PrepUnits& u = list.u[i];
     const PrepArgs& a = u.a = *sets[i];
-    u.w_units = a.nseg > 0 ? (size_t)a.nseg * a.w_pitch * (a.K / 16) : 0;
-    u.q_units = a.qb != nullptr ? (size_t)a.M * (a.qK / 16) : 0;
-    u.g_row_units = a.gb != nullptr ? a.g_seg * a.g_pitch / 8 : 0;
-    u.g_units = (size_t)u.g_row_units * a.g_rows;
-    total += u.w_units + u.q_units + u.g_units;
+    u.w_pieces = a.nseg > 0 ? (size_t)a.nseg * a.w_pitch * (a.K / 8) : 0;
+    u.q_pieces = a.qb != nullptr ? (size_t)a.M * (a.qK / 8) : 0;
+    u.g_row_pieces = a.gb != nullptr ? a.g_seg * a.g_pitch / 8 : 0;
+    u.g_pieces = (size_t)u.g_row_pieces * a.g_rows;
+    total += u.warps();
+    most = std::max({most, u.w_pieces, u.q_pieces, u.g_pieces});
     if (a.gb != nullptr) dt = a.dy_dt;
   }
   if (total == 0) return cudaSuccess;
-  const dim3 grid(blocks_for(total, 8));
-  return dt == MMF_BF16 ? launch_pdl(train_prep_kernel<bf16>, grid, dim3(kThreads), 0, stream, list)
-                        : launch_pdl(train_prep_kernel<float>, grid, dim3(kThreads), 0, stream, list);
+  const dim3 grid(blocks_for(total * 32, kPrepBlocks)), block(kThreads);
+  const bool wide = most >= (size_t(1) << 31);
+  if (dt == MMF_BF16)
+    return launch_pdl(wide ? train_prep_kernel<bf16, size_t> : train_prep_kernel<bf16, uint32_t>, grid, block, 0, stream, list);
+  return launch_pdl(wide ? train_prep_kernel<float, size_t> : train_prep_kernel<float, uint32_t>, grid, block, 0, stream, list);
 }
 
 template <typename T, int WPR, int NV, bool STAT, int N>
@@ -713,7 +786,7 @@ cudaError_t launch_norm_back(const NormBackArgs& a, bool stat, mmf_dtype dt, cud
 
 cudaError_t launch_dot_join(const float* part, int slots, int M, int K, const float* scale, float* cmean,
                             cudaStream_t stream) {
-  return launch_pdl(dot_join_kernel, dim3(ceil_div(M, kThreads)), dim3(kThreads), 0, stream, part, slots, M, K, scale,
+  return launch_pdl(dot_join_kernel, dim3(ceil_div(M, kDotRows)), dim3(kThreads), 0, stream, part, slots, M, K, scale,
                     cmean);
 }
 
