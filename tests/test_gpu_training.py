@@ -608,3 +608,58 @@ def test_offsets_beyond_32_bits():
     near(got.dx[tail], dx, "bf16", "dx")
     near(y[tail], through(layer, cut), "bf16", "y")
     mmf.check()
+
+
+def a_workspace(nbytes):
+    """`nbytes` on a 16-byte boundary that is not a 32-byte one, every byte 0xFF (NaN in each float type), between
+    bytes that stay 0xA5, and a check that those did."""
+    whole = torch.full((nbytes + 4096 + 16,), 0xA5, dtype=torch.uint8, device="cuda")
+    ws = whole[2048 + 16:2048 + 16 + nbytes]
+    ws.fill_(0xFF)
+
+    def check():
+        assert (whole[:2048 + 16] == 0xA5).all() and (whole[2048 + 16 + nbytes:] == 0xA5).all()
+    return ws, check
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,k,n", [(1, 16, 3), (130, 272, 401), (1503, 336, 528), (5000, 512, 1027)])
+def test_a_callers_workspace(m, k, n, dtype):
+    """What a workspace of exactly the size asked for held before changes nothing, and nothing beside it is written."""
+    from ternary_weight_matmul_fusedbitlinear_b200 import _lib
+    lib, code = _lib.load(), _lib.MMF_BF16 if dtype == "bf16" else _lib.MMF_F32
+    g, ls, x = make(61, m, k, n, dtype, gain=True, bias=True, layers=2)
+    lins = [l.lin for l in ls]
+    dy = torch.randn(m, 2, n, generator=g, device="cuda").to(DT[dtype])
+    inner = (n + 15) // 16 * 16
+    gate, up = (Layer(g, inner, k, ls[0].gain, True).lin for _ in range(2))
+    down = Layer(g, k, inner).lin
+    dz = torch.randn(m, k, generator=g, device="cuda").to(DT[dtype])
+    labels = torch.randint(0, n, (m,), generator=g, device="cuda", dtype=torch.int32)
+    labels[::9] = -100
+
+    def chain(ws):
+        y, k1 = mmf.bitlinear_train(lins, x, ws=ws("mmf_bitlinear_train", 2, n, k, m))
+        g1 = mmf.bitlinear_backward(lins, k1, dy, ws=ws("mmf_bitlinear_backward", 2, n, k, m, code))
+        z, k2 = mmf.glu_train(gate, up, down, x, ws=ws("mmf_glu_train", m, k, inner, code))
+        g2 = mmf.glu_backward(gate, up, down, k2, dz, ws=ws("mmf_glu_backward", m, k, inner, code))
+        loss, k3 = mmf.head_loss(lins[0], x, labels, ws=ws("mmf_head_loss", m, n, k))
+        g3 = mmf.head_loss_backward(lins[0], k3, labels, ws=ws("mmf_head_loss_backward", m, n, k, code))
+        return [y, g1.dx, *g1.dw, g1.dgain, *g1.dbias, z, g2.dx, *g2.dw, g2.dgain[0], *g2.dbias[:2], loss, k3.lse,
+                g3.dx, g3.dw[0], g3.dgain, g3.dbias[0]]
+
+    checks = []
+
+    def own(name, *sizes):
+        need = getattr(lib, name + "_ws_size")(*sizes)
+        ws, check = a_workspace(max(need, 16))
+        checks.append(check)
+        return ws
+
+    want, got = chain(lambda *a: None), chain(own)
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(a, b), i
+        assert torch.isfinite(a.float()).all(), i
+    for check in checks:
+        check()
+    mmf.check()
