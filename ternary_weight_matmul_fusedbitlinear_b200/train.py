@@ -15,7 +15,7 @@ of the input's device.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 from typing import NamedTuple, Optional, Sequence, Union
 
 import torch
@@ -24,8 +24,11 @@ from . import _lib as L
 from .api import _DT, DEFAULT_EPS, TLinear
 
 _REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
-_P3 = L.c_vp * 3
-_byref = ctypes.byref
+# The header's structs as bytes (a tenth of the time that ctypes' own take to fill).
+_pack_layer = struct.Struct("@4P2iP").pack     # mmf_tlinear
+_pack_act8 = struct.Struct("@4P").pack         # mmf_act8
+_pack_linear = struct.Struct("@8P").pack       # mmf_linear_grads
+_pack_glu = struct.Struct("@9P").pack          # mmf_glu_grads
 
 
 class Act8:
@@ -67,16 +70,16 @@ class Act8:
     qsum = property(lambda self: self._tensors()[2])
     rinv = property(lambda self: self._tensors()[3])
 
-    def _c(self, m: int, k: int, device: int) -> L.Act8:
+    def _c(self, m: int, k: int, device: int) -> bytes:
         if self._m != m or self._k != k:
             raise ValueError(f"kept activations are of {self._m} rows of {self._k}, not {m} of {k}")
         if self._buf is not None:
             if self._buf.get_device() != device:
                 raise ValueError("all tensors must be on one device")
             p, at, step = self._buf.data_ptr(), _pad16(m * k), _pad16(4 * m)
-            return L.Act8(p, p + at, p + at + step, p + at + 2 * step)
+            return _pack_act8(p, p + at, p + at + step, p + at + 2 * step)
         _check(device, *self._parts)
-        return L.Act8(*[t.data_ptr() for t in self._parts])
+        return _pack_act8(*[t.data_ptr() for t in self._parts])
 
 
 class HeadKept:
@@ -137,8 +140,8 @@ def _call(index: int, name: str, *args) -> None:
         L.check(status, name)
 
 
-def _p(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+def _p(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _check(index: int, *ts: Optional[torch.Tensor]) -> None:
@@ -182,8 +185,9 @@ def _on_device(lins: Sequence[TLinear], index: int) -> None:
             raise ValueError("all tensors must be on one CUDA device")
 
 
-def _c_layers(lins: Sequence[TLinear]):
-    return (L.TLinear * len(lins))(*[lin.c() for lin in lins])
+def _c_layer(lin: TLinear) -> bytes:
+    return _pack_layer(lin.packed.data_ptr(), lin.gamma.data_ptr(), _p(lin.gain), _p(lin.bias), lin.N, lin.K,
+                       _p(lin.codes))
 
 
 def _rows(x: torch.Tensor, width: int, what: str) -> int:
@@ -224,12 +228,12 @@ def bitlinear_train(lins: Union[TLinear, Sequence[TLinear]], x: torch.Tensor, ep
     n, N, K = len(ls), ls[0].N, ls[0].K
     m = _rows(x, K, "x")
     code = _code(dt)
-    y = x.new_empty(x.shape[:-1] + ((N,) if isinstance(lins, TLinear) else (n, N)))
+    y = x.new_empty(*x.shape[:-1], N) if isinstance(lins, TLinear) else x.new_empty(*x.shape[:-1], n, N)
     kept = Act8._new(m, K, x)
     lib = L.load()
     wp, wn, _keep = _scratch(lib.mmf_bitlinear_train_ws_size(n, N, K, m), x, ws)
-    _call(idx, "mmf_bitlinear_train", _c_layers(ls), n, x.data_ptr(), code, m, y.data_ptr(), eps,
-          _byref(kept._c(m, K, idx)), wp, wn)
+    _call(idx, "mmf_bitlinear_train", b"".join(map(_c_layer, ls)), n, x.data_ptr(), code, m, y.data_ptr(), eps,
+          kept._c(m, K, idx), wp, wn)
     return y, kept
 
 
@@ -254,15 +258,16 @@ def bitlinear_backward(lins: Union[TLinear, Sequence[TLinear]], kept: Act8, dy: 
     _like(x, m * K, dt, "x")
     _like(dres, m * K, dt, "dres")
     new = dy.new_empty
-    dx = new(dy.shape[:-1 if one else -2] + (K,))
-    dw = [new((N, K)) for _ in ls]
-    dgain = None if ls[0].gain is None else new((K,))
-    dbias = [None if lin.bias is None else new((N,)) for lin in ls]
-    cg = L.LinearGrads(dx.data_ptr(), _P3(*[t.data_ptr() for t in dw]), _p(dgain), _P3(*[_p(t) for t in dbias]))
+    dx = new(*dy.shape[:-1 if one else -2], K)
+    dw = [new(N, K) for _ in ls]
+    dgain = None if ls[0].gain is None else new(K)
+    dbias = [None if lin.bias is None else new(N) for lin in ls]
+    none = (0,) * (3 - n)
+    cg = _pack_linear(dx.data_ptr(), *map(_p, dw), *none, _p(dgain), *map(_p, dbias), *none)
     lib = L.load()
     wp, wn, _keep = _scratch(lib.mmf_bitlinear_backward_ws_size(n, N, K, m, code), dy, ws)
-    _call(idx, "mmf_bitlinear_backward", _c_layers(ls), n, _byref(kept._c(m, K, idx)), _p(x), dy.data_ptr(),
-          _p(dres), code, m, _byref(cg), wp, wn)
+    _call(idx, "mmf_bitlinear_backward", b"".join(map(_c_layer, ls)), n, kept._c(m, K, idx), _p(x), dy.data_ptr(),
+          _p(dres), code, m, cg, wp, wn)
     return LinearGrads(dx, dw, dgain, dbias)
 
 
@@ -278,12 +283,12 @@ def glu_train(gate: TLinear, up: TLinear, down: TLinear, x: torch.Tensor, residu
     m = _rows(x, d, "x")
     code = _code(dt)
     _like(residual, m * d, dt, "residual")
-    y = x.new_empty(x.shape)
+    y = x.new_empty(*x.shape)
     kx, kp = Act8._new(m, d, x), Act8._new(m, inner, x)
     lib = L.load()
     wp, wn, _keep = _scratch(lib.mmf_glu_train_ws_size(m, d, inner, code), x, ws)
-    _call(idx, "mmf_glu_train", _byref(gate.c()), _byref(up.c()), _byref(down.c()), x.data_ptr(), _p(residual),
-          y.data_ptr(), m, code, eps, _byref(kx._c(m, d, idx)), _byref(kp._c(m, inner, idx)),
+    _call(idx, "mmf_glu_train", _c_layer(gate), _c_layer(up), _c_layer(down), x.data_ptr(), _p(residual),
+          y.data_ptr(), m, code, eps, kx._c(m, d, idx), kp._c(m, inner, idx),
           wp, wn)
     return y, (kx, kp)
 
@@ -304,15 +309,15 @@ def glu_backward(gate: TLinear, up: TLinear, down: TLinear, kept, dy: torch.Tens
     _like(dres, m * d, dt, "dres")
     kx, kp = kept
     new = dy.new_empty
-    dx = new(dy.shape)
-    dw = [new((lin.N, lin.K)) for lin in ls]
-    dgain = [None if lin.gain is None else new((lin.K,)) for lin in (gate, down)]
-    dbias = [None if lin.bias is None else new((lin.N,)) for lin in ls]
-    cg = L.GluGrads(dx.data_ptr(), *[t.data_ptr() for t in dw], *[_p(t) for t in dgain], *[_p(t) for t in dbias])
+    dx = new(*dy.shape)
+    dw = [new(lin.N, lin.K) for lin in ls]
+    dgain = [None if lin.gain is None else new(lin.K) for lin in (gate, down)]
+    dbias = [None if lin.bias is None else new(lin.N) for lin in ls]
+    cg = _pack_glu(dx.data_ptr(), *map(_p, dw), *map(_p, dgain), *map(_p, dbias))
     lib = L.load()
     wp, wn, _keep = _scratch(lib.mmf_glu_backward_ws_size(m, d, inner, code), dy, ws)
-    _call(idx, "mmf_glu_backward", _byref(gate.c()), _byref(up.c()), _byref(down.c()), _byref(kx._c(m, d, idx)),
-          _byref(kp._c(m, inner, idx)), _p(x), dy.data_ptr(), _p(dres), code, m, _byref(cg),
+    _call(idx, "mmf_glu_backward", _c_layer(gate), _c_layer(up), _c_layer(down), kx._c(m, d, idx),
+          kp._c(m, inner, idx), _p(x), dy.data_ptr(), _p(dres), code, m, cg,
           wp, wn)
     return GluGrads(dx, dw, dgain, dbias)
 
@@ -345,8 +350,8 @@ def head_loss(head: TLinear, x: torch.Tensor, labels: torch.Tensor, ignore_index
     lse, count = kept._ptrs()
     lib = L.load()
     wp, wn, _keep = _scratch(lib.mmf_head_loss_ws_size(m, N, K), x, ws)
-    _call(idx, "mmf_head_loss", _byref(head.c()), x.data_ptr(), code, m, labels.data_ptr(), ignore_index, red, eps,
-          loss.data_ptr(), _byref(kept.act._c(m, K, idx)), lse, count, wp, wn)
+    _call(idx, "mmf_head_loss", _c_layer(head), x.data_ptr(), code, m, labels.data_ptr(), ignore_index, red, eps,
+          loss.data_ptr(), kept.act._c(m, K, idx), lse, count, wp, wn)
     return loss, kept
 
 
@@ -365,14 +370,14 @@ def head_loss_backward(head: TLinear, kept: HeadKept, labels: torch.Tensor, dlos
     if dloss is not None and (dloss.dtype != torch.float32 or dloss.numel() != (m if red == 0 else 1)):
         raise ValueError("dloss must be float32, one value (one per token for reduction 'none')")
     _like(x, m * K, dt, "x")
-    dx = labels.new_empty(labels.shape + (K,), dtype=dt)
-    dw = dx.new_empty((N, K))
-    dgain = None if head.gain is None else dx.new_empty((K,))
-    dbias = None if head.bias is None else dx.new_empty((N,))
-    cg = L.LinearGrads(dx.data_ptr(), _P3(dw.data_ptr()), _p(dgain), _P3(_p(dbias)))
+    dx = labels.new_empty(*labels.shape, K, dtype=dt)
+    dw = dx.new_empty(N, K)
+    dgain = None if head.gain is None else dx.new_empty(K)
+    dbias = None if head.bias is None else dx.new_empty(N)
+    cg = _pack_linear(dx.data_ptr(), dw.data_ptr(), 0, 0, _p(dgain), _p(dbias), 0, 0)
     lse, count = kept._ptrs()
     lib = L.load()
     wp, wn, _keep = _scratch(lib.mmf_head_loss_backward_ws_size(m, N, K, code), labels, ws)
-    _call(idx, "mmf_head_loss_backward", _byref(head.c()), _byref(kept.act._c(m, K, idx)), _p(x), labels.data_ptr(),
-          lse, count, _p(dloss), ignore_index, red, code, m, _byref(cg), wp, wn)
+    _call(idx, "mmf_head_loss_backward", _c_layer(head), kept.act._c(m, K, idx), _p(x), labels.data_ptr(),
+          lse, count, _p(dloss), ignore_index, red, code, m, cg, wp, wn)
     return LinearGrads(dx, [dw], dgain, [dbias])

@@ -203,3 +203,15 @@ def test_training_workspace_sizes(lib):
     # the logits' gradient is held in pieces: far below M x V values
     assert lib.mmf_head_loss_backward_ws_size(65536, 64000, 1024, 1) < 65536 * 64000
     assert lib.mmf_head_loss_ws_size(65536, 32000, 1024) < 65536 * 32000
+
+
+def test_packed_structs_are_the_headers():
+    """The bytes that the training calls pass are the ctypes structs, field by field."""
+    from ternary_weight_matmul_fusedbitlinear_b200 import train
+    layer = L.TLinear(16, 32, None, 48, 7, 64, 80)
+    assert train._pack_layer(16, 32, 0, 48, 7, 64, 80) == bytes(layer)
+    assert train._pack_layer(16, 32, 0, 48, 7, 64, 80) * 2 == bytes((L.TLinear * 2)(layer, layer))
+    assert train._pack_act8(16, 32, 48, 64) == bytes(L.Act8(16, 32, 48, 64))
+    three = L.c_vp * 3
+    assert train._pack_linear(1, 2, 3, 0, 5, 6, 7, 0) == bytes(L.LinearGrads(1, three(2, 3, None), 5, three(6, 7, None)))
+    assert train._pack_glu(*range(1, 10)) == bytes(L.GluGrads(*range(1, 10)))
