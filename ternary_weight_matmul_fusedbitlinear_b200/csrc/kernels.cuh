@@ -98,7 +98,7 @@ enum class Epi : int {
 struct TrainEpi {
   const int32_t* labels;    // kLse, kDz: [M]
   int col0, vocab;          // kLse, kDz: vocabulary index of column 0; vocabulary size
-  float2* part;             // kLse: [ceil(N / 128)][M] (max, sum) in log2 units
+  float2* part;             // kLse: [tgemm_tc_share * ceil(N / 128)][M] (max, sum) in log2 units
   float* zlabel;            // kLse: [M] the label's logit in log2 units (written where the label lies in these columns)
   const float* lse;         // kDz: [M]
   const float* dloss;       // kDz: upstream gradient, [M] or one value
@@ -164,6 +164,8 @@ bool tgemm_tc_supported(const TGemmArgs& a, Epi epi);
 bool tgemm_tc_any_supported(const TGemmArgs& a, Epi epi, mmf_dtype dt);
 cudaError_t launch_tgemm_tc(const TGemmArgs& a, Epi epi, mmf_dtype dt, int* status, cudaStream_t stream);
 // The training epilogues kLse, kDz, kGluBwd (a.wu set; out: bf16 planes, ldo columns).
+// Blocks that share one tile's kLse or kDz epilogue; kLse writes so many times ceil(N / 128) slots.
+int tgemm_tc_share(int M, int N);
 cudaError_t launch_tgemm_train(const TGemmArgs& a, const TrainEpi& t, Epi epi, int* status, cudaStream_t stream);
 
 // bf16 training products (bgemm_tc.cu), D fp32 accumulated:

@@ -737,7 +737,7 @@ extern "C" mmf_status mmf_glu_backward(const mmf_tlinear* gate, const mmf_tlinea
 
 namespace {
 
-int loss_slots(int V) { return ceil_div(V, 128); }
+int loss_slots(int M, int V) { return tgemm_tc_share(M, V) * ceil_div(V, 128); }
 
 struct LossWs {
   uint8_t* wu;
@@ -747,7 +747,7 @@ struct LossWs {
 LossWs carve_loss(Carver& c, int M, int V, int K) {
   LossWs w;
   w.wu = c.take<uint8_t>((size_t)V * K);
-  w.part = c.take<float2>((size_t)loss_slots(V) * M);
+  w.part = c.take<float2>((size_t)loss_slots(M, V) * M);
   w.zlabel = c.take<float>(M);
   w.token = c.take<float>(M);
   return w;
@@ -839,7 +839,7 @@ extern "C" mmf_status mmf_head_loss(const mmf_tlinear* head, const void* x, mmf_
            "logits");
   LossArgs l = {};
   l.part = w.part;
-  l.slots = loss_slots(V);
+  l.slots = loss_slots(M, V);
   l.M = M;
   l.vocab = V;
   l.zlabel = w.zlabel;
